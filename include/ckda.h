@@ -87,6 +87,12 @@ extern "C" {
 #define CKDA_QK_L2NORM 32      /* flag: q and k are L2-normalised inside the kernel   */
 #define CKDA_DELTA_PRODUCT2 64 /* flag: two rank-one delta updates per token          */
 
+#define CKDA_DECAY_PER_TOKEN 0 /* linear attention: g is [B, T, H] (decode: [B, H])   */
+#define CKDA_DECAY_PER_HEAD 1  /* linear attention: g is [H], the same at every token */
+
+#define CKDA_ROTARY_HALF 0         /* rotary pair i: channels i and i + n_freqs       */
+#define CKDA_ROTARY_INTERLEAVED 1  /* rotary pair i: channels 2 i and 2 i + 1         */
+
 /*
  * Chunkwise (WY / UT-transform) parallel forward, "prefill".
  *
@@ -200,6 +206,86 @@ size_t ckda_chunk_bwd_workspace_size(int B, int T, int H, int dk, int dv, int n_
 int ckda_decode_step(const void *q, const void *k, const void *v, const void *a, const float *b,
                      float *S, int B, int H, int dk, int dv, int signed_gate, int io_dtype,
                      int o_dtype, void *o, void *stream);
+
+/*
+ * Linear attention with a decay for each head (no delta rule: CyFA blog, section 2.1, with a
+ * scalar gate), chunkwise forward.  Per sequence and head
+ *
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,      o_t = S_t^T q_t
+ *
+ *   q : [B, T, Hq, dk]   k : [B, T, Hk, dk]   v : [B, T, Hv, dv]   io_dtype
+ *            Hq, Hk, Hv divide H: head h reads head h * Hx / H of a tensor with Hx heads.
+ *   g : log decays, float32, g <= 0 (-inf forgets everything before; a value above 0 or a NaN
+ *            gives undefined values in its own sequence and head, but no fault):
+ *            [B, T, H] with decay = CKDA_DECAY_PER_TOKEN, [H] with CKDA_DECAY_PER_HEAD
+ *   o : [B, T, H, dv] io_dtype (NULL: not written)
+ *   S0, S_T : [N, H, dk, dv] float32, as in ckda_chunk_fwd (S_T may alias S0; an empty
+ *            sequence's S_T is its S0)
+ *   cu_seqlens, n_seqs, B, T, stream : as in ckda_chunk_fwd.  Offsets are checked on the
+ *            device; where any is bad, the status word is CKDA_ERR_SEQLENS and nothing is written.
+ *   dk, dv in {16, 32, 64, 128}; q, k, v, o and states 16-byte aligned.
+ *   workspace : device scratch of ckda_linattn_fwd_workspace_size() bytes, 256-byte aligned,
+ *            never shared by two calls in flight at once; its status word is read with
+ *            ckda_workspace_status.
+ * fp32 inputs are computed in exact fp32.  Returns CKDA_OK or a negative CKDA_ERR_* code.
+ */
+int ckda_linattn_fwd(const void *q, const void *k, const void *v, const float *g, const float *S0,
+                     const int32_t *cu_seqlens, int n_seqs, int B, int T, int H, int Hq, int Hk,
+                     int Hv, int dk, int dv, int decay, int io_dtype, void *o, float *S_T,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace ckda_linattn_fwd needs (host arithmetic, no CUDA call). */
+size_t ckda_linattn_fwd_workspace_size(int B, int T, int H, int dk, int dv, int io_dtype, int n_seqs);
+
+/*
+ * Backward of ckda_linattn_fwd: the gradients of  L = sum dO . o + sum dS_T . S_T.
+ *   dO : [B, T, H, dv] io_dtype, NULL = zero       dS_T : [N, H, dk, dv] float32, NULL = zero
+ *   dq, dk_out, dv_out : shaped and typed as q, k, v (all required); a shared head's gradient
+ *            is the sum over the heads that read it, summed in fp32 and rounded once
+ *   dg : shaped as g, float32 (required); with CKDA_DECAY_PER_HEAD the sum over all tokens.
+ *            A decay of -inf has gradient 0.
+ *   dS0 : [N, H, dk, dv] float32, NULL = not written; may alias dS_T
+ * Sums are taken in a fixed order: the same inputs give the same bits.
+ * Returns CKDA_OK or a negative CKDA_ERR_* code.
+ */
+int ckda_linattn_bwd(const void *q, const void *k, const void *v, const float *g, const float *S0,
+                     const int32_t *cu_seqlens, int n_seqs, int B, int T, int H, int Hq, int Hk,
+                     int Hv, int dk, int dv, int decay, int io_dtype, const void *dO,
+                     const float *dS_T, void *dq, void *dk_out, void *dv_out, float *dg, float *dS0,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace ckda_linattn_bwd needs (host arithmetic, no CUDA call). */
+size_t ckda_linattn_bwd_workspace_size(int B, int T, int H, int Hq, int Hk, int Hv, int dk, int dv,
+                                       int decay, int io_dtype, int n_seqs);
+
+/*
+ * One token of linear attention with a decay for each head, the state updated in place:
+ *   q [B, Hq, dk], k [B, Hk, dk], v [B, Hv, dv] io_dtype; g [B, H] or [H] float32;
+ *   S [B, H, dk, dv] float32 (16-byte aligned); o [B, H, dv] io_dtype (NULL: not written).
+ * Returns CKDA_OK or a negative CKDA_ERR_* code.
+ */
+int ckda_linattn_decode_step(const void *q, const void *k, const void *v, const float *g, float *S,
+                             int B, int H, int Hq, int Hk, int Hv, int dk, int dv, int decay,
+                             int io_dtype, void *o, void *stream);
+
+/*
+ * Rotary positions on q and k in one launch: with t = pos * freqs[i], channel pair i of every
+ * head becomes
+ *   scale * (x_a cos t - x_b sin t,  x_b cos t + x_a sin t)       (inverse: t -> -t)
+ * for the 2 * n_freqs first channels (CKDA_ROTARY_HALF: a = i, b = i + n_freqs;
+ * CKDA_ROTARY_INTERLEAVED: a = 2 i, b = 2 i + 1); the other channels are copied.  The inverse
+ * with the same scale is the gradient.  The angle is formed exactly modulo one turn, at any
+ * position.
+ *   q, q_out : [n_tokens, Hq, d]   k, k_out : [n_tokens, Hk, d] io_dtype (Hk = 0: q alone);
+ *            an output may be its input, else no two of them overlap; element-aligned
+ *            (16-byte aligned tensors with n_freqs and d in whole 16-byte vectors run faster)
+ *   pos    : [n_tokens] int32, or int64 with pos_int64 != 0
+ *   freqs  : [n_freqs] float64 on the device, radians per position (finite); 2 * n_freqs <= d <= 1024
+ * Returns CKDA_OK or a negative CKDA_ERR_* code.
+ */
+int ckda_rotary(const void *q, const void *k, const void *pos, const double *freqs,
+                long long n_tokens, int Hq, int Hk, int d, int n_freqs, int layout, int pos_int64,
+                float scale, int inverse, int io_dtype, void *q_out, void *k_out, void *stream);
 
 /*
  * ckda_chunk_fwd without a caller-provided workspace.  The pages describe no

@@ -26,23 +26,6 @@ bool valid_gate(int sg) {
          (sg & ~(15 | CKDA_GATE_PER_HEAD | CKDA_QK_L2NORM | CKDA_DELTA_PRODUCT2)) == 0;
 }
 
-// sm_100 check for the current device, cached per device (atomics: host threads may call the
-// library concurrently; the cached value is the same whoever writes it).
-int check_device() {
-  static std::atomic<int> cached[64];  // 0 unknown, 1 ok, -1 not sm_100
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return CKDA_ERR_CUDA;
-  const int known = dev >= 0 && dev < 64 ? cached[dev].load(std::memory_order_relaxed) : 0;
-  if (known != 0) return known > 0 ? CKDA_OK : CKDA_ERR_DEVICE;
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return CKDA_ERR_CUDA;
-  const bool ok = (major == 10 && minor == 0);
-  if (dev >= 0 && dev < 64) cached[dev].store(ok ? 1 : -1, std::memory_order_relaxed);
-  return ok ? CKDA_OK : CKDA_ERR_DEVICE;
-}
-
 // ckda_debug_wait_injection's settings (process-wide, read at each launch)
 std::atomic<int> g_inject_chunk{-1};
 std::atomic<unsigned long long> g_inject_wait_ns{0};
@@ -72,6 +55,23 @@ ckda::SegChoice seg_choice_for_lengths(const int32_t *lengths, int n, int H, int
 }  // namespace
 
 namespace ckda {
+
+// sm_100 check for the current device, cached per device (atomics: host threads may call the
+// library concurrently; the cached value is the same whoever writes it).
+int check_device() {
+  static std::atomic<int> cached[64];  // 0 unknown, 1 ok, -1 not sm_100
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return CKDA_ERR_CUDA;
+  const int known = dev >= 0 && dev < 64 ? cached[dev].load(std::memory_order_relaxed) : 0;
+  if (known != 0) return known > 0 ? CKDA_OK : CKDA_ERR_DEVICE;
+  int major = 0, minor = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+    return CKDA_ERR_CUDA;
+  const bool ok = (major == 10 && minor == 0);
+  if (dev >= 0 && dev < 64) cached[dev].store(ok ? 1 : -1, std::memory_order_relaxed);
+  return ok ? CKDA_OK : CKDA_ERR_DEVICE;
+}
 
 int check_chunk_args(const void *q, const void *k, const void *v, const void *a, const float *b,
                      const float *S0, const int32_t *cu_seqlens, int n_seqs, int B, int T, int H,
@@ -164,7 +164,7 @@ int ckda_chunk_fwd(const void *q, const void *k, const void *v, const void *a, c
   if (!workspace || workspace_bytes < ckda::kWorkspaceHeader ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return CKDA_ERR_WORKSPACE;
-  const int dev_rc = check_device();
+  const int dev_rc = ckda::check_device();
   if (dev_rc != CKDA_OK) return dev_rc;
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -211,7 +211,7 @@ int ckda_chunk_bwd(const void *q, const void *k, const void *v, const void *a, c
   const size_t need = ckda_chunk_bwd_workspace_size(B, T, H, dk, dv, cu_seqlens ? n_seqs : 0);
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return CKDA_ERR_WORKSPACE;
-  const int dev_rc = check_device();
+  const int dev_rc = ckda::check_device();
   if (dev_rc != CKDA_OK) return dev_rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(workspace, 0, ckda::kWorkspaceHeader, s) != cudaSuccess) return CKDA_ERR_CUDA;
@@ -243,7 +243,7 @@ int ckda_decode_step(const void *q, const void *k, const void *v, const void *a,
   if (!aligned(q, in_sz) || !aligned(k, in_sz) || !aligned(v, in_sz) || !aligned(a, in_sz) ||
       !aligned(b, 4) || !aligned16(S) || !aligned(o, out_sz))
     return CKDA_ERR_ALIGN;
-  const int dev_rc = check_device();
+  const int dev_rc = ckda::check_device();
   if (dev_rc != CKDA_OK) return dev_rc;
   ckda::DecodeArgs g;
   g.q = q; g.k = k; g.v = v; g.a = a; g.b = b; g.S = S; g.o = o;

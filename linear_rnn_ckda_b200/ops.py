@@ -8,6 +8,7 @@ a CUDA device, these functions raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 from typing import Optional
@@ -24,6 +25,9 @@ CKDA_BF16 = 1
 GATE_PER_HEAD = 16   # one gate logit per token and head: a is [B,T,H] ([B,H] for decode)
 QK_L2NORM = 32       # q and k are L2-normalised inside the kernels
 DELTA_PRODUCT2 = 64  # two keys, values, strengths per token: k [B,T,2,H,dk], v [B,T,2,H,dv], b [B,T,2,H]
+# how linear attention's log decays are given, and rotary channel pairs
+DECAY_PER_TOKEN, DECAY_PER_HEAD = 0, 1
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
 _DT = {torch.float32: CKDA_F32, torch.bfloat16: CKDA_BF16}
 _TORCH_DT = {CKDA_F32: torch.float32, CKDA_BF16: torch.bfloat16}
 
@@ -42,6 +46,13 @@ SIGNATURES = {
     "ckda_chunk_bwd_workspace_size": (ctypes.c_size_t, [_i, _i, _i, _i, _i, _i]),
     "ckda_chunk_fwd_noalloc": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
                                     _i, _i, _i, _vp, _vp, _vp]),
+    "ckda_linattn_fwd": (_i, [_vp] * 6 + [_i] * 11 + [_vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "ckda_linattn_fwd_workspace_size": (ctypes.c_size_t, [_i] * 7),
+    "ckda_linattn_bwd": (_i, [_vp] * 6 + [_i] * 11 + [_vp] * 8 + [ctypes.c_size_t, _vp]),
+    "ckda_linattn_bwd_workspace_size": (ctypes.c_size_t, [_i] * 11),
+    "ckda_linattn_decode_step": (_i, [_vp] * 5 + [_i] * 9 + [_vp, _vp]),
+    "ckda_rotary": (_i, [_vp] * 4 + [ctypes.c_longlong] + [_i] * 6 + [ctypes.c_float, _i, _i, _vp,
+                                                                      _vp, _vp]),
     "ckda_workspace_status": (_i, [_vp, ctypes.POINTER(_i), _vp]),
     "ckda_noalloc_status": (_i, [ctypes.POINTER(_i), _vp]),
     "ckda_debug_wait_injection": (None, [_i, ctypes.c_ulonglong]),
@@ -320,3 +331,220 @@ def workspace_status(workspace: torch.Tensor) -> int:
     if rc != 0:
         raise CkdaError("ckda_workspace_status", rc)
     return st.value
+
+
+# ------------------------------------------------------------------ linear attention
+def _lin_heads(g, lead, **tensors):
+    """(H, decay code, [heads of each tensor]) of linear attention tensors [*lead, Hx, d]."""
+    _need(g.dtype == torch.float32 and (g.dim() == 1 or (g.dim() == len(lead) + 1
+                                                         and tuple(g.shape[:-1]) == lead)),
+          f"g must be {lead + ('H',)} or [H] float32, got {tuple(g.shape)}, {g.dtype}")
+    H = g.shape[-1]
+    _need(H >= 1, "g has no heads")
+    heads = []
+    for name, t in tensors.items():
+        _need(t.dim() == len(lead) + 2 and tuple(t.shape[:-2]) == lead,
+              f"{name} must be {lead + ('heads', 'channels')}, got {tuple(t.shape)}")
+        _need(t.shape[-2] >= 1 and H % t.shape[-2] == 0,
+              f"{name} has {t.shape[-2]} heads, which must divide g's {H}")
+        heads.append(t.shape[-2])
+    return H, (DECAY_PER_HEAD if g.dim() == 1 else DECAY_PER_TOKEN), heads
+
+
+def _lin_types(q, k, v):
+    _need(q.dtype in _DT, f"q must be float32 or bfloat16, got {q.dtype}")
+    _need(k.dtype == q.dtype and v.dtype == q.dtype,
+          f"k and v must be in q's dtype {q.dtype}, got {k.dtype}, {v.dtype}")
+    _need(k.shape[-1] == q.shape[-1], f"q has {q.shape[-1]} channels, k {k.shape[-1]}")
+
+
+def check_linattn_args(q, k, v, g, S0=None, cu_seqlens=None, **states):
+    """Shapes, dtypes and devices that ``ckda_linattn_fwd`` and ``ckda_linattn_bwd`` cannot see.
+    Raises ValueError; returns (N, H, decay code, (Hq, Hk, Hv))."""
+    _need(q.dim() == 4, f"q must be [B,T,Hq,dk], got {tuple(q.shape)}")
+    lead = tuple(q.shape[:2])
+    H, decay, heads = _lin_heads(g, lead, q=q, k=k, v=v)
+    _lin_types(q, k, v)
+    N = lead[0]
+    if cu_seqlens is not None:
+        _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 1 and cu_seqlens.dtype == torch.int32,
+              "cu_seqlens must be a 1-D int32 tensor of N+1 offsets")
+        _need(lead[0] == 1, "packed sequences (cu_seqlens) need B == 1")
+        N = cu_seqlens.numel() - 1
+        _need(N > 0 or lead[1] == 0, "cu_seqlens names no sequence")
+    shape = (N, H, q.shape[-1], v.shape[-1])
+    for name, t in (("S0", S0), *states.items()):
+        _need(t is None or (tuple(t.shape) == shape and t.dtype == torch.float32),
+              f"{name} must be [N,H,dk,dv] = {shape} float32")
+    _same_device(q, k=k, v=v, g=g, S0=S0, cu_seqlens=cu_seqlens, **states)
+    return N, H, decay, tuple(heads)
+
+
+def _call(dev, name, *args):
+    """Calls an entry point on ``dev`` and its current stream (the last argument)."""
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(dev))
+    if rc != 0:
+        raise CkdaError(name, rc)
+
+
+def linattn_fwd_workspace_size(B, T, H, dk, dv, dtype, n_seqs=0) -> int:
+    return int(load().ckda_linattn_fwd_workspace_size(B, T, H, dk, dv, _DT[dtype], n_seqs))
+
+
+def linattn_fwd(q, k, v, g, S0=None, cu_seqlens=None, o=None, S_T=None, workspace=None,
+                want_o: bool = True, want_state: bool = True):
+    """Linear attention with a decay for each head, S_t = exp(g_t) S_{t-1} + k_t v_t^T,
+    o_t = S_t^T q_t.  Returns (o, S_T) (either None when not wanted).
+
+    q [B,T,Hq,dk], k [B,T,Hk,dk], v [B,T,Hv,dv] in one dtype (float32 or bfloat16); g: log
+    decays <= 0, float32 [B,T,H], or [H] for fixed ones; Hq, Hk and Hv divide H; S0 [N,H,dk,dv]
+    float32 or None; cu_seqlens int32 [N+1] on the device (B == 1) or None.  o [B,T,H,dv]."""
+    N, H, decay, heads = check_linattn_args(q, k, v, g, S0, cu_seqlens, S_T=S_T)
+    B, T, _, dk = q.shape
+    dv, dev, packed = v.shape[-1], q.device, cu_seqlens is not None
+    _need(o is None or (tuple(o.shape) == (B, T, H, dv) and o.dtype == q.dtype and o.device == dev),
+          f"o must be [B,T,H,dv] = {(B, T, H, dv)} in {q.dtype} on {dev}")
+    if want_o and o is None:
+        o = torch.empty((B, T, H, dv), dtype=q.dtype, device=dev)
+    if want_state and S_T is None:
+        S_T = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+    if workspace is None:
+        n = linattn_fwd_workspace_size(B, T, H, dk, dv, q.dtype, N if packed else 0)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    _need(workspace.device == dev, f"workspace is on {workspace.device}, q on {dev}")
+    _call(dev, "ckda_linattn_fwd", _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(cu_seqlens),
+          N if packed else 0, B, T, H, *heads, dk, dv, decay, _DT[q.dtype],
+          _ptr(o if want_o else None), _ptr(S_T if want_state else None), _ptr(workspace),
+          workspace.numel() * workspace.element_size())
+    return (o if want_o else None), (S_T if want_state else None)
+
+
+def linattn_bwd_workspace_size(B, T, H, Hq, Hk, Hv, dk, dv, decay, dtype, n_seqs=0) -> int:
+    return int(load().ckda_linattn_bwd_workspace_size(B, T, H, Hq, Hk, Hv, dk, dv, decay,
+                                                      _DT[dtype], n_seqs))
+
+
+def linattn_bwd(q, k, v, g, S0=None, cu_seqlens=None, dO=None, dS_T=None, want_dS0: bool = True,
+                workspace=None, grads=None):
+    """Backward of ``linattn_fwd``: gradients of sum(dO * o) + sum(dS_T * S_T).
+
+    Returns (dq, dk, dv, dg, dS0): dq, dk, dv as q, k, v; dg as g; dS0 [N,H,dk,dv] float32
+    (None when not wanted).  dO [B,T,H,dv] in q's dtype or None (zero); dS_T [N,H,dk,dv]
+    float32 or None (zero).  ``grads`` may supply the five output tensors."""
+    N, H, decay, heads = check_linattn_args(q, k, v, g, S0, cu_seqlens, dS_T=dS_T)
+    B, T, _, dk = q.shape
+    dv, dev, packed = v.shape[-1], q.device, cu_seqlens is not None
+    _need(dO is None or (tuple(dO.shape) == (B, T, H, dv) and dO.dtype == q.dtype),
+          f"dO must be [B,T,H,dv] = {(B, T, H, dv)} in {q.dtype}")
+    if grads is None:
+        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g),
+                 torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if want_dS0 else None)
+    gq, gk, gv, gg, gS0 = grads
+    for name, t, like in (("dq", gq, q), ("dk", gk, k), ("dv", gv, v), ("dg", gg, g)):
+        _need(t is not None and t.shape == like.shape and t.dtype == like.dtype,
+              f"{name} must be {tuple(like.shape)} in {like.dtype}")
+    _need(gS0 is None or (tuple(gS0.shape) == (N, H, dk, dv) and gS0.dtype == torch.float32),
+          f"dS0 must be [N,H,dk,dv] = {(N, H, dk, dv)} float32")
+    _need(gS0 is not None or not want_dS0, "dS0 buffer missing")
+    _same_device(q, dO=dO, dq=gq, dk=gk, dv=gv, dg=gg, dS0=gS0)
+    if workspace is None:
+        n = linattn_bwd_workspace_size(B, T, H, *heads, dk, dv, decay, q.dtype, N if packed else 0)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    _need(workspace.device == dev, f"workspace is on {workspace.device}, q on {dev}")
+    _call(dev, "ckda_linattn_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(cu_seqlens),
+          N if packed else 0, B, T, H, *heads, dk, dv, decay, _DT[q.dtype], _ptr(dO), _ptr(dS_T),
+          _ptr(gq), _ptr(gk), _ptr(gv), _ptr(gg), _ptr(gS0 if want_dS0 else None), _ptr(workspace),
+          workspace.numel() * workspace.element_size())
+    return gq, gk, gv, gg, (gS0 if want_dS0 else None)
+
+
+def linattn_decode_step(q, k, v, g, S, o=None, want_o: bool = True):
+    """One token of ``linattn_fwd``: S [B,H,dk,dv] float32 is updated in place; returns o
+    [B,H,dv] (None when not wanted).  q [B,Hq,dk], k [B,Hk,dk], v [B,Hv,dv]; g [B,H] or [H]."""
+    _need(q.dim() == 3, f"q must be [B,Hq,dk], got {tuple(q.shape)}")
+    B, dk, dev = q.shape[0], q.shape[-1], q.device
+    H, decay, heads = _lin_heads(g, (B,), q=q, k=k, v=v)
+    _lin_types(q, k, v)
+    dv = v.shape[-1]
+    _need(tuple(S.shape) == (B, H, dk, dv) and S.dtype == torch.float32,
+          f"S must be [B,H,dk,dv] = {(B, H, dk, dv)} float32")
+    _need(o is None or (tuple(o.shape) == (B, H, dv) and o.dtype == q.dtype),
+          f"o must be [B,H,dv] = {(B, H, dv)} in {q.dtype}")
+    _same_device(q, k=k, v=v, g=g, S=S, o=o)
+    if want_o and o is None:
+        o = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
+    _call(dev, "ckda_linattn_decode_step", _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S), B, H,
+          *heads, dk, dv, decay, _DT[q.dtype], _ptr(o if want_o else None))
+    return o if want_o else None
+
+
+# ------------------------------------------------------------------ rotary positions
+def rotary_freqs(dim: int, base: float = 10000.0, scaling: Optional[str] = None,
+                 factor: float = 1.0, original_len: int = 4096, fast: float = 32.0,
+                 slow: float = 1.0, device=None):
+    """(freqs, scale) for ``rotary``: float64 radians per position of dim / 2 channel pairs,
+    base^(-2 i / dim), and the factor on the turned channels.
+
+    scaling, for contexts ``factor`` times longer than ``original_len``: "linear" divides every
+    frequency by the factor; "base" raises the base by factor^(dim / (dim - 2)), which keeps the
+    fastest pair and divides the slowest by the factor; "ramp" divides the pairs that turn fewer
+    than ``slow`` times over the original length, keeps those that turn more than ``fast`` times,
+    blends between, and scales by 0.1 ln(factor) + 1."""
+    _need(dim >= 0 and dim % 2 == 0, f"dim must be even, got {dim}")
+    _need(scaling in (None, "linear", "base", "ramp"), f"unknown scaling {scaling!r}")
+    _need(factor >= 1.0, f"factor must be at least 1, got {factor}")
+    _need(scaling != "base" or dim > 2, "scaling 'base' needs more than one pair")
+    i = torch.arange(dim // 2, dtype=torch.float64)
+    if scaling == "base":
+        base = base * factor ** (dim / (dim - 2))
+    f = torch.pow(torch.tensor(float(base), dtype=torch.float64), -2.0 * i / max(dim, 1))
+    scale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "ramp":
+        turns = original_len * f / (2.0 * math.pi)
+        keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
+        f = f / factor * (1.0 - keep) + f * keep
+        scale = 0.1 * math.log(factor) + 1.0
+    return f.to(device or "cuda"), scale
+
+
+def rotary(q, k, pos, freqs, layout: str = "half", inverse: bool = False, scale: float = 1.0,
+           q_out=None, k_out=None):
+    """Turns channel pairs of q and k by pos * freqs (one launch); returns (q_out, k_out).
+
+    q [*lead,Hq,d], k [*lead,Hk,d] or None, float32 or bfloat16; pos int32 or int64 [*lead];
+    freqs float64 [n], 2 n <= d: pair i is channels (i, i + n) ("half") or (2 i, 2 i + 1)
+    ("interleaved"); channels from 2 n on are copied.  ``inverse`` turns back (with the same
+    scale: the gradient).  An output may be its input."""
+    _need(layout in ROTARY_LAYOUTS, f"layout must be one of {sorted(ROTARY_LAYOUTS)}, got {layout!r}")
+    _need(q.dim() >= 2, f"q must be [*lead,Hq,d], got {tuple(q.shape)}")
+    _need(q.dtype in _DT, f"q must be float32 or bfloat16, got {q.dtype}")
+    lead, (Hq, d), dev = tuple(q.shape[:-2]), q.shape[-2:], q.device
+    _need(k is None or (k.dim() == q.dim() and tuple(k.shape[:-2]) == lead and k.shape[-1] == d
+                        and k.dtype == q.dtype),
+          f"k must be {lead + ('Hk', d)} in q's dtype")
+    _need(tuple(pos.shape) == lead and pos.dtype in (torch.int32, torch.int64),
+          f"pos must be {lead} int32 or int64, got {tuple(pos.shape)}, {pos.dtype}")
+    _need(freqs.dim() == 1 and freqs.dtype == torch.float64 and 2 * freqs.numel() <= d,
+          f"freqs must be float64 [n] with 2 n <= {d}")
+    q_out = torch.empty_like(q) if q_out is None else q_out
+    if k is None:
+        _need(k_out is None, "k_out without k")
+    elif k_out is None:
+        k_out = torch.empty_like(k)
+    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+        _need(t is None or (t.shape == like.shape and t.dtype == like.dtype),
+              f"{name} must be shaped and typed as its input")
+    _same_device(q, k=k, pos=pos, freqs=freqs, q_out=q_out, k_out=k_out)
+    _call(dev, "ckda_rotary", _ptr(q), _ptr(k), _ptr(pos), _ptr(freqs), pos.numel(), Hq,
+          k.shape[-2] if k is not None else 0, d, freqs.numel(), ROTARY_LAYOUTS[layout],
+          int(pos.dtype == torch.int64), scale, int(inverse), _DT[q.dtype], _ptr(q_out), _ptr(k_out))
+    return q_out, k_out

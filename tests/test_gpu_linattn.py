@@ -1,0 +1,345 @@
+"""Linear attention with a decay for each head on the GPU against the float64 token loop.
+
+Tolerances (relative Frobenius error, assert_close): fp32 results hold the library's fp32 bar,
+1e-5 (sums of a few hundred products, each rounded by 2^-24, stay below 1e-6), and dg, a
+difference of sums, the backward's 1e-4.  bf16 outputs are rounded once (at most 2^-8 of a
+value, in the mean square at most 2^-8 / sqrt 3) and may read a state and scores rounded
+likewise, whose errors add in squares: sqrt 2 * 2^-8 / sqrt 3 = 3.2e-3 < 2^-8."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import linattn_ref as ref
+from helpers import assert_close, f64
+
+pytestmark = pytest.mark.gpu
+TOL = {torch.float32: 1e-5, torch.bfloat16: 2.0 ** -8}
+TOL_DG = 1e-4
+F32, BF = torch.float32, torch.bfloat16
+
+
+def make(B, T, H, Hq, Hk, Hv, dk, dv, dtype, fixed=False, N=None, state=True, seed=0, gate=4.0):
+    gen = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=gen, dtype=torch.float64)  # noqa: E731
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True)  # noqa: E731
+    N = B if N is None else N
+    t = dict(q=unit(r(B, T, Hq, dk)).to(dtype), k=unit(r(B, T, Hk, dk)).to(dtype), v=r(B, T, Hv, dv).to(dtype))
+    if fixed:
+        t["g"] = -torch.exp2(-8.0 * torch.arange(1, H + 1) / H).float()
+    else:
+        t["g"] = torch.nn.functional.logsigmoid(gate + r(B, T, H)).float()
+    t["S0"] = (0.1 * r(N, H, dk, dv)).float() if state else None
+    return t, (r(B, T, H, dv).to(dtype), r(N, H, dk, dv).float() if state else None)
+
+
+def cuda(t):
+    return {n: None if x is None else x.cuda() for n, x in t.items()}
+
+
+def normal(x):
+    """Values below fp32's smallest normal number, 2^-126, as 0: there fp32 is spaced by 2^-149, so
+    no relative tolerance holds (a value of 5e-45 is off by up to 2^-150 = 7e-46, 14 % of it)."""
+    x = np.array(x, dtype=np.float64)
+    x[np.abs(x) < 2.0 ** -126] = 0.0
+    return x
+
+
+def offsets(lens):
+    return torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32)
+
+
+def check_fwd(ops, t, cu=None):
+    d = cuda(t)
+    o, S = ops.linattn_fwd(**d, cu_seqlens=None if cu is None else cu.cuda())
+    ro, rS = ref.fwd(**t, cu=cu)
+    dt = t["q"].dtype
+    assert o.dtype == dt and S.dtype == F32
+    assert_close(f64(o), ro.numpy(), TOL[dt], "o", bf16_out=dt == BF)
+    assert_close(normal(f64(S)), normal(rS.numpy()), TOL[F32], "S_T")
+    return o, S
+
+
+def check_bwd(ops, t, dO, dS, cu=None):
+    d = cuda(t)
+    got = ops.linattn_bwd(**d, cu_seqlens=None if cu is None else cu.cuda(),
+                          dO=None if dO is None else dO.cuda(), dS_T=None if dS is None else dS.cuda())
+    want = ref.bwd(**t, cu=cu, dO=dO, dS_T=dS)
+    dt = t["q"].dtype
+    for name, x, y in zip(("dq", "dk", "dv", "dg", "dS0"), got, want):
+        low = name in ("dq", "dk", "dv")
+        assert x.dtype == (dt if low else F32) and bool(torch.isfinite(x).all()), name
+        y = y.detach().numpy()
+        if name == "dg":
+            assert_close(f64(x).reshape(-1, x.shape[-1]), y.reshape(-1, y.shape[-1]), TOL_DG, name)
+        else:
+            x, y = (f64(x), y) if low else (normal(f64(x)), normal(y))
+            assert_close(x, y, TOL[dt] if low else TOL[F32], name, bf16_out=low and dt == BF)
+
+
+HEADS = [(3, 3, 3, 3), (4, 4, 2, 2), (4, 1, 1, 4), (6, 2, 3, 1)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T", [1, 2, 63, 64, 65, 200])
+def test_fwd_lengths(cuda_lib, T, dtype):
+    check_fwd(cuda_lib, make(2, T, 2, 2, 2, 2, 128, 128, dtype, seed=T)[0])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("dk,dv", [(16, 16), (32, 128), (128, 32), (64, 64), (16, 128), (128, 64)])
+def test_dims(cuda_lib, dk, dv, dtype):
+    t, (dO, dS) = make(1, 130, 2, 2, 2, 2, dk, dv, dtype, seed=dk + dv)
+    check_fwd(cuda_lib, t)
+    check_bwd(cuda_lib, t, dO, dS)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("H,Hq,Hk,Hv", HEADS)
+@pytest.mark.parametrize("fixed", [False, True])
+def test_shared_heads(cuda_lib, H, Hq, Hk, Hv, fixed, dtype):
+    t, (dO, dS) = make(2, 70, H, Hq, Hk, Hv, 32, 64, dtype, fixed=fixed, seed=H + Hq)
+    check_fwd(cuda_lib, t)
+    check_bwd(cuda_lib, t, dO, dS)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("lens", [[1, 0, 64, 65, 0, 63, 7], [0, 0, 300], [0], [0, 1, 0], [128, 128]])
+def test_packed(cuda_lib, lens, dtype):
+    t, (dO, dS) = make(1, sum(lens), 2, 2, 2, 2, 64, 128, dtype, N=len(lens), seed=len(lens))
+    cu = offsets(lens)
+    check_fwd(cuda_lib, t, cu)
+    check_bwd(cuda_lib, t, dO, dS, cu)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T", [1, 64, 129])
+def test_bwd_lengths(cuda_lib, T, dtype):
+    t, (dO, dS) = make(2, T, 2, 2, 2, 2, 128, 128, dtype, seed=T)
+    check_bwd(cuda_lib, t, dO, dS)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_missing_parts(cuda_lib, dtype):
+    """No S0; no dO; no dS_T; nothing wanted but one output."""
+    t, (dO, _) = make(1, 100, 2, 2, 2, 2, 64, 64, dtype, state=False)
+    check_fwd(cuda_lib, t)
+    check_bwd(cuda_lib, t, dO, None)
+    t, (dO, dS) = make(1, 100, 2, 2, 2, 2, 64, 64, dtype)
+    check_bwd(cuda_lib, t, None, dS)
+    check_bwd(cuda_lib, t, dO, None)
+    d = cuda(t)
+    o, S = cuda_lib.linattn_fwd(**d)
+    o1, none = cuda_lib.linattn_fwd(**d, want_state=False)
+    none2, S1 = cuda_lib.linattn_fwd(**d, want_o=False)
+    assert none is None and none2 is None and torch.equal(o, o1) and torch.equal(S, S1)
+    got = cuda_lib.linattn_bwd(**d, dO=dO.cuda(), want_dS0=False)
+    assert got[4] is None
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_long_sequences(cuda_lib, dtype):
+    """Long enough to be split over many SMs; few and many heads, slow decays."""
+    for B, T, H in ((1, 4000, 1), (2, 1500, 3)):
+        t, (dO, dS) = make(B, T, H, H, H, H, 64, 64, dtype, seed=T, gate=7.0)
+        check_fwd(cuda_lib, t)
+        check_bwd(cuda_lib, t, dO, dS)
+    lens = [2000, 0, 37, 900]
+    t, (dO, dS) = make(1, sum(lens), 2, 2, 1, 1, 128, 128, dtype, N=4, seed=9, gate=6.0)
+    check_fwd(cuda_lib, t, offsets(lens))
+    check_bwd(cuda_lib, t, dO, dS, offsets(lens))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_extreme_decays(cuda_lib, dtype):
+    """Resets (-inf), decays that underflow within a chunk, exact ones (0), in one batch."""
+    t, (dO, dS) = make(1, 200, 3, 3, 3, 3, 64, 64, dtype, seed=3)
+    g = t["g"]
+    g[0, :, 0] = 0.0
+    g[0, 10::37, 1] = -math.inf
+    g[0, :, 2] = -60.0
+    g[0, 100:110, 2] = -1e30
+    check_fwd(cuda_lib, t)
+    check_bwd(cuda_lib, t, dO, dS)
+
+
+def test_large_sums_of_decays(cuda_lib):
+    """A chunk that starts with a thousandfold underflow and then decays slowly: the weights among
+    the later tokens keep fp32 accuracy although their summed decays are large."""
+    t, (dO, dS) = make(1, 128, 1, 1, 1, 1, 64, 64, F32, seed=4)
+    t["g"][0, :, 0] = -0.001
+    t["g"][0, 0:30, 0] = -99.7
+    check_fwd(cuda_lib, t)
+    check_bwd(cuda_lib, t, dO, dS)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_values_stay_in_their_sequence(cuda_lib, dtype):
+    """NaN and infinity in one sequence (all its inputs) leave the neighbours' results as they are."""
+    lens = [30, 70, 100, 5]
+    t, (dO, dS) = make(1, sum(lens), 2, 2, 2, 2, 64, 64, dtype, N=4, seed=5)
+    cu = offsets(lens).cuda()
+    d = cuda(t)
+    clean = cuda_lib.linattn_fwd(**d, cu_seqlens=cu)
+    clean_b = cuda_lib.linattn_bwd(**d, cu_seqlens=cu, dO=dO.cuda(), dS_T=dS.cuda())
+    for val in (math.nan, math.inf):
+        e = {n: x.clone() for n, x in d.items()}
+        do = dO.cuda().clone()
+        for n in ("q", "k", "v"):
+            e[n][0, 30:100] = val
+        e["g"][0, 30:100] = math.nan
+        do[0, 30:100] = val
+        o, S = cuda_lib.linattn_fwd(**e, cu_seqlens=cu)
+        keep = torch.ones(sum(lens), dtype=torch.bool)
+        keep[30:100] = False
+        assert torch.equal(o[0, keep], clean[0][0, keep])
+        assert torch.equal(S[[0, 2, 3]], clean[1][[0, 2, 3]])
+        got = cuda_lib.linattn_bwd(**e, cu_seqlens=cu, dO=do, dS_T=dS.cuda())
+        for x, y in zip(got[:4], clean_b[:4]):
+            assert torch.equal(x[0, keep], y[0, keep])
+        assert torch.equal(got[4][[0, 2, 3]], clean_b[4][[0, 2, 3]])
+
+
+def test_bad_offsets_write_nothing(cuda_lib):
+    t, _ = make(1, 100, 2, 2, 2, 2, 64, 64, BF, N=3)
+    d = cuda(t)
+    good = torch.tensor([0, 20, 60, 100], dtype=torch.int32, device="cuda")
+    n = cuda_lib.linattn_fwd_workspace_size(1, 100, 2, 64, 64, BF, 3)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for bad in ([0, 60, 20, 100], [0, 20, 60, 90], [1, 20, 60, 100], [0, 20, 400, 100], [0, -5, 60, 100]):
+        o = torch.full((1, 100, 2, 64), 7.0, dtype=BF, device="cuda")
+        S = torch.full((3, 2, 64, 64), 7.0, device="cuda")
+        cuda_lib.linattn_fwd(**d, cu_seqlens=torch.tensor(bad, dtype=torch.int32, device="cuda"), o=o, S_T=S,
+                             workspace=ws)
+        assert cuda_lib.workspace_status(ws) == -6
+        assert bool((o == 7).all()) and bool((S == 7).all())
+    cuda_lib.linattn_fwd(**d, cu_seqlens=good, o=o, S_T=S, workspace=ws)
+    assert cuda_lib.workspace_status(ws) == 0
+    ro, _ = ref.fwd(**t, cu=good.cpu())
+    assert_close(f64(o), ro.numpy(), TOL[BF], "o", bf16_out=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_prompt_in_parts_and_tokens(cuda_lib, dtype):
+    """A prompt, the same in two parts through the state (S_T in S0's place), and token by token."""
+    t, _ = make(2, 150, 4, 4, 2, 2, 64, 64, dtype, seed=6)
+    d = cuda(t)
+    o, S = cuda_lib.linattn_fwd(**d)
+    cut = lambda a, b: {n: d[n][:, a:b].contiguous() for n in ("q", "k", "v", "g")}  # noqa: E731
+    St = d["S0"].clone()
+    oa, _ = cuda_lib.linattn_fwd(**cut(0, 71), S0=St, S_T=St)
+    ob, _ = cuda_lib.linattn_fwd(**cut(71, 150), S0=St, S_T=St)
+    ro, rS = ref.fwd(**t)
+    assert_close(f64(torch.cat([oa, ob], 1)), ro.numpy(), TOL[dtype], "parts", bf16_out=dtype == BF)
+    assert_close(f64(St), rS.numpy(), TOL[F32], "S of parts")
+    St = d["S0"].clone()
+    steps = [cuda_lib.linattn_decode_step(*(d[n][:, i].contiguous() for n in ("q", "k", "v", "g")), St)
+             for i in range(150)]
+    assert_close(f64(torch.stack(steps, 1)), ro.numpy(), TOL[dtype], "tokens", bf16_out=dtype == BF)
+    assert_close(f64(St), rS.numpy(), TOL[F32], "S of tokens")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("B,H,Hq,Hk,Hv,dk,dv,fixed", [
+    (1, 1, 1, 1, 1, 128, 128, False), (3, 6, 2, 3, 6, 64, 16, True), (5, 4, 4, 1, 1, 16, 128, False),
+    (2, 2, 2, 2, 2, 32, 32, True), (64, 32, 32, 8, 8, 128, 64, False)])
+def test_decode(cuda_lib, B, H, Hq, Hk, Hv, dk, dv, fixed, dtype):
+    t, _ = make(B, 1, H, Hq, Hk, Hv, dk, dv, dtype, fixed=fixed, seed=B)
+    d = cuda(t)
+    g = d["g"] if fixed else d["g"][:, 0].contiguous()
+    args = [d[n][:, 0].contiguous() for n in ("q", "k", "v")] + [g]
+    S, S1 = d["S0"].clone(), d["S0"].clone()
+    o = cuda_lib.linattn_decode_step(*args, S)
+    assert cuda_lib.linattn_decode_step(*args, S1, want_o=False) is None
+    ro, rS = ref.fwd(**t)
+    assert_close(f64(o), ro[:, 0].numpy(), TOL[dtype], "o", bf16_out=dtype == BF)
+    assert_close(f64(S), rS.numpy(), TOL[F32], "S")
+    assert torch.equal(S, S1)
+
+
+def test_decode_unaligned_and_empty(cuda_lib):
+    """q, k, v, o that start at an odd element; B = 0."""
+    t, _ = make(3, 1, 2, 2, 2, 2, 64, 64, BF, seed=8)
+    d = cuda(t)
+    odd = lambda x: torch.cat([x.new_zeros(1), x.flatten()])[1:].view(x.shape)  # noqa: E731
+    args = [d[n][:, 0].contiguous() for n in ("q", "k", "v", "g")]
+    Sa, Sb = d["S0"].clone(), d["S0"].clone()
+    o = cuda_lib.linattn_decode_step(*args, Sa)
+    ob = cuda_lib.linattn_decode_step(*(odd(x) for x in args), Sb, o=odd(torch.zeros_like(o)))
+    assert torch.equal(o, ob) and torch.equal(Sa, Sb)
+    e = cuda_lib.linattn_decode_step(*(x[:0] for x in args), Sa[:0])
+    assert e.shape == (0, 2, 64)
+
+
+def test_empty_calls(cuda_lib):
+    for B, T in ((0, 5), (2, 0)):
+        t, (dO, dS) = make(B, T, 2, 2, 2, 2, 64, 64, BF, fixed=True, seed=1)
+        d = cuda(t)
+        o, S = cuda_lib.linattn_fwd(**d)
+        assert o.shape == (B, T, 2, 64) and torch.equal(S, d["S0"])
+        got = cuda_lib.linattn_bwd(**d, dO=dO.cuda(), dS_T=dS.cuda())
+        assert torch.equal(got[4], dS.cuda()) and bool((got[3] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_same_bits_again_and_in_graphs(cuda_lib, dtype):
+    """Repeats, another stream, and two captured graphs replayed in turn give the same bits."""
+    t, (dO, dS) = make(2, 333, 4, 4, 2, 2, 64, 128, dtype, seed=7)
+    d, dO, dS = cuda(t), dO.cuda(), dS.cuda()
+
+    def call():
+        return [*cuda_lib.linattn_fwd(**d), *cuda_lib.linattn_bwd(**d, dO=dO, dS_T=dS)]
+
+    first = call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = call()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = call()
+        graphs.append((g, out))
+    for _ in range(2):
+        for g, out in graphs:
+            for x in out:
+                x.zero_()
+            g.replay()
+    torch.cuda.synchronize()
+    for x, y, a, b in zip(first, other, graphs[0][1], graphs[1][1]):
+        assert torch.equal(x, y) and torch.equal(x, a) and torch.equal(x, b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_rotary_then_attention(cuda_lib, dtype):
+    """Rotary positions, linear attention and its gradients back through the turn, as a layer
+    runs them; then one more token of each sequence from the state."""
+    B, T, H, Hk, d_ = 2, 90, 4, 2, 64
+    t, (dO, dS) = make(B, T + 1, H, H, Hk, Hk, d_, d_, dtype, seed=11)
+    dS = dS * 0.1
+    d = cuda(t)
+    pos = (torch.arange(T + 1, dtype=torch.int32) + torch.tensor([[5], [100000]], dtype=torch.int32))
+    freqs, scale = cuda_lib.rotary_freqs(48, scaling="ramp", factor=4.0)
+    part = lambda n, a, b: d[n][:, a:b].contiguous()  # noqa: E731
+    qr, kr = cuda_lib.rotary(part("q", 0, T), part("k", 0, T), pos[:, :T].contiguous().cuda(), freqs, scale=scale)
+    o, S = cuda_lib.linattn_fwd(qr, kr, part("v", 0, T), part("g", 0, T), S0=d["S0"])
+    dq, dk, dv, dg, dS0 = cuda_lib.linattn_bwd(qr, kr, part("v", 0, T), part("g", 0, T), S0=d["S0"],
+                                               dO=dO[:, :T].contiguous().cuda(), dS_T=dS.cuda())
+    dq, dk = cuda_lib.rotary(dq, dk, pos[:, :T].contiguous().cuda(), freqs, scale=scale, inverse=True)
+    # the same in float64, fed the kernel's own rounded q and k
+    want = ref.bwd(qr.cpu(), kr.cpu(), t["v"][:, :T], t["g"][:, :T], t["S0"], None, dO[:, :T], dS)
+    wq, wk = (ref.rotary(x.detach(), pos[:, :T], freqs.cpu(), "half", inverse=True, scale=scale) for x in want[:2])
+    ro, rS = ref.fwd(qr, kr, t["v"][:, :T], t["g"][:, :T], t["S0"])
+    b = dtype == BF
+    assert_close(f64(o), ro.numpy(), TOL[dtype], "o", bf16_out=b)
+    # (a second rounding on the way back: bf16 errors add in squares, sqrt 3 / sqrt 3 * 2^-8)
+    for x, y, n in ((dq, wq, "dq"), (dk, wk, "dk")):
+        assert_close(f64(x), y.numpy(), 2 * TOL[dtype], n, bf16_out=b)
+    tok = pos[:, T].contiguous().cuda()
+    q1, k1 = cuda_lib.rotary(d["q"][:, T].contiguous(), d["k"][:, T].contiguous(), tok, freqs, scale=scale)
+    o1 = cuda_lib.linattn_decode_step(q1, k1, d["v"][:, T].contiguous(), d["g"][:, T].contiguous(), S)
+    r1, _ = ref.fwd(q1[:, None], k1[:, None], t["v"][:, T:], t["g"][:, T:], rS)
+    assert_close(f64(o1), r1[:, 0].numpy(), TOL[dtype], "o of the next token", bf16_out=b)
