@@ -36,7 +36,8 @@ __device__ __forceinline__ bool find_piece(const Slots &s, long slot, Piece &p) 
   long first;
   int total;
   if (s.cu) {
-    if (*s.status) return false;
+    // (only the plan writes this code, so all threads read the same)
+    if (*s.status == CKDA_ERR_SEQLENS) return false;
     p.n = s.table[slot];
     if (p.n < 0) return false;
     first = s.cu[p.n];
@@ -63,6 +64,16 @@ struct PlanTable {
 };
 int launch_plan(const int32_t *cu, int N, int T, const PlanTable *tables, int n_tables, int *status,
                 cudaStream_t s);
+
+// The tensor-core path (linattn_tc.cu): bf16 inputs.
+size_t tc_workspace(bool packed, int N, int B, int T, int H, int Hq, int Hk, int Hv, int dk, int dv,
+                    bool g_fixed, bool back);
+int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s);
+// Sums over the heads that share one head of x [rows, Hx, d], and of a fixed decay's gradient
+// over the rows (linattn_simt.cu).
+void launch_share(const void *part, void *out, long rows, int H, int Hx, int d, bool bf16,
+                  const int *status, cudaStream_t s);
+void launch_fixed(const float *part, float *dg, long rows, int H, const int *status, cudaStream_t s);
 
 // Log decays in base 2.  exp2 of anything below -200 is 0 in fp32, so clamping there changes no
 // result, keeps -inf (a reset) finite, and bounds a chunk's sum by 12,800.

@@ -574,16 +574,10 @@ int run(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
   if (b) {
     const long rows = (long)a.B * a.T;
     if (grid.x > 0) lin_grad_kernel<T><<<flat, kThreads, kGradSmem, s>>>(p);
-    auto share = [&](const void *part, void *out, int Hx, int d) {
-      const long n = rows * Hx * d;
-      if (n > 0)
-        lin_share_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(
-            static_cast<const float *>(part), static_cast<T *>(out), n, a.H, Hx, d, a.status);
-    };
-    if (p.part_q) share(p.dq, b->dq, a.Hq, a.dk);
-    if (p.part_k) share(p.dk, b->dk, a.Hk, a.dk);
-    if (p.part_v) share(p.dv, b->dv, a.Hv, a.dv);
-    if (a.g_fixed) lin_fixed_kernel<<<a.H, 256, 0, s>>>(p.dg, b->dg, rows, a.H, a.status);
+    if (p.part_q) launch_share(p.dq, b->dq, rows, a.H, a.Hq, a.dk, sizeof(T) == 2, a.status, s);
+    if (p.part_k) launch_share(p.dk, b->dk, rows, a.H, a.Hk, a.dk, sizeof(T) == 2, a.status, s);
+    if (p.part_v) launch_share(p.dv, b->dv, rows, a.H, a.Hv, a.dv, sizeof(T) == 2, a.status, s);
+    if (a.g_fixed) launch_fixed(p.dg, b->dg, rows, a.H, a.status, s);
   }
   return cudaGetLastError() == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
 }
@@ -614,6 +608,21 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t *cu, int N, in
 
 }  // namespace
 
+void launch_share(const void *part, void *out, long rows, int H, int Hx, int d, bool bf16,
+                  const int *status, cudaStream_t s) {
+  const long n = rows * Hx * d;
+  if (n == 0) return;
+  const unsigned grid = (unsigned)((n + 255) / 256);
+  const float *in = static_cast<const float *>(part);
+  if (bf16)
+    lin_share_kernel<<<grid, 256, 0, s>>>(in, static_cast<__nv_bfloat16 *>(out), n, H, Hx, d, status);
+  else
+    lin_share_kernel<<<grid, 256, 0, s>>>(in, static_cast<float *>(out), n, H, Hx, d, status);
+}
+void launch_fixed(const float *part, float *dg, long rows, int H, const int *status, cudaStream_t s) {
+  lin_fixed_kernel<<<H, 256, 0, s>>>(part, dg, rows, H, status);
+}
+
 int launch_plan(const int32_t *cu, int N, int T, const PlanTable *tables, int n_tables, int *status,
                 cudaStream_t s) {
   PlanTable none{nullptr, 1, 0, 0};
@@ -624,17 +633,21 @@ int launch_plan(const int32_t *cu, int N, int T, const PlanTable *tables, int n_
 
 }  // namespace lin
 
-size_t linattn_fwd_workspace(int B, int T, int H, int dk, int dv, int N, bool packed, int) {
+// fp32 inputs run in exact fp32 on CUDA cores, bf16 ones on the tensor cores.
+size_t linattn_fwd_workspace(int B, int T, int H, int dk, int dv, int N, bool packed, int io_dtype) {
+  if (io_dtype == CKDA_BF16) return lin::tc_workspace(packed, N, B, T, H, H, H, H, dk, dv, false, false);
   return lin::layout(packed, N, T, B, H, H, H, H, dk, dv, false, false).total;
 }
 size_t linattn_bwd_workspace(const LinArgs &a, bool packed) {
+  if (a.io_dtype == CKDA_BF16)
+    return lin::tc_workspace(packed, a.N, a.B, a.T, a.H, a.Hq, a.Hk, a.Hv, a.dk, a.dv, a.g_fixed, true);
   return lin::layout(packed, a.N, a.T, a.B, a.H, a.Hq, a.Hk, a.Hv, a.dk, a.dv, a.g_fixed, true).total;
 }
 int launch_linattn_fwd(const LinArgs &a, cudaStream_t s) {
-  return a.io_dtype == CKDA_BF16 ? lin::run<__nv_bfloat16>(a, nullptr, s) : lin::run<float>(a, nullptr, s);
+  return a.io_dtype == CKDA_BF16 ? lin::launch_tc(a, nullptr, s) : lin::run<float>(a, nullptr, s);
 }
 int launch_linattn_bwd(const LinBwdArgs &b, cudaStream_t s) {
-  return b.f.io_dtype == CKDA_BF16 ? lin::run<__nv_bfloat16>(b.f, &b, s) : lin::run<float>(b.f, &b, s);
+  return b.f.io_dtype == CKDA_BF16 ? lin::launch_tc(b.f, &b, s) : lin::run<float>(b.f, &b, s);
 }
 
 }  // namespace ckda
