@@ -75,22 +75,30 @@ void launch_share(const void *part, void *out, long rows, int H, int Hx, int d, 
                   const int *status, cudaStream_t s);
 void launch_fixed(const float *part, float *dg, long rows, int H, const int *status, cudaStream_t s);
 
-// Log decays in base 2.  exp2 of anything below -200 is 0 in fp32, so clamping there changes no
-// result, keeps -inf (a reset) finite, and bounds a chunk's sum by 12,800.
-constexpr float kMinLog2 = -200.f;
-__device__ __forceinline__ double log2_decay(float g) {
-  const double x = (double)g * 1.4426950408889634;
-  return x < (double)kMinLog2 ? (double)kMinLog2 : x;     // NaN stays NaN
+// Log decays in base 2 as 64-bit fixed point, 32 bits of fraction: sums and differences are exact,
+// so the weight between two tokens keeps fp32 accuracy however large the sums before them are (an
+// fp32 sum of a few thousand would lose 2^-12 of it), and 2^x splits into its integer word and
+// its fraction word for nothing.  2^x below -200 is 0 in fp32, so clamping there changes no
+// result, keeps -inf (a reset) finite and bounds a chunk's sum by 12,800.
+__device__ __forceinline__ long long fixed_log2(float g) {
+  return __double2ll_rn((double)fmaxf(g, -140.f) * 6196328018.8645515);   // log2(e) 2^32
 }
-// A sum G is summed in fp64 and held as two floats, hi a multiple of 2^-8 and lo the rest, so
-// that the difference of two sums (hi exactly, lo to 2^-33) keeps fp32 accuracy when both are
-// large and near each other; a single fp32 sum of a few thousand would lose 2^-12 of the weight.
-__device__ __forceinline__ float2 split_sum(double G) {
-  const float hi = (float)(rint(G * 256.0) * 0.00390625);
-  return make_float2(hi, (float)(G - (double)hi));
+// 2^x, 0 below 2^-126
+__device__ __forceinline__ float exp2_fixed(long long x) {
+  const int n = (int)(x >> 32);
+  const float r = exp2f(__uint2float_rn((uint32_t)x) * 2.3283064365386963e-10f);
+  return n < -126 ? 0.f : r * __int_as_float((min(n, 126) + 127) << 23);
 }
-__device__ __forceinline__ float pair_weight(float2 a, float2 b) {     // 2^(a - b)
-  return exp2f((a.x - b.x) + (a.y - b.y));
+// Sums over the warp's tokens, two per lane (x0, x1): returns the sum up to and with the second.
+__device__ __forceinline__ long long scan_pairs(long long x0, long long x1) {
+  const int lane = threadIdx.x & 31;
+  long long sum = x0 + x1;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, sum, off);
+    if (lane >= off) sum += y;
+  }
+  return sum;
 }
 
 }  // namespace lin

@@ -36,7 +36,7 @@ struct ChunkParams {
   float *own_S, *own_X;      // [slots, H, dk, dv]: chunks' own states, then states at the borders
   float *decay;              // [slots, H]: e^{G_C}
   void *o;
-  void *dq, *dk, *dv;        // io dtype, or fp32 per-head partial sums (shared heads)
+  float *dq, *dk, *dv;       // gradients, or per-head shares of them (shared heads)
   float *dg;                 // [rows, H]
   int part_q, part_k, part_v;
   int H, Hq, Hk, Hv, ndk, ndv, g_fixed;
@@ -44,46 +44,48 @@ struct ChunkParams {
 };
 
 // Loads rows [0, len) of head `hx` of x [rows, Hx, d] into a 64 x 128 fp32 tile, zeros elsewhere.
-template <typename T>
 __device__ void load_tile(float *t, const void *x, long row0, int len, int Hx, int hx, int d) {
-  const T *src = static_cast<const T *>(x) + ((size_t)row0 * Hx + hx) * d;
+  const float *src = static_cast<const float *>(x) + ((size_t)row0 * Hx + hx) * d;
   for (int i = threadIdx.x; i < kC * 32; i += kThreads) {
     const int r = i >> 5, c = (i & 31) * 4;
     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
     if (x && r < len && c < d) {
-      const T *s = src + (size_t)r * Hx * d + c;
-      f = make_float4(to_f32(s[0]), to_f32(s[1]), to_f32(s[2]), to_f32(s[3]));
+      f = *reinterpret_cast<const float4 *>(src + (size_t)r * Hx * d + c);
     }
     *reinterpret_cast<float4 *>(t + r * kLd + c) = f;
   }
 }
 
+// A sum as two floats, hi a multiple of 2^-8 and lo the rest: the difference of two sums is
+// (hi - hi), exact, plus (lo - lo), to 2^-33.
+__device__ __forceinline__ float2 split_sum(long long G) {
+  return make_float2((float)(int)(G >> 24) * 0.00390625f,
+                     (float)(int)(G & 0xffffff) * 2.3283064365386963e-10f);
+}
+__device__ __forceinline__ float pair_weight(float2 a, float2 b) {     // 2^(a - b)
+  return exp2f((a.x - b.x) + (a.y - b.y));
+}
 // The chunk's sums G_i (hi, lo; base 2) to sG[0 .. 63], rows past len continuing the last;
 // e^{G_i} to sE and e^{G_C - G_i} to sW.  One warp; the caller synchronises.
 __device__ void chunk_gates(float2 *sG, float *sE, float *sW, const float *g, long row0, int len,
                             int H, int h, int g_fixed) {
   const int lane = threadIdx.x;
   if (lane >= 32) return;
-  double x[2];
+  long long x[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int i = 2 * lane + u;
-    x[u] = i < len ? log2_decay(g[g_fixed ? (size_t)h : (size_t)(row0 + i) * H + h]) : 0.0;
+    x[u] = i < len ? fixed_log2(g[g_fixed ? (size_t)h : (size_t)(row0 + i) * H + h]) : 0;
   }
-  double sum = x[0] + x[1];
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, sum, off);
-    if (lane >= off) sum += y;
-  }
-  const double all = __shfl_sync(0xffffffffu, sum, 31);
+  const long long sum = scan_pairs(x[0], x[1]);
+  const long long all = __shfl_sync(0xffffffffu, sum, 31);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int i = 2 * lane + u;
-    const double G = u ? sum : sum - x[1];
+    const long long G = u ? sum : sum - x[1];
     sG[i] = split_sum(G);
-    sE[i] = exp2f((float)G);
-    sW[i] = i < len ? exp2f((float)(all - G)) : 0.f;
+    sE[i] = exp2_fixed(G);
+    sW[i] = i < len ? exp2_fixed(all - G) : 0.f;
   }
 }
 
@@ -146,7 +148,6 @@ __device__ __forceinline__ int col_of(int j) {
 
 // ---------------------------------------------------------------- chunks' own states
 // blockIdx: (slot, head, direction); direction 1: own_X from q, dO with weights e^{G_i}.
-template <typename T>
 __global__ void __launch_bounds__(kThreads) lin_local_kernel(const ChunkParams p) {
   extern __shared__ __align__(16) float sm[];
   float *sY = sm, *sZ = sm + kTile;
@@ -157,8 +158,8 @@ __global__ void __launch_bounds__(kThreads) lin_local_kernel(const ChunkParams p
   const int h = blockIdx.y, back = blockIdx.z;
   chunk_gates(sG, sE, sW, p.g, u.row0, u.len, p.H, h, p.g_fixed);
   const int Hy = back ? p.Hq : p.Hk, Hz = back ? p.H : p.Hv;
-  load_tile<T>(sY, back ? p.q : p.k, u.row0, u.len, Hy, h * Hy / p.H, p.ndk);
-  load_tile<T>(sZ, back ? p.dO : p.v, u.row0, u.len, Hz, h * Hz / p.H, p.ndv);
+  load_tile(sY, back ? p.q : p.k, u.row0, u.len, Hy, h * Hy / p.H, p.ndk);
+  load_tile(sZ, back ? p.dO : p.v, u.row0, u.len, Hz, h * Hz / p.H, p.ndv);
   __syncthreads();
   const float *w = back ? sE : sW;
   for (int i = threadIdx.x; i < kC * 32; i += kThreads) {
@@ -258,7 +259,6 @@ __device__ __forceinline__ void store_scores(float *P, const float (&acc)[4][4],
 }
 
 // ---------------------------------------------------------------- outputs
-template <typename T>
 __global__ void __launch_bounds__(kThreads) lin_out_kernel(const ChunkParams p) {
   extern __shared__ __align__(16) float sm[];
   float *sQ = sm, *sK = sQ + kTile, *sV = sK + kTile, *sP = sV + kTile;
@@ -268,9 +268,9 @@ __global__ void __launch_bounds__(kThreads) lin_out_kernel(const ChunkParams p) 
   if (!find_piece(p.slots, blockIdx.x, u)) return;
   const int h = blockIdx.y, ty = threadIdx.x >> 4;
   chunk_gates(sG, sE, sW, p.g, u.row0, u.len, p.H, h, p.g_fixed);
-  load_tile<T>(sQ, p.q, u.row0, u.len, p.Hq, h * p.Hq / p.H, p.ndk);
-  load_tile<T>(sK, p.k, u.row0, u.len, p.Hk, h * p.Hk / p.H, p.ndk);
-  load_tile<T>(sV, p.v, u.row0, u.len, p.Hv, h * p.Hv / p.H, p.ndv);
+  load_tile(sQ, p.q, u.row0, u.len, p.Hq, h * p.Hq / p.H, p.ndk);
+  load_tile(sK, p.k, u.row0, u.len, p.Hk, h * p.Hk / p.H, p.ndk);
+  load_tile(sV, p.v, u.row0, u.len, p.Hv, h * p.Hv / p.H, p.ndv);
   __syncthreads();
   {
     float acc[4][4];
@@ -296,18 +296,16 @@ __global__ void __launch_bounds__(kThreads) lin_out_kernel(const ChunkParams p) 
   for (int i = 0; i < 4; ++i) {
     const int r = 4 * ty + i;
     if (r >= u.len) continue;
-    T *o = static_cast<T *>(p.o) + ((size_t)(u.row0 + r) * p.H + h) * p.ndv;
+    float *o = static_cast<float *>(p.o) + ((size_t)(u.row0 + r) * p.H + h) * p.ndv;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (col_of<false>(j) < p.ndv) o[col_of<false>(j)] = from_f32<T>(acc[i][j]);
+      if (col_of<false>(j) < p.ndv) o[col_of<false>(j)] = acc[i][j];
   }
 }
 
 // ---------------------------------------------------------------- gradients
-// Writes one row-block gradient in the io dtype, or as this head's fp32 partial sum; returns
-// nothing.  Columns of an NC product.
-template <typename T, bool BKC>
-__device__ __forceinline__ void store_grad(void *out, int part, const float (&acc)[4][8], const Piece &u,
+// Writes one gradient, or this head's share of it (part).  Columns of an NC product.
+__device__ __forceinline__ void store_grad(float *out, int part, const float (&acc)[4][8], const Piece &u,
                                            int Hx, int H, int h, int d) {
   const int ty = threadIdx.x >> 4;
 #pragma unroll
@@ -318,10 +316,9 @@ __device__ __forceinline__ void store_grad(void *out, int part, const float (&ac
                             : ((size_t)(u.row0 + r) * Hx + h) * d;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int c = col_of<BKC>(j);
+      const int c = col_of<false>(j);
       if (c >= d) continue;
-      if (part) static_cast<float *>(out)[off + c] = acc[i][j];
-      else static_cast<T *>(out)[off + c] = from_f32<T>(acc[i][j]);
+      out[off + c] = acc[i][j];
     }
   }
 }
@@ -339,7 +336,6 @@ __device__ __forceinline__ void row_dots(float *s, const float *X, const float (
   }
 }
 
-template <typename T>
 __global__ void __launch_bounds__(kThreads) lin_grad_kernel(const ChunkParams p) {
   extern __shared__ __align__(16) float sm[];
   float *sQ = sm, *sK = sQ + kTile, *sV = sK + kTile, *sD = sV + kTile, *sS = sD + kTile;
@@ -353,10 +349,10 @@ __global__ void __launch_bounds__(kThreads) lin_grad_kernel(const ChunkParams p)
   const int dk = p.ndk, dv = p.ndv;
   chunk_gates(sG, sE, sW, p.g, u.row0, u.len, p.H, h, p.g_fixed);
   if (tid < kC) sR[tid] = 0.f;
-  load_tile<T>(sQ, p.q, u.row0, u.len, p.Hq, h * p.Hq / p.H, dk);
-  load_tile<T>(sK, p.k, u.row0, u.len, p.Hk, h * p.Hk / p.H, dk);
-  load_tile<T>(sV, p.v, u.row0, u.len, p.Hv, h * p.Hv / p.H, dv);
-  load_tile<T>(sD, p.dO, u.row0, u.len, p.H, h, dv);
+  load_tile(sQ, p.q, u.row0, u.len, p.Hq, h * p.Hq / p.H, dk);
+  load_tile(sK, p.k, u.row0, u.len, p.Hk, h * p.Hk / p.H, dk);
+  load_tile(sV, p.v, u.row0, u.len, p.Hv, h * p.Hv / p.H, dv);
+  load_tile(sD, p.dO, u.row0, u.len, p.H, h, dv);
   const size_t elems = (size_t)dk * dv;
   const float *S = p.own_S + ((size_t)blockIdx.x * p.H + h) * elems;
   const float *S_out = p.own_S + ((size_t)(blockIdx.x + 1) * p.H + h) * elems;
@@ -400,7 +396,7 @@ __global__ void __launch_bounds__(kThreads) lin_grad_kernel(const ChunkParams p)
   }
   mm<8, true, false>(acc, sP, kLdP, sK, kLd, kC, 8);
   row_dots(sR, sQ, acc, 1.f);
-  store_grad<T, false>(p.dq, p.part_q, acc, u, p.Hq, p.H, h, dk);
+  store_grad(p.dq, p.part_q, acc, u, p.Hq, p.H, h, dk);
   // dk: X v_j likewise
   zero(acc);
   for (int m0 = 0; m0 < dk; m0 += 64) {
@@ -425,7 +421,7 @@ __global__ void __launch_bounds__(kThreads) lin_grad_kernel(const ChunkParams p)
   }
   mm<8, false, false>(acc, sP, kLdP, sQ, kLd, kC, 8);
   row_dots(sR, sK, acc, -1.f);
-  store_grad<T, false>(p.dk, p.part_k, acc, u, p.Hk, p.H, h, dk);
+  store_grad(p.dk, p.part_k, acc, u, p.Hk, p.H, h, dk);
   __syncthreads();                            // the scores' gradients and sR are done
   {
     float sc[4][4];
@@ -446,7 +442,7 @@ __global__ void __launch_bounds__(kThreads) lin_grad_kernel(const ChunkParams p)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] *= sW[4 * ty + i];
   mm<8, false, false>(acc, sP, kLdP, sD, kLd, kC, 8);
-  store_grad<T, false>(p.dv, p.part_v, acc, u, p.Hv, p.H, h, dv);
+  store_grad(p.dv, p.part_v, acc, u, p.Hv, p.H, h, dv);
   // dg: suffix sums within the chunk (two rows per lane, from the end)
   if (tid < 32) {
     float all = 0.f;
@@ -532,8 +528,7 @@ bool set_smem(K kern, int bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
 }
 
-template <typename T>
-int run(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
+int run_simt(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
   const SimtLayout L = layout(a.cu != nullptr, a.N, a.T, a.B, a.H, a.Hq, a.Hk, a.Hv, a.dk, a.dv,
                               a.g_fixed, b != nullptr);
   ChunkParams p = {};
@@ -551,18 +546,18 @@ int run(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
   if (b) {
     p.dO = b->dO;
     p.part_q = a.Hq < a.H; p.part_k = a.Hk < a.H; p.part_v = a.Hv < a.H;
-    p.dq = p.part_q ? static_cast<void *>(a.ws + L.pq) : b->dq;
-    p.dk = p.part_k ? static_cast<void *>(a.ws + L.pk) : b->dk;
-    p.dv = p.part_v ? static_cast<void *>(a.ws + L.pv) : b->dv;
+    p.dq = p.part_q ? reinterpret_cast<float *>(a.ws + L.pq) : static_cast<float *>(b->dq);
+    p.dk = p.part_k ? reinterpret_cast<float *>(a.ws + L.pk) : static_cast<float *>(b->dk);
+    p.dv = p.part_v ? reinterpret_cast<float *>(a.ws + L.pv) : static_cast<float *>(b->dv);
     p.dg = a.g_fixed ? reinterpret_cast<float *>(a.ws + L.dg) : b->dg;
   }
   const dim3 grid((unsigned)L.slots, (unsigned)a.H, b ? 2 : 1);
   const int elems = a.dk * a.dv;
   const dim3 scan((unsigned)a.N, (unsigned)a.H, (unsigned)((elems / 4 + 127) / 128));
-  if (!set_smem(lin_local_kernel<T>, kLocalSmem) || !set_smem(lin_out_kernel<T>, kOutSmem) ||
-      !set_smem(lin_grad_kernel<T>, kGradSmem))
+  if (!set_smem(lin_local_kernel, kLocalSmem) || !set_smem(lin_out_kernel, kOutSmem) ||
+      !set_smem(lin_grad_kernel, kGradSmem))
     return CKDA_ERR_CUDA;
-  if (grid.x > 0) lin_local_kernel<T><<<grid, kThreads, kLocalSmem, s>>>(p);
+  if (grid.x > 0) lin_local_kernel<<<grid, kThreads, kLocalSmem, s>>>(p);
   ScanParams f{p.own_S, p.decay, a.S0, a.S_T, a.H, elems, 0, b != nullptr, p.slots};
   lin_scan_kernel<<<scan, 128, 0, s>>>(f);
   if (b) {
@@ -570,13 +565,13 @@ int run(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
     lin_scan_kernel<<<scan, 128, 0, s>>>(r);
   }
   const dim3 flat(grid.x, grid.y);
-  if (grid.x > 0 && !b && a.o) lin_out_kernel<T><<<flat, kThreads, kOutSmem, s>>>(p);
+  if (grid.x > 0 && !b && a.o) lin_out_kernel<<<flat, kThreads, kOutSmem, s>>>(p);
   if (b) {
     const long rows = (long)a.B * a.T;
-    if (grid.x > 0) lin_grad_kernel<T><<<flat, kThreads, kGradSmem, s>>>(p);
-    if (p.part_q) launch_share(p.dq, b->dq, rows, a.H, a.Hq, a.dk, sizeof(T) == 2, a.status, s);
-    if (p.part_k) launch_share(p.dk, b->dk, rows, a.H, a.Hk, a.dk, sizeof(T) == 2, a.status, s);
-    if (p.part_v) launch_share(p.dv, b->dv, rows, a.H, a.Hv, a.dv, sizeof(T) == 2, a.status, s);
+    if (grid.x > 0) lin_grad_kernel<<<flat, kThreads, kGradSmem, s>>>(p);
+    if (p.part_q) launch_share(p.dq, b->dq, rows, a.H, a.Hq, a.dk, false, a.status, s);
+    if (p.part_k) launch_share(p.dk, b->dk, rows, a.H, a.Hk, a.dk, false, a.status, s);
+    if (p.part_v) launch_share(p.dv, b->dv, rows, a.H, a.Hv, a.dv, false, a.status, s);
     if (a.g_fixed) launch_fixed(p.dg, b->dg, rows, a.H, a.status, s);
   }
   return cudaGetLastError() == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
@@ -644,10 +639,10 @@ size_t linattn_bwd_workspace(const LinArgs &a, bool packed) {
   return lin::layout(packed, a.N, a.T, a.B, a.H, a.Hq, a.Hk, a.Hv, a.dk, a.dv, a.g_fixed, true).total;
 }
 int launch_linattn_fwd(const LinArgs &a, cudaStream_t s) {
-  return a.io_dtype == CKDA_BF16 ? lin::launch_tc(a, nullptr, s) : lin::run<float>(a, nullptr, s);
+  return a.io_dtype == CKDA_BF16 ? lin::launch_tc(a, nullptr, s) : lin::run_simt(a, nullptr, s);
 }
 int launch_linattn_bwd(const LinBwdArgs &b, cudaStream_t s) {
-  return b.f.io_dtype == CKDA_BF16 ? lin::launch_tc(b.f, &b, s) : lin::run<float>(b.f, &b, s);
+  return b.f.io_dtype == CKDA_BF16 ? lin::launch_tc(b.f, &b, s) : lin::run_simt(b.f, &b, s);
 }
 
 }  // namespace ckda

@@ -70,6 +70,9 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+}
 // two fp32 values rounded to bf16 (first in the low half), and back
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -99,10 +102,10 @@ struct Cfg {
   static constexpr uint32_t offTok = kStages * kStage;                        // tokf Z, three terms
   static constexpr uint32_t offP = offTok + 3 * kTileB;
   static constexpr uint32_t offGate = offP + kPBufs * kPanel;
-  static constexpr uint32_t kGate = 5 * 64 * 4 + 16;                          // one stage's decays
+  static constexpr uint32_t kGate = 6 * 64 * 4 + 16;                          // one stage's decays
   static constexpr uint32_t offDot = offGate + kStages * kGate;               // kGrad: 2 x 64 + 2 x 2 x 4 x 32 floats
   static constexpr uint32_t offBar = offDot + (KIND == kGrad ? 2 * 64 * 4 + 512 * 4 : 0);
-  static constexpr int kBars = 3 * kStages + 16;
+  static constexpr int kBars = 3 * kStages + 19;
   static constexpr uint32_t kSmem = offBar + kBars * 8 + 64 + 1024;           // + slack to align
   // TMEM columns
   static constexpr uint32_t cSc = 0, cSc2 = 64, cO2 = KIND == kGrad ? 0 : 64;
@@ -191,11 +194,11 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
   uint64_t *b_full = bars, *b_empty = bars + C::kStages, *b_gate = bars + 2 * C::kStages;
   uint64_t *bx = bars + 3 * C::kStages;
   uint64_t *b_zeroed = bx, *b_sc = bx + 1, *b_p = bx + 2, *b_s = bx + 3, *b_o = bx + 4 /* 2 */,
-           *b_ofree = bx + 6, *b_w = bx + 7, *b_d = bx + 8, *b_dfree = bx + 9, *b_drain = bx + 10,
-           *b_red = bx + 11 /* 2 */;
-  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bx + 13);
-  volatile int *s_abort = reinterpret_cast<volatile int *>(bx + 14);
-  volatile int *s_issued = reinterpret_cast<volatile int *>(bx + 15);
+           *b_ofree = bx + 6, *b_d = bx + 7, *b_dfree = bx + 8, *b_drain = bx + 9, *b_red = bx + 10 /* 2 */,
+           *b_w = bx + 12 /* 2 */, *b_wfree = bx + 14 /* 2 */;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bx + 16);
+  volatile int *s_abort = reinterpret_cast<volatile int *>(bx + 17);
+  volatile int *s_issued = reinterpret_cast<volatile int *>(bx + 18);
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -211,7 +214,10 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     mbar_init(b_o, 1);
     mbar_init(b_o + 1, 1);
     mbar_init(b_ofree, 8);
-    mbar_init(b_w, 4);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(b_w + s, 4);
+      mbar_init(b_wfree + s, 1);
+    }
     mbar_init(b_d, 1);
     mbar_init(b_dfree, 8);
     mbar_init(b_drain, 1);
@@ -235,16 +241,20 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
   auto chunk_at = [&](int c) { return rev ? nc - 1 - c : c; };
   auto rows_of = [&](int ci) { return min(kC, u.len - ci * kC); };
   auto gates = [&](int st) { return reinterpret_cast<float *>(sm + C::offGate + st * C::kGate); };
-  // gates: [0] G as (hi, lo) pairs x 64, [128] rowf, [192] tokf, [256] crossf, [320] e^{G_C}
+  // gates (floats): [0] rowf, [64] tokf, [128] rowa, [192] colb, [256] G (64-bit fixed point),
+  // [384] e^{G_C}, [385] whether P_ij is formed as rowa_i (colb_j x_i . y_j)
 
   if (warp == 10) {
     // ---------------------------------------------------------------- loads and decays
     const int px = (ps.dx + 63) / 64, pz = (ps.dz + 63) / 64;
     const bool has_w = KIND == kGrad && ps.iw >= 0;
     const uint32_t bytes = kPanel * ((KIND != kStates ? px : 0) + px + pz + (has_w ? pz : 0));
-    const int hx = KIND != kStates ? h * ps.hx / p.H : 0, hy = h * ps.hy / p.H, hz = h * ps.hz / p.H,
-              hw = has_w ? h * ps.hw / p.H : 0;
-    double whole = 0.0;
+    // lane 2 t + q loads panel q of tile t (Y Z, X Y Z, or X Y Z W)
+    const int tile = (lane >> 1) + (KIND == kStates ? 1 : 0);
+    const bool load = lane < 2 * C::kTiles && (lane & 1) < (tile < 2 ? px : pz) && (tile < 3 || has_w);
+    const int map = tile == 0 ? ps.ix : tile == 1 ? ps.iy : tile == 2 ? ps.iz : ps.iw;
+    const int head = h * (tile == 0 ? ps.hx : tile == 1 ? ps.hy : tile == 2 ? ps.hz : ps.hw) / p.H;
+    long long whole = 0, all = 0;
     float gv[2];
     auto load_g = [&](int c) {
       const int ci = chunk_at(c), len = rows_of(ci);
@@ -258,52 +268,60 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     for (int c = 0; c < nc; ++c) {
       const int st = c % C::kStages, ci = chunk_at(c), len = rows_of(ci);
       if (c >= C::kStages && !warp_wait(b_empty + st, c / C::kStages - 1, s_abort, p.status)) break;
+      // one lane per panel
       if (lane == 0) {
-        uint8_t *dst = sm + st * C::kStage;
-        const int row = (int)(u.row0 + ci * kC);
-        // (no dO: its loads start past the tensor's end, where TMA reads 0)
-        auto row_in = [&](int map) { return map == 3 && p.no_dO ? 1 << 30 : row; };
         mbar_arrive_expect_tx(b_full + st, bytes);
-        for (int q = 0; q < px; ++q) {
-          if (KIND != kStates) tma_load_3d(dst + C::oX + q * kPanel, &p.maps[ps.ix], b_full + st, 64 * q, hx, row_in(ps.ix));
-          tma_load_3d(dst + C::oY + q * kPanel, &p.maps[ps.iy], b_full + st, 64 * q, hy, row_in(ps.iy));
-        }
-        for (int q = 0; q < pz; ++q) {
-          tma_load_3d(dst + C::oZ + q * kPanel, &p.maps[ps.iz], b_full + st, 64 * q, hz, row_in(ps.iz));
-          if (has_w) tma_load_3d(dst + C::oW + q * kPanel, &p.maps[ps.iw], b_full + st, 64 * q, hw, row_in(ps.iw));
-        }
         *s_issued = c + 1;
       }
-      const double x0 = 2 * lane < len ? log2_decay(gv[0]) : 0.0;
-      const double x1 = 2 * lane + 1 < len ? log2_decay(gv[1]) : 0.0;
-      if (c + 1 < nc) load_g(c + 1);
-      double sum = x0 + x1;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, sum, off);
-        if (lane >= off) sum += y;
+      __syncwarp();
+      if (load) {
+        // (no dO: its loads start past the tensor's end, where TMA reads 0)
+        const int row = map == 3 && p.no_dO ? 1 << 30 : (int)(u.row0 + ci * kC);
+        tma_load_3d(sm + st * C::kStage + lane * kPanel, &p.maps[map], b_full + st, 64 * (lane & 1), head, row);
       }
-      const double all = __shfl_sync(0xffffffffu, sum, 31), mid = __shfl_sync(0xffffffffu, sum, 15);
-      whole += all;
-      float *gt = gates(st);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = 2 * lane + e;
-        const double G = e ? sum : sum - x1;
-        reinterpret_cast<float2 *>(gt)[i] = split_sum(G);
-        const float since = exp2f((float)G), until = exp2f((float)(all - G));
-        gt[128 + i] = rev ? until : since;
-        gt[192 + i] = i < len ? (rev ? since : until) : 0.f;
-        gt[256 + i] = exp2f((float)(i < 32 ? mid - G : G - mid));   // to / from token 31
+      // (fixed decays: a stage that held as many rows holds the same decays)
+      if (!p.g_fixed || c < C::kStages || rows_of(chunk_at(c - C::kStages)) != len) {
+        const long long x0 = 2 * lane < len ? fixed_log2(gv[0]) : 0;
+        const long long x1 = 2 * lane + 1 < len ? fixed_log2(gv[1]) : 0;
+        if (c + 1 < nc) load_g(c + 1);
+        const long long sum = scan_pairs(x0, x1);
+        all = __shfl_sync(0xffffffffu, sum, 31);
+        const long long mid = __shfl_sync(0xffffffffu, sum, 15);      // up to token 31
+        // weights as one product about token 31 while neither half decays by more than 2^-60
+        const long long lim = 60ll << 32;
+        const bool plain = mid >= -lim && all - mid >= -lim;
+        float *gt = gates(st);
+        float2 rf, tf, ra, cb;
+        auto one = [&](long long G, int i, float &r, float &t, float &a, float &b) {
+          const float since = exp2_fixed(G), until = exp2_fixed(all - G);
+          r = rev ? until : since;
+          t = i < len ? (rev ? since : until) : 0.f;
+          if (KIND == kStates) return;
+          const float up = exp2_fixed(G - mid), down = exp2_fixed(mid - G);
+          a = plain ? (rev ? down : up) : 1.f;
+          b = plain ? (rev ? up : down) : i < 32 ? down : up;   // (to / from token 31)
+        };
+        one(sum - x1, 2 * lane, rf.x, tf.x, ra.x, cb.x);
+        one(sum, 2 * lane + 1, rf.y, tf.y, ra.y, cb.y);
+        reinterpret_cast<float2 *>(gt)[lane] = rf;
+        reinterpret_cast<float2 *>(gt + 64)[lane] = tf;
+        if (KIND != kStates) {
+          reinterpret_cast<float2 *>(gt + 128)[lane] = ra;
+          reinterpret_cast<float2 *>(gt + 192)[lane] = cb;
+          reinterpret_cast<longlong2 *>(gt + 256)[lane] = make_longlong2(sum - x1, sum);
+        }
+        if (lane == 0) {
+          gt[384] = exp2_fixed(all);
+          gt[385] = plain ? 1.f : 0.f;
+        }
       }
-      if (lane == 0) gt[320] = exp2f((float)all);
+      whole = max(whole + all, -(1ll << 52));
       __syncwarp();
       if (lane == 0) mbar_arrive(b_gate + st);
     }
     // (a backward walk's segments but the last belong to the forward walk too, which writes theirs)
     if (KIND == kStates && lane == 0 && (!rev || u.piece == u.pieces - 1)) {
-      const float2 w = split_sum(whole);
-      ps.decay[(size_t)blockIdx.x * p.H + h] = exp2f(w.x) * exp2f(w.y);
+      ps.decay[(size_t)blockIdx.x * p.H + h] = exp2_fixed(whole);
     }
   } else if (warp == 11) {
     // ---------------------------------------------------------------- MMA issue
@@ -335,21 +353,24 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
           }
         mma_commit(b_sc);
       };
-      auto state = [&](int c) {
+      // D from the tokens of one half of the chunk
+      auto state = [&](int c, int half) {
         const uint32_t st = (c % C::kStages) * C::kStage;
         const uint64_t dy = mnmajor(st + C::oY);
 #pragma unroll
         for (int t = 0; t < 3; ++t) {
           const uint64_t dw = mnmajor(C::offTok + t * kTileB);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16_ss(tmem + C::cD, dw + 128 * kk, dy + 128 * kk, id_d, t + kk > 0);
+          for (int kk = 2 * half; kk < 2 * half + 2; ++kk)
+            mma_bf16_ss(tmem + C::cD, dw + 128 * kk, dy + 128 * kk, id_d, half + t + (kk & 1) > 0);
         }
-        mma_commit(b_d);
+        mma_commit(b_wfree + half);
+        if (half) mma_commit(b_d);
       };
       auto out1 = [&](int c) {
         const uint32_t st = (c % C::kStages) * C::kStage;
-        for (int t = 0; t < C::kTerms; ++t)
+        const int terms = KIND == kGrad && ps.iw >= 0 ? C::kTerms : 1;
+        for (int t = 0; t < terms; ++t)
           for (int kk = 0; kk < kx; ++kk)
             mma_bf16_ts(tmem + C::cO1, tmem + C::cM + 64 * t + 8 * kk,
                         kmajor(st + C::oX + (kk >> 2) * kPanel) + 2 * (kk & 3), id_sc, t + kk > 0);
@@ -368,26 +389,30 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       }
       for (int c = 0; ok && c < nc; ++c) {
         if (KIND != kOut && !(ok = tiles(c))) break;
+        if (KIND == kGrad) {
+          if (!(ok = c == 0 || need(b_ofree, c - 1))) break;
+          tc_fence_after();
+          scores(c);
+        }
         if (!(ok = need(b_w, c) && (c == 0 || need(b_dfree, c - 1)))) break;
         tc_fence_after();
-        state(c);
+        state(c, 0);
         if (KIND == kOut) {
           if (!(ok = need(b_p, c) && (c + 1 >= nc || tiles(c + 1)))) break;
           tc_fence_after();
           if (c + 1 < nc) scores(c + 1);
-          if (!(ok = need(b_s, c) && (c == 0 || need(b_ofree, c - 1)))) break;
+        }
+        if (!(ok = need(b_w + 1, c))) break;
+        tc_fence_after();
+        state(c, 1);
+        if (KIND != kStates) {
+          if (!(ok = need(b_s, c) && (KIND == kGrad || c == 0 || need(b_ofree, c - 1)))) break;
           tc_fence_after();
           out1(c);
-          out2(c);
-        } else if (KIND == kGrad) {
-          if (!(ok = c == 0 || need(b_ofree, c - 1))) break;
-          tc_fence_after();
-          scores(c);
-          if (!(ok = need(b_s, c))) break;
-          tc_fence_after();
-          out1(c);
-          if (!(ok = need(b_p, c))) break;
-          tc_fence_after();
+          if (KIND == kGrad) {
+            if (!(ok = need(b_p, c))) break;
+            tc_fence_after();
+          }
           out2(c);
         }
         mma_commit(b_empty + c % C::kStages);
@@ -399,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     __syncwarp();
   } else if (warp >= 12) {
     // ---------------------------------------------------------------- tokf Z in three bf16 terms
-    const int t = tid - 12 * 32, n16 = (ps.dz + 63) / 64 * (int)(kPanel / 16);
+    const int t = tid - 12 * 32, pz = (ps.dz + 63) / 64;
     for (int c = 0; c < nc; ++c) {
       const int st = c % C::kStages, len = rows_of(chunk_at(c));
       uint8_t *base = sm + st * C::kStage;
@@ -414,36 +439,42 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         if (!warp_wait(b_zeroed, 0, s_abort, p.status)) break;
       }
       if (!warp_wait(b_gate + st, c / C::kStages, s_abort, p.status)) break;
-      if (c > 0 && !warp_wait(b_d, c - 1, s_abort, p.status)) break;
-      const float *tokf = gates(st) + 192;
+      const float *tokf = gates(st) + 64;
       const uint4 *src = reinterpret_cast<const uint4 *>(base + C::oZ);
       uint4 *dst = reinterpret_cast<uint4 *>(sm + C::offTok);
-#pragma unroll 2
-      for (int i = t; i < n16; i += 128) {
-        const float w = tokf[i >> 3 & 63];
-        const uint4 z = src[i];
-        uint4 r[3];
-        const uint32_t *zi = &z.x;
-        uint32_t *r0 = &r[0].x, *r1 = &r[1].x, *r2 = &r[2].x;
+      bool ok = true;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        if (c > 0 && !(ok = warp_wait(b_wfree + half, c - 1, s_abort, p.status))) break;
+        for (int q = 0; q < pz; ++q) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float a = lo_f32(zi[e]) * w, b = hi_f32(zi[e]) * w;
-          r0[e] = pack_bf16(a, b);
-          a -= lo_f32(r0[e]); b -= hi_f32(r0[e]);
-          r1[e] = pack_bf16(a, b);
-          a -= lo_f32(r1[e]); b -= hi_f32(r1[e]);
-          r2[e] = pack_bf16(a, b);
+          for (int v = 0; v < 2; ++v) {
+            const int i = 512 * q + 256 * half + 128 * v + t;
+            const float w = tokf[i >> 3 & 63];
+            const uint4 z = src[i];
+            uint4 r[3];
+            const uint32_t *zi = &z.x;
+            uint32_t *r0 = &r[0].x, *r1 = &r[1].x, *r2 = &r[2].x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float a = lo_f32(zi[e]) * w, b = hi_f32(zi[e]) * w;
+              r0[e] = pack_bf16(a, b);
+              a -= lo_f32(r0[e]); b -= hi_f32(r0[e]);
+              r1[e] = pack_bf16(a, b);
+              a -= lo_f32(r1[e]); b -= hi_f32(r1[e]);
+              r2[e] = pack_bf16(a, b);
+            }
+            dst[i] = r[0];
+            dst[kTileB / 16 + i] = r[1];
+            dst[2 * kTileB / 16 + i] = r[2];
+          }
         }
-        dst[i] = r[0];
-        dst[kTileB / 16 + i] = r[1];
-        dst[2 * kTileB / 16 + i] = r[2];
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_w + half);
       }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(b_w);
-        mbar_arrive(b_empty + st);
-      }
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(b_empty + st);
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- scores (warps 8, 9)
@@ -463,38 +494,56 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
           break;
         const float *gt = gates(st);
         uint8_t *P = sm + C::offP + (C::kPBufs > 1 ? (c & 1) * kPanel : 0) + row * 128;
-        const float2 me = reinterpret_cast<const float2 *>(gt)[row];
-        const float mine = gt[256 + row];
+        const bool plain = gt[385] != 0.f;
+        const float mine = gt[192 + row];
+        const long long *G = reinterpret_cast<const long long *>(gt + 256);
         float dot = 0.f;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (b != wr && b != other) continue;      // acausal
-          if (b != wr && wr == other) continue;
+#pragma unroll 1
+        for (int b = wr == other ? wr : 0; b < (wr == other ? wr + 1 : 2); ++b) {
+          if (!plain && b == wr) {                  // every weight from its own difference of sums
+            const long long me = G[row];
+#pragma unroll 1
+            for (int j = 0; j < 32; ++j) {
+              uint32_t s1, w1 = 0;
+              tmem_ld1(lanes + C::cSc + 32 * b + j, s1);
+              if (dots) tmem_ld1(lanes + C::cSc2 + 32 * b + j, w1);
+              tmem_wait_ld();
+              const long long o = G[32 * b + j];
+              const float x = (rev ? j >= lane : j <= lane) ? __uint_as_float(s1) * exp2_fixed(rev ? o - me : me - o) : 0.f;
+              if (dots && j != lane) dot = (rev ? j > lane : j < lane) ? fmaf(x, __uint_as_float(w1), dot) : dot;
+              *reinterpret_cast<__nv_bfloat16 *>(P + (((4 * b + j / 8) ^ (row & 7)) << 4) + 2 * (j & 7)) =
+                  __float2bfloat16_rn(x);
+            }
+            continue;
+          }
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const int j0 = 32 * b + 16 * half;
-            uint32_t s[16];
+            uint32_t s[16], w2[16];
             tmem_ld16(lanes + C::cSc + j0, s);
-            uint32_t w2[16];
             if (dots) tmem_ld16(lanes + C::cSc2 + j0, w2);
+            float f[16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(f + 4 * j) = *reinterpret_cast<const float4 *>(gt + 192 + j0 + 4 * j);
+            if (!plain) {                           // (off the diagonal block: through token 31)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) f[j] *= mine;
+            }
             tmem_wait_ld();
             float v[16];
-            if (b == wr) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(s[j]) * f[j];
+            if (b == wr) {                          // the diagonal block: mask, and no diagonal in the dot
+              const uint32_t m = (rev ? ~0u << lane : ~0u >> (31 - lane)) >> (16 * half);
+              const uint32_t m1 = m & ~((1u << lane) >> (16 * half));
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const int col = 16 * half + j;      // within the diagonal block
-                const float2 o = reinterpret_cast<const float2 *>(gt)[j0 + j];
-                const float wt = rev ? pair_weight(o, me) : pair_weight(me, o);
-                v[j] = (rev ? col >= lane : col <= lane) ? __uint_as_float(s[j]) * wt : 0.f;
-                if (dots && col != lane)            // (the diagonal's share cancels in q.dq - k.dk)
-                  dot = (rev ? col > lane : col < lane) ? fmaf(v[j], __uint_as_float(w2[j]), dot) : dot;
+                v[j] = m & (1u << j) ? v[j] : 0.f;
+                if (dots) dot = m1 & (1u << j) ? fmaf(v[j], __uint_as_float(w2[j]), dot) : dot;
               }
-            } else {
+            } else if (dots) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                v[j] = __uint_as_float(s[j]) * (mine * gt[256 + j0 + j]);
-                if (dots) dot = fmaf(v[j], __uint_as_float(w2[j]), dot);
-              }
+              for (int j = 0; j < 16; ++j) dot = fmaf(v[j], __uint_as_float(w2[j]), dot);
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -507,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             }
           }
         }
+        dot *= gt[128 + row];
         if (dots) row_dot[(c & 1) * 64 + row] = dot;
         fence_proxy_async();
         tc_fence_before();
@@ -523,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     const int z = 32 * quad + lane;                 // this thread's value channel (TMEM lane)
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
     const bool live = z < ps.dz && 64 * hf < ps.dx;
+    const bool dots = KIND == kGrad && ps.iw >= 0;
     const int ncol = min(64, ps.dx - 64 * hf);      // state columns of this half (<= 0: none)
     float M[64];
     {
@@ -532,8 +583,16 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         else if (ps.init) src = ps.init + ((size_t)u.n * p.H + h) * p.elems;
       }
       if (src) src += (size_t)z * ps.sz + (size_t)(64 * hf) * ps.sx;
+      const bool have = src && live;
+      if (ps.sx == 1) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) M[i] = src && live && i < ncol ? src[(size_t)i * ps.sx] : 0.f;
+        for (int i = 0; i < 64; i += 4)
+          *reinterpret_cast<float4 *>(M + i) = have && i < ncol ? *reinterpret_cast<const float4 *>(src + i)
+                                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) M[i] = have && i < ncol ? src[(size_t)i * ps.sx] : 0.f;
+      }
     }
     // M as the next chunk's operand
     auto put_state = [&]() {
@@ -543,15 +602,24 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float x = M[16 * b + 2 * i], y = M[16 * b + 2 * i + 1];
+          r[0][i] = pack_bf16(x, y);
+          if constexpr (KIND == kGrad) {
+            if (!dots) continue;
 #pragma unroll
-          for (int t = 0; t < C::kTerms; ++t) {
-            r[t][i] = pack_bf16(x, y);
-            x -= lo_f32(r[t][i]);
-            y -= hi_f32(r[t][i]);
+            for (int t = 1; t < 3; ++t) {
+              x -= lo_f32(r[t - 1][i]);
+              y -= hi_f32(r[t - 1][i]);
+              r[t][i] = pack_bf16(x, y);
+            }
           }
         }
-#pragma unroll
-        for (int t = 0; t < C::kTerms; ++t) tmem_st8(lanes + C::cM + 64 * t + 32 * hf + 8 * b, r[t]);
+        tmem_st8(lanes + C::cM + 32 * hf + 8 * b, r[0]);
+        if constexpr (KIND == kGrad) {
+          if (dots) {
+            tmem_st8(lanes + C::cM + 64 + 32 * hf + 8 * b, r[1]);
+            tmem_st8(lanes + C::cM + 128 + 32 * hf + 8 * b, r[2]);
+          }
+        }
       }
       tmem_wait_st();
       tc_fence_before();
@@ -560,14 +628,13 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     };
     bool ok = true;
     if (KIND != kStates) put_state();
-    const bool dots = KIND == kGrad && ps.iw >= 0;
     float *row_dot = reinterpret_cast<float *>(sm + C::offDot);
     float *red = row_dot + 128;                     // [2][2 halves][4 quads][32]
     for (int c = 0; c < nc; ++c) {
       const int st = c % C::kStages, ci = chunk_at(c), len = rows_of(ci);
       if (!(ok = warp_wait(b_gate + st, c / C::kStages, s_abort, p.status))) break;
       const float *gt = gates(st);
-      const float a = gt[320];
+      const float a = gt[384];
       if (!(ok = warp_wait(b_d, c, s_abort, p.status))) break;
       tc_fence_after();
 #pragma unroll
@@ -586,10 +653,11 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         // (the scores' row dots; waited for here, before b_ofree lets the next phase complete)
         if (dots && !(ok = warp_wait(b_p, c, s_abort, p.status))) break;
         tc_fence_after();
-        if (c + 1 < nc) put_state();
+        if (KIND == kOut && c + 1 < nc) put_state();
         // outputs of 32 tokens, 16 at a time
         const size_t ostr = (size_t)(ps.part ? p.H : ps.ho) * ps.dz;
         const size_t o0 = (size_t)(u.row0 + ci * kC + 32 * hf) * ostr + (size_t)h * ps.dz + z;
+        const int lim = z < ps.dz && ps.out ? len - 32 * hf : 0;
         const uint8_t *wt = sm + st * C::kStage + C::oW + (z >> 6) * kPanel + (32 * hf) * 128;
         float sums = 0.f;
 #pragma unroll
@@ -603,25 +671,31 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(b_ofree);
           }
-          const float4 *rf = reinterpret_cast<const float4 *>(gt + 128 + 32 * hf + 16 * b);
-          float x[16];
+          const float4 *rf = reinterpret_cast<const float4 *>(gt + 32 * hf + 16 * b);
+          const float4 *ra = reinterpret_cast<const float4 *>(gt + 128 + 32 * hf + 16 * b);
+          float x[16], v[16];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float4 f = rf[i];
+            const float4 f = rf[i], e = ra[i];
             x[4 * i] = f.x * __uint_as_float(r1[4 * i]);
             x[4 * i + 1] = f.y * __uint_as_float(r1[4 * i + 1]);
             x[4 * i + 2] = f.z * __uint_as_float(r1[4 * i + 2]);
             x[4 * i + 3] = f.w * __uint_as_float(r1[4 * i + 3]);
+            v[4 * i] = fmaf(e.x, __uint_as_float(r2[4 * i]), x[4 * i]);
+            v[4 * i + 1] = fmaf(e.y, __uint_as_float(r2[4 * i + 1]), x[4 * i + 1]);
+            v[4 * i + 2] = fmaf(e.z, __uint_as_float(r2[4 * i + 2]), x[4 * i + 2]);
+            v[4 * i + 3] = fmaf(e.w, __uint_as_float(r2[4 * i + 3]), x[4 * i + 3]);
           }
-          if (z < ps.dz && ps.out) {
+          if (ps.part) {
+            float *o = static_cast<float *>(ps.out) + o0 + (size_t)(16 * b) * ostr;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int t = 16 * b + i;
-              if (32 * hf + t >= len) continue;
-              const float v = x[i] + __uint_as_float(r2[i]);
-              if (ps.part) static_cast<float *>(ps.out)[o0 + (size_t)t * ostr] = v;
-              else static_cast<__nv_bfloat16 *>(ps.out)[o0 + (size_t)t * ostr] = __float2bfloat16_rn(v);
-            }
+            for (int i = 0; i < 16; ++i, o += ostr)
+              if (16 * b + i < lim) *o = v[i];
+          } else {
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(ps.out) + o0 + (size_t)(16 * b) * ostr;
+#pragma unroll
+            for (int i = 0; i < 16; ++i, o += ostr)
+              if (16 * b + i < lim) *o = __float2bfloat16_rn(v[i]);
           }
           if (dots) {
 #pragma unroll
@@ -635,6 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             if ((lane >> 4) == b) sums = s;         // lane t holds token t of this half
           }
         }
+        if (KIND == kGrad && c + 1 < nc) put_state();
         if (dots) {
           float *rd = red + ((c & 1) * 2 + hf) * 128;
           rd[quad * 32 + lane] = sums;
