@@ -20,15 +20,16 @@
 // M is kept in fp32 registers.  Roundings to bf16: P, M as an operand of O1 (each 2^-9 of a
 // term in the mean, the size of the output's own rounding); tokf Z is split into three terms
 // (24 bits), so M itself carries fp32 accuracy over any length.  Where row dots are wanted
-// (decay gradients, which cancel) M goes into O1 in three terms and the scores' part of the dot
-// is summed in fp32 from unrounded scores.
+// (decay gradients, which cancel) M and P go into O1 and O2 in three terms too.
 //
-// One CTA per (segment, head), 16 warps: 0-7 state and output, 8-9 scores (TMEM lanes 0-63),
-// 10 TMA loads and decays, 11 MMA issue (one thread), 12-15 tokf Z.  The roles run the chunks
-// at their own pace through mbarriers.  A sequence may be cut into segments: a first launch
-// computes every segment's own state, an elementwise walk over a sequence's segments gives each
-// its incoming state (the decay is a scalar, so a segment's state map is one factor), and the
-// main launch runs all segments side by side.
+// One CTA per (segment, head), 20 warps: 0-3 state (176 registers a thread, 128 of them M),
+// 4-11 outputs, 12-13 scores (TMEM lanes 0-63), 14 TMA loads and decays, 15 issue of scores and
+// O1, 16-18 tokf Z, 19 issue of D and O2 (two issuers: one thread's products take 50 cycles or
+// more each to issue).  The roles run the chunks at their own pace through mbarriers.  A
+// sequence may be cut into segments: a first launch computes every segment's own state, an
+// elementwise walk over a sequence's segments gives each its incoming state (the decay is a
+// scalar, so a segment's state map is one factor), and the main launch runs all segments side
+// by side.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -70,8 +71,19 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+}
+// a * b + c on two fp32 values
+__device__ __forceinline__ uint64_t f2fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 // two fp32 values rounded to bf16 (first in the low half), and back
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -79,20 +91,31 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float lo_f32(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi_f32(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
+  float a, b;
+  f2up(v, a, b);
+  return pack_bf16(a, b);
+}
+__device__ __forceinline__ uint64_t unpack_bf16(uint32_t u) {
+  return f2pk(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ uint64_t f2bits(uint32_t a, uint32_t b) {
+  return f2pk(__uint_as_float(a), __uint_as_float(b));
+}
 
 // ------------------------------------------------------------------ shapes
 enum : int { kStates = 0, kOut = 1, kGrad = 2 };   // what a launch computes
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr uint32_t kPanel = 8192;                  // 64 tokens x 64 channels of bf16, 128-byte swizzle
 constexpr uint32_t kTileB = 2 * kPanel;            // 64 tokens x 128 channels
+// Registers a thread by role: 128 x 176 + 512 x 72 = 59,392 of the launch's 640 x 96 = 61,440.
+constexpr int kRegsState = 176, kRegsOther = 72;
 
 template <int KIND>
 struct Cfg {
   static constexpr int kTiles = KIND == kStates ? 2 : KIND == kOut ? 3 : 4;   // Y Z | X Y Z | X Y Z W
   static constexpr int kStages = KIND == kStates ? 4 : KIND == kOut ? 3 : 2;
-  static constexpr int kTerms = KIND == kGrad ? 3 : 1;                        // of M in O1
+  static constexpr int kTerms = KIND == kGrad ? 3 : 1;                        // of M and P
   static constexpr int kPBufs = KIND == kStates ? 0 : KIND == kOut ? 2 : 1;
   static constexpr uint32_t kStage = kTiles * kTileB;
   static constexpr uint32_t oX = 0;
@@ -101,16 +124,17 @@ struct Cfg {
   static constexpr uint32_t oW = oZ + kTileB;                                 // kGrad
   static constexpr uint32_t offTok = kStages * kStage;                        // tokf Z, three terms
   static constexpr uint32_t offP = offTok + 3 * kTileB;
-  static constexpr uint32_t offGate = offP + kPBufs * kPanel;
+  static constexpr uint32_t kP = kTerms * kPanel;                             // one P
+  static constexpr uint32_t offGate = offP + kPBufs * kP;
   static constexpr uint32_t kGate = 6 * 64 * 4 + 16;                          // one stage's decays
-  static constexpr uint32_t offDot = offGate + kStages * kGate;               // kGrad: 2 x 64 + 2 x 2 x 4 x 32 floats
-  static constexpr uint32_t offBar = offDot + (KIND == kGrad ? 2 * 64 * 4 + 512 * 4 : 0);
-  static constexpr int kBars = 3 * kStages + 19;
+  static constexpr uint32_t offDot = offGate + kStages * kGate;               // kGrad: 2 x 2 x 4 x 32 floats
+  static constexpr uint32_t offBar = offDot + (KIND == kGrad ? 512 * 4 : 0);
+  static constexpr int kBars = 3 * kStages + 22;
   static constexpr uint32_t kSmem = offBar + kBars * 8 + 64 + 1024;           // + slack to align
+  // tokf Z: three warps beside the other roles; alone, the eight that would write outputs
+  static constexpr int kTokWarp = KIND == kStates ? 4 : 16, kTokWarps = KIND == kStates ? 8 : 3;
   // TMEM columns
-  static constexpr uint32_t cSc = 0, cSc2 = 64, cO2 = KIND == kGrad ? 0 : 64;
-  static constexpr uint32_t cM = 128, cO1 = cM + 64 * kTerms, cD = KIND == kStates ? 0 : 384;
-  static constexpr uint32_t kCols = KIND == kStates ? 128 : 512;
+  static constexpr uint32_t cSc = 0, cO2 = 64, cM = 128, cO1 = cM + 64 * kTerms, cD = 384;
 };
 static_assert(Cfg<kOut>::kSmem <= 232448 && Cfg<kGrad>::kSmem <= 232448 && Cfg<kStates>::kSmem <= 232448,
               "shared memory");
@@ -142,21 +166,20 @@ struct Params {
   int *status;
 };
 
-constexpr uint64_t kWaitNs = 2000000000ull;
-
-// A role's wait: all lanes agree on the outcome; a wait that runs out ends every role.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {
-  const bool ok = mbar_wait_or_abort(bar, parity & 1u, kWaitNs, abort);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  *abort = 1;
-  if ((threadIdx.x & 31) == 0) set_status(status, CKDA_ERR_TIMEOUT);
-  return false;
+// Waits are bounded by a count of tries, each of which may sleep for a microsecond: some seconds,
+// after which every role ends and the status word says so.  (The code is kept small: twenty warps
+// run six roles, and their loops together have to stay in the instruction caches.)
+constexpr uint32_t kTryNs = 1000, kTries = 4000000;
+constexpr uint64_t kDrainNs = 2000000000ull;
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  uint32_t n = 0;
+  while (!mbar_try_wait_sleep(bar, parity & 1u, kTryNs))
+    if (*abort || ++n > kTries) return false;
+  return true;
 }
-__device__ __forceinline__ bool thread_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {
-  if (mbar_wait_or_abort(bar, parity & 1u, kWaitNs, abort)) return true;
+__device__ __forceinline__ void give_up(volatile int *abort, int *status) {
   *abort = 1;
   set_status(status, CKDA_ERR_TIMEOUT);
-  return false;
 }
 
 // The sum over the warp's lanes of d[t], t < 16: lane l returns token l % 16's.
@@ -193,431 +216,119 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::offBar);
   uint64_t *b_full = bars, *b_empty = bars + C::kStages, *b_gate = bars + 2 * C::kStages;
   uint64_t *bx = bars + 3 * C::kStages;
-  uint64_t *b_zeroed = bx, *b_sc = bx + 1, *b_p = bx + 2, *b_s = bx + 3, *b_o = bx + 4 /* 2 */,
-           *b_ofree = bx + 6, *b_d = bx + 7, *b_dfree = bx + 8, *b_drain = bx + 9, *b_red = bx + 10 /* 2 */,
-           *b_w = bx + 12 /* 2 */, *b_wfree = bx + 14 /* 2 */;
-  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bx + 16);
-  volatile int *s_abort = reinterpret_cast<volatile int *>(bx + 17);
-  volatile int *s_issued = reinterpret_cast<volatile int *>(bx + 18);
+  uint64_t *b_zeroed = bx, *b_sc = bx + 1, *b_p = bx + 17 /* 2 */, *b_s = bx + 3, *b_o = bx + 4 /* 2 */,
+           *b_ofree = bx + 6, *b_d = bx + 7, *b_dfree = bx + 8, *b_drain = bx + 9 /* 2 */,
+           *b_red = bx + 11 /* 2 */, *b_w = bx + 13 /* 2 */, *b_wfree = bx + 15 /* 2 */;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bx + 19);
+  volatile int *s_abort = reinterpret_cast<volatile int *>(bx + 20);
+  volatile int *s_issued = reinterpret_cast<volatile int *>(bx + 21);
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(b_full + s, 1);
-      // the MMA's commit, warps 0-7, 12-15 and the scores' two
-      mbar_init(b_empty + s, KIND == kStates ? 13 : 15);
+      // state 4, tokf Z, and the products' commit; beside outputs 8, scores 2 and a second commit
+      mbar_init(b_empty + s, 4 + C::kTokWarps + 1 + (KIND == kStates ? 0 : 11));
       mbar_init(b_gate + s, 1);
     }
-    mbar_init(b_zeroed, 4);
+    mbar_init(b_zeroed, C::kTokWarps);
     mbar_init(b_sc, 1);
-    mbar_init(b_p, 2);
-    mbar_init(b_s, 8);
-    mbar_init(b_o, 1);
-    mbar_init(b_o + 1, 1);
+    mbar_init(b_s, 4);
     mbar_init(b_ofree, 8);
+    mbar_init(b_d, 1);
+    mbar_init(b_dfree, 4);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(b_w + s, 4);
+      mbar_init(b_o + s, 2);         // O1's commit and O2's
+      mbar_init(b_p + s, 2);
+      mbar_init(b_drain + s, 1);
+      mbar_init(b_red + s, 4);
+      mbar_init(b_w + s, C::kTokWarps);
       mbar_init(b_wfree + s, 1);
     }
-    mbar_init(b_d, 1);
-    mbar_init(b_dfree, 8);
-    mbar_init(b_drain, 1);
-    mbar_init(b_red, 4);
-    mbar_init(b_red + 1, 4);
     *s_abort = 0;
     *s_issued = 0;
     mbar_fence_init();
   }
-  if (warp == 11) tmem_alloc(s_tmem, C::kCols);
+  if (warp == 15) tmem_alloc(s_tmem, 512);
   // (scores on the acausal side are never written: they stay 0)
-  for (int i = tid; i < (int)(C::kPBufs * kPanel / 16); i += kThreads)
+  for (int i = tid; i < (int)(C::kPBufs * C::kP / 16); i += kThreads)
     reinterpret_cast<uint4 *>(sm + C::offP)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;
+  constexpr uint32_t tmem = 0;    // all 512 columns are this CTA's (one CTA an SM)
 
   // chunk c of the walk: its index in the segment, its valid rows
   auto chunk_at = [&](int c) { return rev ? nc - 1 - c : c; };
   auto rows_of = [&](int ci) { return min(kC, u.len - ci * kC); };
+  // Matrix descriptors: a low word over one common high word (8-row groups 1024 bytes apart,
+  // version, 128-byte swizzle); K-major tiles, or MN-major ones of two panels.
+  const uint32_t sb = smem_u32(sm);
+  constexpr uint64_t kHi = (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32;
+  auto kmajor = [&](uint32_t at) { return kHi | (((sb + at) >> 4) | (1u << 16)); };
+  auto mnmajor = [&](uint32_t at) { return kHi | (((sb + at) >> 4) | ((kPanel >> 4) << 16)); };
   auto gates = [&](int st) { return reinterpret_cast<float *>(sm + C::offGate + st * C::kGate); };
   // gates (floats): [0] rowf, [64] tokf, [128] rowa, [192] colb, [256] G (64-bit fixed point),
   // [384] e^{G_C}, [385] whether P_ij is formed as rowa_i (colb_j x_i . y_j)
+  const bool exact = KIND == kGrad && ps.iw >= 0;   // row dots: M and P in three terms
+  // a warp's wait (all lanes agree on the outcome) and a single thread's
+  auto wait = [&](uint64_t *b, int ph) { return __all_sync(0xffffffffu, bar_wait(b, (uint32_t)ph, s_abort)) != 0; };
+  auto need = [&](uint64_t *b, int ph) { return bar_wait(b, (uint32_t)ph, s_abort); };
+  bool done = KIND == kStates && warp == 15;        // this role reached its end (15: none there)
 
-  if (warp == 10) {
-    // ---------------------------------------------------------------- loads and decays
-    const int px = (ps.dx + 63) / 64, pz = (ps.dz + 63) / 64;
-    const bool has_w = KIND == kGrad && ps.iw >= 0;
-    const uint32_t bytes = kPanel * ((KIND != kStates ? px : 0) + px + pz + (has_w ? pz : 0));
-    // lane 2 t + q loads panel q of tile t (Y Z, X Y Z, or X Y Z W)
-    const int tile = (lane >> 1) + (KIND == kStates ? 1 : 0);
-    const bool load = lane < 2 * C::kTiles && (lane & 1) < (tile < 2 ? px : pz) && (tile < 3 || has_w);
-    const int map = tile == 0 ? ps.ix : tile == 1 ? ps.iy : tile == 2 ? ps.iz : ps.iw;
-    const int head = h * (tile == 0 ? ps.hx : tile == 1 ? ps.hy : tile == 2 ? ps.hz : ps.hw) / p.H;
-    long long whole = 0, all = 0;
-    float gv[2];
-    auto load_g = [&](int c) {
-      const int ci = chunk_at(c), len = rows_of(ci);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = 2 * lane + e;
-        gv[e] = i < len ? p.g[p.g_fixed ? (size_t)h : (size_t)(u.row0 + ci * kC + i) * p.H + h] : 0.f;
-      }
-    };
-    load_g(0);
-    for (int c = 0; c < nc; ++c) {
-      const int st = c % C::kStages, ci = chunk_at(c), len = rows_of(ci);
-      if (c >= C::kStages && !warp_wait(b_empty + st, c / C::kStages - 1, s_abort, p.status)) break;
-      // one lane per panel
-      if (lane == 0) {
-        mbar_arrive_expect_tx(b_full + st, bytes);
-        *s_issued = c + 1;
-      }
-      __syncwarp();
-      if (load) {
-        // (no dO: its loads start past the tensor's end, where TMA reads 0)
-        const int row = map == 3 && p.no_dO ? 1 << 30 : (int)(u.row0 + ci * kC);
-        tma_load_3d(sm + st * C::kStage + lane * kPanel, &p.maps[map], b_full + st, 64 * (lane & 1), head, row);
-      }
-      // (fixed decays: a stage that held as many rows holds the same decays)
-      if (!p.g_fixed || c < C::kStages || rows_of(chunk_at(c - C::kStages)) != len) {
-        const long long x0 = 2 * lane < len ? fixed_log2(gv[0]) : 0;
-        const long long x1 = 2 * lane + 1 < len ? fixed_log2(gv[1]) : 0;
-        if (c + 1 < nc) load_g(c + 1);
-        const long long sum = scan_pairs(x0, x1);
-        all = __shfl_sync(0xffffffffu, sum, 31);
-        const long long mid = __shfl_sync(0xffffffffu, sum, 15);      // up to token 31
-        // weights as one product about token 31 while neither half decays by more than 2^-60
-        const long long lim = 60ll << 32;
-        const bool plain = mid >= -lim && all - mid >= -lim;
-        float *gt = gates(st);
-        float2 rf, tf, ra, cb;
-        auto one = [&](long long G, int i, float &r, float &t, float &a, float &b) {
-          const float since = exp2_fixed(G), until = exp2_fixed(all - G);
-          r = rev ? until : since;
-          t = i < len ? (rev ? since : until) : 0.f;
-          if (KIND == kStates) return;
-          const float up = exp2_fixed(G - mid), down = exp2_fixed(mid - G);
-          a = plain ? (rev ? down : up) : 1.f;
-          b = plain ? (rev ? up : down) : i < 32 ? down : up;   // (to / from token 31)
-        };
-        one(sum - x1, 2 * lane, rf.x, tf.x, ra.x, cb.x);
-        one(sum, 2 * lane + 1, rf.y, tf.y, ra.y, cb.y);
-        reinterpret_cast<float2 *>(gt)[lane] = rf;
-        reinterpret_cast<float2 *>(gt + 64)[lane] = tf;
-        if (KIND != kStates) {
-          reinterpret_cast<float2 *>(gt + 128)[lane] = ra;
-          reinterpret_cast<float2 *>(gt + 192)[lane] = cb;
-          reinterpret_cast<longlong2 *>(gt + 256)[lane] = make_longlong2(sum - x1, sum);
-        }
-        if (lane == 0) {
-          gt[384] = exp2_fixed(all);
-          gt[385] = plain ? 1.f : 0.f;
-        }
-      }
-      whole = max(whole + all, -(1ll << 52));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_gate + st);
-    }
-    // (a backward walk's segments but the last belong to the forward walk too, which writes theirs)
-    if (KIND == kStates && lane == 0 && (!rev || u.piece == u.pieces - 1)) {
-      ps.decay[(size_t)blockIdx.x * p.H + h] = exp2_fixed(whole);
-    }
-  } else if (warp == 11) {
-    // ---------------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      const uint32_t sb = smem_u32(sm);
-      const int kx = ps.dx / 16;
-      const uint32_t id_sc = idesc_bf16(128, 64, false, false), id_o2 = idesc_bf16(128, 64, true, false),
-                     id_d = idesc_bf16(128, ps.dx, true, true);
-      auto kmajor = [&](uint32_t at) { return smem_desc_sw128(sb + at, 16, 1024); };
-      auto mnmajor = [&](uint32_t at) { return smem_desc_sw128(sb + at, kPanel, 1024); };
-      // wait helper: false ends the role
-      auto need = [&](uint64_t *b, int ph) { return thread_wait(b, (uint32_t)ph, s_abort, p.status); };
-      auto tiles = [&](int c) {      // chunk c's tiles have landed (and rows past a ragged end are 0)
-        if (!need(b_full + c % C::kStages, c / C::kStages)) return false;
-        return rows_of(chunk_at(c)) == kC || need(b_zeroed, 0);
-      };
-      auto scores = [&](int c) {
-        const uint32_t st = (c % C::kStages) * C::kStage;
-        for (int kk = 0; kk < kx; ++kk) {
-          const uint32_t pan = (kk >> 2) * kPanel;
-          mma_bf16_ss(tmem + C::cSc, kmajor(st + C::oX + pan) + 2 * (kk & 3),
-                      kmajor(st + C::oY + pan) + 2 * (kk & 3), id_sc, kk > 0);
-        }
-        if (KIND == kGrad && ps.iw >= 0)
-          for (int kk = 0; kk < ps.dz / 16; ++kk) {
-            const uint32_t pan = (kk >> 2) * kPanel;
-            mma_bf16_ss(tmem + C::cSc2, kmajor(st + C::oW + pan) + 2 * (kk & 3),
-                        kmajor(st + C::oZ + pan) + 2 * (kk & 3), id_sc, kk > 0);
-          }
-        mma_commit(b_sc);
-      };
-      // D from the tokens of one half of the chunk
-      auto state = [&](int c, int half) {
-        const uint32_t st = (c % C::kStages) * C::kStage;
-        const uint64_t dy = mnmajor(st + C::oY);
-#pragma unroll
-        for (int t = 0; t < 3; ++t) {
-          const uint64_t dw = mnmajor(C::offTok + t * kTileB);
-#pragma unroll
-          for (int kk = 2 * half; kk < 2 * half + 2; ++kk)
-            mma_bf16_ss(tmem + C::cD, dw + 128 * kk, dy + 128 * kk, id_d, half + t + (kk & 1) > 0);
-        }
-        mma_commit(b_wfree + half);
-        if (half) mma_commit(b_d);
-      };
-      auto out1 = [&](int c) {
-        const uint32_t st = (c % C::kStages) * C::kStage;
-        const int terms = KIND == kGrad && ps.iw >= 0 ? C::kTerms : 1;
-        for (int t = 0; t < terms; ++t)
-          for (int kk = 0; kk < kx; ++kk)
-            mma_bf16_ts(tmem + C::cO1, tmem + C::cM + 64 * t + 8 * kk,
-                        kmajor(st + C::oX + (kk >> 2) * kPanel) + 2 * (kk & 3), id_sc, t + kk > 0);
-      };
-      auto out2 = [&](int c) {
-        const uint32_t st = (c % C::kStages) * C::kStage;
-        const uint64_t dz = mnmajor(st + C::oZ), dp = kmajor(C::offP + (C::kPBufs > 1 ? (c & 1) * kPanel : 0));
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_bf16_ss(tmem + C::cO2, dz + 128 * kk, dp + 2 * kk, id_o2, kk > 0);
-        mma_commit(b_o + (c & 1));
-      };
-      bool ok = true;
-      if (KIND == kOut) {
-        ok = tiles(0);
-        if (ok) { tc_fence_after(); scores(0); }
-      }
-      for (int c = 0; ok && c < nc; ++c) {
-        if (KIND != kOut && !(ok = tiles(c))) break;
-        if (KIND == kGrad) {
-          if (!(ok = c == 0 || need(b_ofree, c - 1))) break;
-          tc_fence_after();
-          scores(c);
-        }
-        if (!(ok = need(b_w, c) && (c == 0 || need(b_dfree, c - 1)))) break;
-        tc_fence_after();
-        state(c, 0);
-        if (KIND == kOut) {
-          if (!(ok = need(b_p, c) && (c + 1 >= nc || tiles(c + 1)))) break;
-          tc_fence_after();
-          if (c + 1 < nc) scores(c + 1);
-        }
-        if (!(ok = need(b_w + 1, c))) break;
-        tc_fence_after();
-        state(c, 1);
-        if (KIND != kStates) {
-          if (!(ok = need(b_s, c) && (KIND == kGrad || c == 0 || need(b_ofree, c - 1)))) break;
-          tc_fence_after();
-          out1(c);
-          if (KIND == kGrad) {
-            if (!(ok = need(b_p, c))) break;
-            tc_fence_after();
-          }
-          out2(c);
-        }
-        mma_commit(b_empty + c % C::kStages);
-      }
-      // every product issued has completed before the tensor memory is released
-      mma_commit(b_drain);
-      mbar_wait(b_drain, 0, kWaitNs);
-    }
-    __syncwarp();
-  } else if (warp >= 12) {
-    // ---------------------------------------------------------------- tokf Z in three bf16 terms
-    const int t = tid - 12 * 32, pz = (ps.dz + 63) / 64;
-    for (int c = 0; c < nc; ++c) {
-      const int st = c % C::kStages, len = rows_of(chunk_at(c));
-      uint8_t *base = sm + st * C::kStage;
-      if (!warp_wait(b_full + st, c / C::kStages, s_abort, p.status)) break;
-      if (len < kC) {
-        // a ragged end: the rows that follow belong to another sequence
-        for (uint32_t i = t; i < C::kStage / 16; i += 128)
-          if ((int)(i >> 3 & 63) >= len) reinterpret_cast<uint4 *>(base)[i] = make_uint4(0, 0, 0, 0);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(b_zeroed);
-        if (!warp_wait(b_zeroed, 0, s_abort, p.status)) break;
-      }
-      if (!warp_wait(b_gate + st, c / C::kStages, s_abort, p.status)) break;
-      const float *tokf = gates(st) + 64;
-      const uint4 *src = reinterpret_cast<const uint4 *>(base + C::oZ);
-      uint4 *dst = reinterpret_cast<uint4 *>(sm + C::offTok);
-      bool ok = true;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        if (c > 0 && !(ok = warp_wait(b_wfree + half, c - 1, s_abort, p.status))) break;
-        for (int q = 0; q < pz; ++q) {
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const int i = 512 * q + 256 * half + 128 * v + t;
-            const float w = tokf[i >> 3 & 63];
-            const uint4 z = src[i];
-            uint4 r[3];
-            const uint32_t *zi = &z.x;
-            uint32_t *r0 = &r[0].x, *r1 = &r[1].x, *r2 = &r[2].x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float a = lo_f32(zi[e]) * w, b = hi_f32(zi[e]) * w;
-              r0[e] = pack_bf16(a, b);
-              a -= lo_f32(r0[e]); b -= hi_f32(r0[e]);
-              r1[e] = pack_bf16(a, b);
-              a -= lo_f32(r1[e]); b -= hi_f32(r1[e]);
-              r2[e] = pack_bf16(a, b);
-            }
-            dst[i] = r[0];
-            dst[kTileB / 16 + i] = r[1];
-            dst[2 * kTileB / 16 + i] = r[2];
-          }
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(b_w + half);
-      }
-      if (!ok) break;
-      if (lane == 0) mbar_arrive(b_empty + st);
-    }
-  } else if (warp >= 8) {
-    // ---------------------------------------------------------------- scores (warps 8, 9)
-    if (KIND != kStates) {
-      const int wr = warp - 8, row = 32 * wr + lane;
-      const uint32_t lanes = tmem + ((uint32_t)(32 * wr) << 16);
-      const bool dots = KIND == kGrad && ps.iw >= 0;
-      float *row_dot = reinterpret_cast<float *>(sm + C::offDot);
-      const int other = rev ? 1 : 0;               // the column block a causal off-diagonal block has
-      for (int c = 0; wr < 2 && c < nc; ++c) {
-        const int st = c % C::kStages;
-        if (!warp_wait(b_gate + st, c / C::kStages, s_abort, p.status)) break;
-        if (!warp_wait(b_sc, c, s_abort, p.status)) break;
-        tc_fence_after();
-        // (the scores two chunks back, or one, have been read)
-        if (c >= C::kPBufs && !warp_wait(b_o + ((c - C::kPBufs) & 1), (c - C::kPBufs) >> 1, s_abort, p.status))
-          break;
-        const float *gt = gates(st);
-        uint8_t *P = sm + C::offP + (C::kPBufs > 1 ? (c & 1) * kPanel : 0) + row * 128;
-        const bool plain = gt[385] != 0.f;
-        const float mine = gt[192 + row];
-        const long long *G = reinterpret_cast<const long long *>(gt + 256);
-        float dot = 0.f;
-#pragma unroll 1
-        for (int b = wr == other ? wr : 0; b < (wr == other ? wr + 1 : 2); ++b) {
-          if (!plain && b == wr) {                  // every weight from its own difference of sums
-            const long long me = G[row];
-#pragma unroll 1
-            for (int j = 0; j < 32; ++j) {
-              uint32_t s1, w1 = 0;
-              tmem_ld1(lanes + C::cSc + 32 * b + j, s1);
-              if (dots) tmem_ld1(lanes + C::cSc2 + 32 * b + j, w1);
-              tmem_wait_ld();
-              const long long o = G[32 * b + j];
-              const float x = (rev ? j >= lane : j <= lane) ? __uint_as_float(s1) * exp2_fixed(rev ? o - me : me - o) : 0.f;
-              if (dots && j != lane) dot = (rev ? j > lane : j < lane) ? fmaf(x, __uint_as_float(w1), dot) : dot;
-              *reinterpret_cast<__nv_bfloat16 *>(P + (((4 * b + j / 8) ^ (row & 7)) << 4) + 2 * (j & 7)) =
-                  __float2bfloat16_rn(x);
-            }
-            continue;
-          }
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int j0 = 32 * b + 16 * half;
-            uint32_t s[16], w2[16];
-            tmem_ld16(lanes + C::cSc + j0, s);
-            if (dots) tmem_ld16(lanes + C::cSc2 + j0, w2);
-            float f[16];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(f + 4 * j) = *reinterpret_cast<const float4 *>(gt + 192 + j0 + 4 * j);
-            if (!plain) {                           // (off the diagonal block: through token 31)
-#pragma unroll
-              for (int j = 0; j < 16; ++j) f[j] *= mine;
-            }
-            tmem_wait_ld();
-            float v[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(s[j]) * f[j];
-            if (b == wr) {                          // the diagonal block: mask, and no diagonal in the dot
-              const uint32_t m = (rev ? ~0u << lane : ~0u >> (31 - lane)) >> (16 * half);
-              const uint32_t m1 = m & ~((1u << lane) >> (16 * half));
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                v[j] = m & (1u << j) ? v[j] : 0.f;
-                if (dots) dot = m1 & (1u << j) ? fmaf(v[j], __uint_as_float(w2[j]), dot) : dot;
-              }
-            } else if (dots) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) dot = fmaf(v[j], __uint_as_float(w2[j]), dot);
-            }
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint4 pk;
-              pk.x = pack_bf16(v[8 * q], v[8 * q + 1]);
-              pk.y = pack_bf16(v[8 * q + 2], v[8 * q + 3]);
-              pk.z = pack_bf16(v[8 * q + 4], v[8 * q + 5]);
-              pk.w = pack_bf16(v[8 * q + 6], v[8 * q + 7]);
-              *reinterpret_cast<uint4 *>(P + (((j0 / 8 + q) ^ (row & 7)) << 4)) = pk;
-            }
-          }
-        }
-        dot *= gt[128 + row];
-        if (dots) row_dot[(c & 1) * 64 + row] = dot;
-        fence_proxy_async();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(b_p);
-          mbar_arrive(b_empty + st);
-        }
-      }
-    }
-  } else {
-    // ---------------------------------------------------------------- state and output (warps 0-7)
-    const int quad = warp & 3, hf = warp >> 2;
-    const int z = 32 * quad + lane;                 // this thread's value channel (TMEM lane)
-    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-    const bool live = z < ps.dz && 64 * hf < ps.dx;
-    const bool dots = KIND == kGrad && ps.iw >= 0;
-    const int ncol = min(64, ps.dx - 64 * hf);      // state columns of this half (<= 0: none)
-    float M[64];
+  if (warp < 4) {
+    // ---------------------------------------------------------------- state (warps 0-3)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsState));
+    const int z = tid;                              // this thread's value channel (TMEM lane)
+    const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+    const bool live = z < ps.dz;
+    uint64_t M[64];                                 // x channels 2 i, 2 i + 1
     {
       const float *src = nullptr;
       if (KIND != kStates) {
         if (ps.seg_in) src = ps.seg_in + ((size_t)blockIdx.x * p.H + h) * p.elems;
         else if (ps.init) src = ps.init + ((size_t)u.n * p.H + h) * p.elems;
       }
-      if (src) src += (size_t)z * ps.sz + (size_t)(64 * hf) * ps.sx;
       const bool have = src && live;
+      if (src) src += (size_t)z * ps.sz;
       if (ps.sx == 1) {
 #pragma unroll
-        for (int i = 0; i < 64; i += 4)
-          *reinterpret_cast<float4 *>(M + i) = have && i < ncol ? *reinterpret_cast<const float4 *>(src + i)
-                                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < 64; i += 2) {
+          float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (have && 2 * i < ps.dx) f = *reinterpret_cast<const float4 *>(src + 2 * i);
+          M[i] = f2pk(f.x, f.y);
+          M[i + 1] = f2pk(f.z, f.w);
+        }
       } else {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) M[i] = have && i < ncol ? src[(size_t)i * ps.sx] : 0.f;
+        for (int i = 0; i < 64; ++i) {
+          const bool in = have && 2 * i < ps.dx;
+          M[i] = f2pk(in ? src[(size_t)(2 * i) * ps.sx] : 0.f, in ? src[(size_t)(2 * i + 1) * ps.sx] : 0.f);
+        }
       }
     }
     // M as the next chunk's operand
     auto put_state = [&]() {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
+      for (int b = 0; b < 8; ++b) {
+        if (16 * b >= ps.dx) break;
         uint32_t r[C::kTerms][8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float x = M[16 * b + 2 * i], y = M[16 * b + 2 * i + 1];
-          r[0][i] = pack_bf16(x, y);
+          r[0][i] = pack_bf16(M[8 * b + i]);
           if constexpr (KIND == kGrad) {
-            if (!dots) continue;
-#pragma unroll
-            for (int t = 1; t < 3; ++t) {
-              x -= lo_f32(r[t - 1][i]);
-              y -= hi_f32(r[t - 1][i]);
-              r[t][i] = pack_bf16(x, y);
-            }
+            if (!exact) continue;
+            uint64_t x = f2sub(M[8 * b + i], unpack_bf16(r[0][i]));
+            r[1][i] = pack_bf16(x);
+            x = f2sub(x, unpack_bf16(r[1][i]));
+            r[2][i] = pack_bf16(x);
           }
         }
-        tmem_st8(lanes + C::cM + 32 * hf + 8 * b, r[0]);
+        tmem_st8(lanes + C::cM + 8 * b, r[0]);
         if constexpr (KIND == kGrad) {
-          if (dots) {
-            tmem_st8(lanes + C::cM + 64 + 32 * hf + 8 * b, r[1]);
-            tmem_st8(lanes + C::cM + 128 + 32 * hf + 8 * b, r[2]);
+          if (exact) {
+            tmem_st8(lanes + C::cM + 64 + 8 * b, r[1]);
+            tmem_st8(lanes + C::cM + 128 + 8 * b, r[2]);
           }
         }
       }
@@ -626,42 +337,400 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) mbar_arrive(b_s);
     };
-    bool ok = true;
     if (KIND != kStates) put_state();
-    float *row_dot = reinterpret_cast<float *>(sm + C::offDot);
-    float *red = row_dot + 128;                     // [2][2 halves][4 quads][32]
-    for (int c = 0; c < nc; ++c) {
-      const int st = c % C::kStages, ci = chunk_at(c), len = rows_of(ci);
-      if (!(ok = warp_wait(b_gate + st, c / C::kStages, s_abort, p.status))) break;
-      const float *gt = gates(st);
-      const float a = gt[384];
-      if (!(ok = warp_wait(b_d, c, s_abort, p.status))) break;
+    int c = 0;
+    for (; c < nc; ++c) {
+      const int st = c % C::kStages;
+      if (!wait(b_gate + st, c / C::kStages)) break;
+      const float a = gates(st)[384];
+      const uint64_t a2 = f2pk(a, a);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_empty + st);
+      if (!wait(b_d, c)) break;
       tc_fence_after();
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        uint32_t r[16];
-        tmem_ld16(lanes + C::cD + 64 * hf + 16 * b, r);
+        if (32 * b >= ps.dx) break;
+        uint32_t r[32];
+        tmem_ld32(lanes + C::cD + 32 * b, r);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) M[16 * b + i] = fmaf(a, M[16 * b + i], __uint_as_float(r[i]));
+        for (int i = 0; i < 16; ++i) M[16 * b + i] = f2fma(a2, M[16 * b + i], f2bits(r[2 * i], r[2 * i + 1]));
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_dfree);
-      if (KIND != kStates) {
-        if (!(ok = warp_wait(b_o + (c & 1), c >> 1, s_abort, p.status))) break;
-        // (the scores' row dots; waited for here, before b_ofree lets the next phase complete)
-        if (dots && !(ok = warp_wait(b_p, c, s_abort, p.status))) break;
+      if (KIND != kStates && c + 1 < nc) {
+        // (O1 of this chunk has read the operand)
+        if (!wait(b_o + (c & 1), c >> 1)) break;
         tc_fence_after();
-        if (KIND == kOut && c + 1 < nc) put_state();
-        // outputs of 32 tokens, 16 at a time
-        const size_t ostr = (size_t)(ps.part ? p.H : ps.ho) * ps.dz;
-        const size_t o0 = (size_t)(u.row0 + ci * kC + 32 * hf) * ostr + (size_t)h * ps.dz + z;
-        const int lim = z < ps.dz && ps.out ? len - 32 * hf : 0;
-        const uint8_t *wt = sm + st * C::kStage + C::oW + (z >> 6) * kPanel + (32 * hf) * 128;
-        float sums = 0.f;
+        put_state();
+      }
+    }
+    done = c == nc;
+    if (done && live) {
+      auto store = [&](float *dst) {
+        dst += (size_t)z * ps.sz;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int i = 0; i < 64; i += 2) {
+          float4 f;
+          f2up(M[i], f.x, f.y);
+          f2up(M[i + 1], f.z, f.w);
+          if (2 * i >= ps.dx) break;
+          if (ps.sx == 1) {
+            *reinterpret_cast<float4 *>(dst + 2 * i) = f;
+          } else {
+            dst[(size_t)(2 * i) * ps.sx] = f.x;
+            dst[(size_t)(2 * i + 1) * ps.sx] = f.y;
+            dst[(size_t)(2 * i + 2) * ps.sx] = f.z;
+            dst[(size_t)(2 * i + 3) * ps.sx] = f.w;
+          }
+        }
+      };
+      if (KIND == kStates) store(ps.end_slot + ((size_t)blockIdx.x * p.H + h) * p.elems);
+      else if (last_seg) {
+        if (ps.end) store(ps.end + ((size_t)u.n * p.H + h) * p.elems);
+        if (ps.end_slot) store(ps.end_slot + ((size_t)(blockIdx.x + 1) * p.H + h) * p.elems);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 14) {
+      // -------------------------------------------------------------- loads and decays
+      const int px = (ps.dx + 63) / 64, pz = (ps.dz + 63) / 64;
+      const uint32_t bytes = kPanel * ((KIND != kStates ? px : 0) + px + pz + (exact ? pz : 0));
+      // lane 2 t + q loads panel q of tile t (Y Z, X Y Z, or X Y Z W)
+      const int tile = (lane >> 1) + (KIND == kStates ? 1 : 0);
+      const bool load = lane < 2 * C::kTiles && (lane & 1) < (tile < 2 ? px : pz) && (tile < 3 || exact);
+      const int map = tile == 0 ? ps.ix : tile == 1 ? ps.iy : tile == 2 ? ps.iz : ps.iw;
+      const int head = h * (tile == 0 ? ps.hx : tile == 1 ? ps.hy : tile == 2 ? ps.hz : ps.hw) / p.H;
+      long long whole = 0, all = 0;
+      float gv[2];
+      auto load_g = [&](int c) {
+        const int ci = chunk_at(c), len = rows_of(ci);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = 2 * lane + e;
+          gv[e] = i < len ? p.g[p.g_fixed ? (size_t)h : (size_t)(u.row0 + ci * kC + i) * p.H + h] : 0.f;
+        }
+      };
+      load_g(0);
+      int c = 0;
+      for (; c < nc; ++c) {
+        const int st = c % C::kStages, ci = chunk_at(c), len = rows_of(ci);
+        if (c >= C::kStages && !wait(b_empty + st, c / C::kStages - 1)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(b_full + st, bytes);
+          *s_issued = c + 1;
+        }
+        __syncwarp();
+        if (load) {
+          // (no dO: its loads start past the tensor's end, where TMA reads 0)
+          const int row = map == 3 && p.no_dO ? 1 << 30 : (int)(u.row0 + ci * kC);
+          tma_load_3d(sm + st * C::kStage + lane * kPanel, &p.maps[map], b_full + st, 64 * (lane & 1), head, row);
+        }
+        // (fixed decays: a stage that held as many rows holds the same decays)
+        if (!p.g_fixed || c < C::kStages || rows_of(chunk_at(c - C::kStages)) != len) {
+          const long long x0 = 2 * lane < len ? fixed_log2(gv[0]) : 0;
+          const long long x1 = 2 * lane + 1 < len ? fixed_log2(gv[1]) : 0;
+          if (c + 1 < nc) load_g(c + 1);
+          const long long sum = scan_pairs(x0, x1);
+          all = __shfl_sync(0xffffffffu, sum, 31);
+          const long long mid = __shfl_sync(0xffffffffu, sum, 15);      // up to token 31
+          // weights as one product about token 31 while neither half decays by more than 2^-60
+          const long long lim = 60ll << 32;
+          const bool plain = mid >= -lim && all - mid >= -lim;
+          float *gt = gates(st);
+          float2 rf, tf, ra, cb;
+          auto one = [&](long long G, int i, float &r, float &t, float &a, float &b) {
+            const float since = exp2_fixed(G), until = exp2_fixed(all - G);
+            r = rev ? until : since;
+            t = i < len ? (rev ? since : until) : 0.f;
+            if (KIND == kStates) return;
+            const float up = exp2_fixed(G - mid), down = exp2_fixed(mid - G);
+            a = plain ? (rev ? down : up) : 1.f;
+            b = plain ? (rev ? up : down) : i < 32 ? down : up;   // (to / from token 31)
+          };
+          one(sum - x1, 2 * lane, rf.x, tf.x, ra.x, cb.x);
+          one(sum, 2 * lane + 1, rf.y, tf.y, ra.y, cb.y);
+          reinterpret_cast<float2 *>(gt)[lane] = rf;
+          reinterpret_cast<float2 *>(gt + 64)[lane] = tf;
+          if (KIND != kStates) {
+            reinterpret_cast<float2 *>(gt + 128)[lane] = ra;
+            reinterpret_cast<float2 *>(gt + 192)[lane] = cb;
+            reinterpret_cast<longlong2 *>(gt + 256)[lane] = make_longlong2(sum - x1, sum);
+          }
+          if (lane == 0) {
+            gt[384] = exp2_fixed(all);
+            gt[385] = plain ? 1.f : 0.f;
+          }
+        }
+        whole = max(whole + all, -(1ll << 52));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_gate + st);
+      }
+      done = c == nc;
+      // (a backward walk's segments but the last belong to the forward walk too, which writes theirs)
+      if (KIND == kStates && lane == 0 && (!rev || u.piece == u.pieces - 1))
+        ps.decay[(size_t)blockIdx.x * p.H + h] = exp2_fixed(whole);
+    } else if (warp == 15) {
+      // -------------------------------------------------------------- issue of scores and O1
+      if (KIND != kStates && lane == 0) {
+        const uint32_t id = idesc_bf16(128, 64, false, false);
+        auto tiles = [&](int c) {      // chunk c's tiles have landed (and rows past a ragged end are 0)
+          if (!need(b_full + c % C::kStages, c / C::kStages)) return false;
+          return rows_of(chunk_at(c)) == kC || need(b_zeroed, 0);
+        };
+        // sums over x channels, 16 at a time: of two K-major tiles, or of M's columns and a tile
+        const int kx = ps.dx / 16;
+        auto scores = [&](int c) {
+          uint64_t a = kmajor((c % C::kStages) * C::kStage + C::oX), b = kmajor((c % C::kStages) * C::kStage + C::oY);
+#pragma unroll 1
+          for (int k = 0; k < kx; ++k) {
+            mma_bf16_ss(tmem + C::cSc, a, b, id, k > 0);
+            const uint64_t step = k == 3 ? (kPanel >> 4) - 6 : 2;
+            a += step;
+            b += step;
+          }
+          mma_commit(b_sc);
+        };
+        auto out1 = [&](uint32_t m, uint64_t b, bool more) {
+#pragma unroll 1
+          for (int k = 0; k < kx; ++k) {
+            mma_bf16_ts(tmem + C::cO1, m, b, id, more || k > 0);
+            m += 8;
+            b += k == 3 ? (kPanel >> 4) - 6 : 2;
+          }
+        };
+        bool ok = tiles(0);
+        if (ok) {
+          tc_fence_after();
+          scores(0);
+        }
+        for (int c = 0; ok && c < nc; ++c) {
+          if (!(ok = need(b_s, c) && (c == 0 || need(b_ofree, c - 1)))) break;
+          tc_fence_after();
+          const uint64_t x = kmajor((c % C::kStages) * C::kStage + C::oX);
+#pragma unroll 1
+          for (int t = 0; t < (exact ? 3 : 1); ++t) out1(tmem + C::cM + 64 * t, x, t > 0);
+          mma_commit(b_o + (c & 1));
+          mma_commit(b_empty + c % C::kStages);
+          if (c + 1 < nc) {
+            // (the scores of this chunk have been read)
+            if (!(ok = need(b_p + (c & 1), c >> 1) && tiles(c + 1))) break;
+            tc_fence_after();
+            scores(c + 1);
+          }
+        }
+        done = ok;
+        // every product issued has completed before the tensor memory is released
+        mma_commit(b_drain);
+        mbar_wait(b_drain, 0, kDrainNs);
+      }
+      __syncwarp();
+    } else if (warp == 19) {
+      // -------------------------------------------------------------- issue of D and O2
+      if (lane == 0) {
+        const uint32_t id_d = idesc_bf16(128, ps.dx, true, true), id_o = idesc_bf16(128, 64, true, false);
+        bool ok = true;
+        for (int c = 0; ok && c < nc; ++c) {
+          const uint32_t st = (c % C::kStages) * C::kStage;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            if (!(ok = need(b_w + half, c) && (half || c == 0 || need(b_dfree, c - 1)))) break;
+            tc_fence_after();
+            const uint64_t dy = mnmajor(st + C::oY) + 256 * half, dw = mnmajor(C::offTok) + 256 * half;
+#pragma unroll 1
+            for (int m = 0; m < 3; ++m)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                mma_bf16_ss(tmem + C::cD, dw + m * (kTileB >> 4) + 128 * k, dy + 128 * k, id_d, half + m + k > 0);
+            mma_commit(b_wfree + half);
+          }
+          if (!ok) break;
+          mma_commit(b_d);
+          if (KIND != kStates) {
+            if (!(ok = need(b_p + (c & 1), c >> 1) && (c == 0 || need(b_ofree, c - 1)))) break;
+            tc_fence_after();
+            const uint64_t dz = mnmajor(st + C::oZ);
+            const uint64_t dp = kmajor(C::offP + (C::kPBufs > 1 ? (c & 1) * C::kP : 0));
+#pragma unroll 1
+            for (int t = 0; t < (exact ? 3 : 1); ++t)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_bf16_ss(tmem + C::cO2, dz + 128 * k, dp + t * (kPanel >> 4) + 2 * k, id_o, t + k > 0);
+            mma_commit(b_o + (c & 1));
+          }
+          mma_commit(b_empty + c % C::kStages);
+        }
+        done = ok;
+        mma_commit(b_drain + 1);
+        mbar_wait(b_drain + 1, 0, kDrainNs);
+      }
+      __syncwarp();
+    } else if (warp >= C::kTokWarp && warp < C::kTokWarp + C::kTokWarps) {
+      // -------------------------------------------------------------- tokf Z in three bf16 terms
+      constexpr int kT = 32 * C::kTokWarps;
+      const int t = tid - 32 * C::kTokWarp, n = 256 * ((ps.dz + 63) / 64);   // 16-byte pieces of half a tile
+      int c = 0;
+      for (; c < nc; ++c) {
+        const int st = c % C::kStages, len = rows_of(chunk_at(c));
+        uint8_t *base = sm + st * C::kStage;
+        if (!wait(b_full + st, c / C::kStages)) break;
+        if (len < kC) {
+          // a ragged end: the rows that follow belong to another sequence
+          for (int i = t; i < (int)(C::kStage / 16); i += kT)
+            if ((i >> 3 & 63) >= len) reinterpret_cast<uint4 *>(base)[i] = make_uint4(0, 0, 0, 0);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_zeroed);
+          if (!wait(b_zeroed, 0)) break;
+        }
+        if (!wait(b_gate + st, c / C::kStages)) break;
+        const float *tokf = gates(st) + 64;
+        const uint4 *src = reinterpret_cast<const uint4 *>(base + C::oZ);
+        uint4 *dst = reinterpret_cast<uint4 *>(sm + C::offTok);
+        bool ok = true;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (c > 0 && !(ok = wait(b_wfree + half, c - 1))) break;
+#pragma unroll 1
+          for (int v = t; v < n; v += kT) {
+            const int i = v + 256 * half + (v & 256);                        // panel v / 256, this half's rows
+            const uint64_t w = f2pk(tokf[i >> 3 & 63], tokf[i >> 3 & 63]);
+            const uint4 z = src[i];
+            const uint32_t zi[4] = {z.x, z.y, z.z, z.w};
+            uint32_t r[3][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint64_t x = f2mul(unpack_bf16(zi[e]), w);
+              r[0][e] = pack_bf16(x);
+              x = f2sub(x, unpack_bf16(r[0][e]));
+              r[1][e] = pack_bf16(x);
+              x = f2sub(x, unpack_bf16(r[1][e]));
+              r[2][e] = pack_bf16(x);
+            }
+#pragma unroll
+            for (int t3 = 0; t3 < 3; ++t3)
+              dst[t3 * (kTileB / 16) + i] = make_uint4(r[t3][0], r[t3][1], r[t3][2], r[t3][3]);
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_w + half);
+        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(b_empty + st);
+      }
+      done = c == nc;
+    } else if (KIND != kStates && warp >= 12 && warp < 14) {
+      // -------------------------------------------------------------- scores (warps 12, 13)
+      const int wr = warp - 12, row = 32 * wr + lane;
+      const uint32_t lanes = tmem + ((uint32_t)(32 * wr) << 16);
+      const int other = rev ? 1 : 0;               // the column block a causal off-diagonal block has
+      int c = 0;
+      for (; c < nc; ++c) {
+        const int st = c % C::kStages;
+        if (!wait(b_gate + st, c / C::kStages)) break;
+        if (!wait(b_sc, c)) break;
+        tc_fence_after();
+        // (the scores two chunks back, or one, have been read)
+        if (c >= C::kPBufs && !wait(b_o + ((c - C::kPBufs) & 1), (c - C::kPBufs) >> 1)) break;
+        const float *gt = gates(st);
+        uint8_t *P = sm + C::offP + (C::kPBufs > 1 ? (c & 1) * C::kP : 0) + row * 128;
+        const bool plain = gt[385] != 0.f;
+        const float scale = plain ? 1.f : gt[192 + row];
+        const uint64_t mine = f2pk(scale, scale);
+        const long long *G = reinterpret_cast<const long long *>(gt + 256);
+#pragma unroll 1
+        for (int b = wr == other ? wr : 0; b < (wr == other ? wr + 1 : 2); ++b) {
+          if (!plain && b == wr) {                  // every weight from its own difference of sums
+            const long long me = G[row];
+#pragma unroll 1
+            for (int j = 0; j < 32; ++j) {
+              uint32_t s1;
+              tmem_ld1(lanes + C::cSc + 32 * b + j, s1);
+              tmem_wait_ld();
+              const long long o = G[32 * b + j];
+              float x = (rev ? j >= lane : j <= lane) ? __uint_as_float(s1) * exp2_fixed(rev ? o - me : me - o) : 0.f;
+#pragma unroll
+              for (int t = 0; t < C::kTerms; ++t) {
+                const __nv_bfloat16 v = __float2bfloat16_rn(x);
+                *reinterpret_cast<__nv_bfloat16 *>(P + t * kPanel + (((4 * b + j / 8) ^ (row & 7)) << 4) + 2 * (j & 7)) = v;
+                x -= __bfloat162float(v);
+              }
+            }
+            continue;
+          }
+          // the diagonal block's causal columns
+          const uint32_t mask = b != wr ? ~0u : rev ? ~0u << lane : ~0u >> (31 - lane);
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            const int j0 = 32 * b + 8 * q;
+            const uint32_t m = mask >> (8 * q);
+            uint32_t s[8];
+            tmem_ld8(lanes + C::cSc + j0, s);
+            const float4 f0 = *reinterpret_cast<const float4 *>(gt + 192 + j0);
+            const float4 f1 = *reinterpret_cast<const float4 *>(gt + 192 + j0 + 4);
+            const uint64_t f[4] = {f2pk(f0.x, f0.y), f2pk(f0.z, f0.w), f2pk(f1.x, f1.y), f2pk(f1.z, f1.w)};
+            tmem_wait_ld();
+            uint32_t r[C::kTerms][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              // (`mine` is 1 but off the diagonal block through token 31; the mask selects, so that
+              // an infinite weight on the acausal side vanishes)
+              float a, c1;
+              f2up(f2mul(f2bits(s[2 * j], s[2 * j + 1]), f2mul(f[j], mine)), a, c1);
+              uint64_t x = f2pk(m & (1u << (2 * j)) ? a : 0.f, m & (2u << (2 * j)) ? c1 : 0.f);
+              r[0][j] = pack_bf16(x);
+              if constexpr (KIND == kGrad) {
+                if (!exact) continue;
+                x = f2sub(x, unpack_bf16(r[0][j]));
+                r[1][j] = pack_bf16(x);
+                x = f2sub(x, unpack_bf16(r[1][j]));
+                r[2][j] = pack_bf16(x);
+              }
+            }
+            uint8_t *at = P + (((j0 / 8) ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4 *>(at) = make_uint4(r[0][0], r[0][1], r[0][2], r[0][3]);
+            if constexpr (KIND == kGrad) {
+              if (exact) {
+                *reinterpret_cast<uint4 *>(at + kPanel) = make_uint4(r[1][0], r[1][1], r[1][2], r[1][3]);
+                *reinterpret_cast<uint4 *>(at + 2 * kPanel) = make_uint4(r[2][0], r[2][1], r[2][2], r[2][3]);
+              }
+            }
+          }
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(b_p + (c & 1));
+          mbar_arrive(b_empty + st);
+        }
+      }
+      done = c == nc;
+    } else if (KIND != kStates && warp < 12) {
+      // -------------------------------------------------------------- outputs (warps 4-11)
+      const int quad = warp & 3, hf = (warp >> 2) - 1;
+      const int z = 32 * quad + lane;
+      const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+      float *red = reinterpret_cast<float *>(sm + C::offDot);      // [2][2 halves][4 quads][32]
+      const size_t ostr = (size_t)(ps.part ? p.H : ps.ho) * ps.dz;
+      int c = 0;
+      for (; c < nc; ++c) {
+        const int st = c % C::kStages, ci = chunk_at(c), len = rows_of(ci);
+        const float *gt = gates(st);
+        if (!wait(b_gate + st, c / C::kStages)) break;
+        if (!wait(b_o + (c & 1), c >> 1)) break;
+        tc_fence_after();
+        const size_t o0 = (size_t)(u.row0 + ci * kC + 32 * hf) * ostr + (size_t)h * ps.dz + z;
+        int lim = z < ps.dz && ps.out ? len - 32 * hf : 0;
+        const uint8_t *wt = sm + st * C::kStage + C::oW + (z >> 6) * kPanel + (32 * hf) * 128;
+        float *of = static_cast<float *>(ps.out) + o0;
+        __nv_bfloat16 *ob = static_cast<__nv_bfloat16 *>(ps.out) + o0;
+        float sums = 0.f;
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b, lim -= 16) {
           uint32_t r1[16], r2[16];
           tmem_ld16(lanes + C::cO1 + 32 * hf + 16 * b, r1);
           tmem_ld16(lanes + C::cO2 + 32 * hf + 16 * b, r2);
@@ -673,82 +742,68 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
           }
           const float4 *rf = reinterpret_cast<const float4 *>(gt + 32 * hf + 16 * b);
           const float4 *ra = reinterpret_cast<const float4 *>(gt + 128 + 32 * hf + 16 * b);
-          float x[16], v[16];
+          float v[16];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float4 f = rf[i], e = ra[i];
-            x[4 * i] = f.x * __uint_as_float(r1[4 * i]);
-            x[4 * i + 1] = f.y * __uint_as_float(r1[4 * i + 1]);
-            x[4 * i + 2] = f.z * __uint_as_float(r1[4 * i + 2]);
-            x[4 * i + 3] = f.w * __uint_as_float(r1[4 * i + 3]);
-            v[4 * i] = fmaf(e.x, __uint_as_float(r2[4 * i]), x[4 * i]);
-            v[4 * i + 1] = fmaf(e.y, __uint_as_float(r2[4 * i + 1]), x[4 * i + 1]);
-            v[4 * i + 2] = fmaf(e.z, __uint_as_float(r2[4 * i + 2]), x[4 * i + 2]);
-            v[4 * i + 3] = fmaf(e.w, __uint_as_float(r2[4 * i + 3]), x[4 * i + 3]);
+            f2up(f2fma(f2pk(e.x, e.y), f2bits(r2[4 * i], r2[4 * i + 1]),
+                       f2mul(f2pk(f.x, f.y), f2bits(r1[4 * i], r1[4 * i + 1]))), v[4 * i], v[4 * i + 1]);
+            f2up(f2fma(f2pk(e.z, e.w), f2bits(r2[4 * i + 2], r2[4 * i + 3]),
+                       f2mul(f2pk(f.z, f.w), f2bits(r1[4 * i + 2], r1[4 * i + 3]))), v[4 * i + 2], v[4 * i + 3]);
           }
-          if (ps.part) {
-            float *o = static_cast<float *>(ps.out) + o0 + (size_t)(16 * b) * ostr;
+          if (KIND == kGrad && ps.part) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i, o += ostr)
-              if (16 * b + i < lim) *o = v[i];
+            for (int i = 0; i < 16; ++i, of += ostr)
+              if (i < lim) *of = v[i];
           } else {
-            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(ps.out) + o0 + (size_t)(16 * b) * ostr;
 #pragma unroll
-            for (int i = 0; i < 16; ++i, o += ostr)
-              if (16 * b + i < lim) *o = __float2bfloat16_rn(v[i]);
+            for (int i = 0; i < 16; ++i, ob += ostr)
+              if (i < lim) *ob = __float2bfloat16_rn(v[i]);
           }
-          if (dots) {
+          if (exact) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int t = 16 * b + i;
               const float w = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(
-                  wt + t * 128 + (((z & 63) * 2) ^ ((t & 7) << 4))));
-              x[i] = z < ps.dz ? x[i] * w : 0.f;
+                  wt + t * 128 + (((z & 63) * 2) ^ ((i & 7) << 4))));
+              v[i] = z < ps.dz ? v[i] * w : 0.f;
             }
-            const float s = lane_sums16(x);
+            const float s = lane_sums16(v);
             if ((lane >> 4) == b) sums = s;         // lane t holds token t of this half
           }
         }
-        if (KIND == kGrad && c + 1 < nc) put_state();
-        if (dots) {
+        if (exact) {
           float *rd = red + ((c & 1) * 2 + hf) * 128;
           rd[quad * 32 + lane] = sums;
           __syncwarp();
           if (lane == 0) mbar_arrive(b_red + hf);
-          if (quad == 0 && !(ok = warp_wait(b_red + hf, c, s_abort, p.status))) break;
-          if (quad == 0 && 32 * hf + lane < len)
-            ps.dots[(size_t)h * p.rows + u.row0 + ci * kC + 32 * hf + lane] =
-                (rd[lane] + rd[32 + lane]) + (rd[64 + lane] + rd[96 + lane]) + row_dot[(c & 1) * 64 + 32 * hf + lane];
+          if (quad == 0) {
+            if (!wait(b_red + hf, c)) break;
+            if (32 * hf + lane < len)
+              ps.dots[(size_t)h * p.rows + u.row0 + ci * kC + 32 * hf + lane] =
+                  (rd[lane] + rd[32 + lane]) + (rd[64 + lane] + rd[96 + lane]);
+          }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_empty + st);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_empty + st);
-    }
-    if (ok && live) {
-      auto store = [&](float *dst) {
-        dst += (size_t)z * ps.sz + (size_t)(64 * hf) * ps.sx;
-#pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if (i < ncol) dst[(size_t)i * ps.sx] = M[i];
-      };
-      if (KIND == kStates) store(ps.end_slot + ((size_t)blockIdx.x * p.H + h) * p.elems);
-      else if (last_seg) {
-        if (ps.end) store(ps.end + ((size_t)u.n * p.H + h) * p.elems);
-        if (ps.end_slot) store(ps.end_slot + ((size_t)(blockIdx.x + 1) * p.H + h) * p.elems);
-      }
+      done = c == nc;
+    } else {
+      done = true;                                  // (a role this launch has no use for)
     }
   }
+  if (!done && (lane == 0 || warp < 4)) give_up(s_abort, p.status);
   tc_fence_before();
   __syncthreads();
   if (tid == 0) {
     // loads that a role which gave up did not wait for have landed
     for (int c = max(0, *s_issued - C::kStages); c < *s_issued; ++c)
-      mbar_wait(b_full + c % C::kStages, (c / C::kStages) & 1, kWaitNs);
+      mbar_wait(b_full + c % C::kStages, (c / C::kStages) & 1, kDrainNs);
   }
   __syncthreads();
-  if (warp == 11) {
+  if (warp == 15) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kCols);
+    tmem_dealloc(*s_tmem, 512);
   }
 }
 
