@@ -12,9 +12,9 @@
 namespace ckda {
 namespace {
 
-template <int DK, typename T>
-__global__ void __launch_bounds__(256) linattn_decode_kernel(const LinDecodeArgs p, int slices,
-                                                             long tasks) {
+template <int DK, int DV, typename T>
+__global__ void __launch_bounds__(256, 2) linattn_decode_kernel(const LinDecodeArgs p, long tasks) {
+  constexpr int slices = DV / 16;
   __shared__ float2 s_kq[8][DK];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long task = (long)blockIdx.x * (blockDim.x >> 5) + warp;
@@ -24,15 +24,15 @@ __global__ void __launch_bounds__(256) linattn_decode_kernel(const LinDecodeArgs
   const long b = head / p.H;
   const int h = (int)(head - b * p.H);
   const int col = slice * 16 + (lane & 3) * 4, r0 = lane >> 2;
-  float *S = p.S + (size_t)head * DK * p.dv + col;
+  float *S = p.S + (size_t)head * DK * DV + col;
   constexpr int kRows = DK / 8;
   float4 st[kRows];
 #pragma unroll
   for (int m = 0; m < kRows; ++m)
-    st[m] = *reinterpret_cast<const float4 *>(S + (size_t)(r0 + 8 * m) * p.dv);
+    st[m] = *reinterpret_cast<const float4 *>(S + (size_t)(r0 + 8 * m) * DV);
   const T *q = static_cast<const T *>(p.q) + ((size_t)b * p.Hq + (long)h * p.Hq / p.H) * DK;
   const T *k = static_cast<const T *>(p.k) + ((size_t)b * p.Hk + (long)h * p.Hk / p.H) * DK;
-  const T *v = static_cast<const T *>(p.v) + ((size_t)b * p.Hv + (long)h * p.Hv / p.H) * p.dv + col;
+  const T *v = static_cast<const T *>(p.v) + ((size_t)b * p.Hv + (long)h * p.Hv / p.H) * DV + col;
   for (int i = lane; i < DK; i += 32) s_kq[warp][i] = make_float2(to_f32(k[i]), to_f32(q[i]));
   const float al = expf(p.g[p.g_fixed ? (long)h : head]);
   const float v0 = to_f32(v[0]), v1 = to_f32(v[1]), v2 = to_f32(v[2]), v3 = to_f32(v[3]);
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(256) linattn_decode_kernel(const LinDecodeArgs
     const float2 kq = s_kq[warp][r0 + 8 * m];
     st[m].x = fmaf(al, st[m].x, kq.x * v0); st[m].y = fmaf(al, st[m].y, kq.x * v1);
     st[m].z = fmaf(al, st[m].z, kq.x * v2); st[m].w = fmaf(al, st[m].w, kq.x * v3);
-    *reinterpret_cast<float4 *>(S + (size_t)(r0 + 8 * m) * p.dv) = st[m];
+    *reinterpret_cast<float4 *>(S + (size_t)(r0 + 8 * m) * DV) = st[m];
     o0 = fmaf(kq.y, st[m].x, o0); o1 = fmaf(kq.y, st[m].y, o1);
     o2 = fmaf(kq.y, st[m].z, o2); o3 = fmaf(kq.y, st[m].w, o3);
   }
@@ -56,29 +56,38 @@ __global__ void __launch_bounds__(256) linattn_decode_kernel(const LinDecodeArgs
     o3 += __shfl_xor_sync(0xffffffffu, o3, off);
   }
   if (r0 == 0) {
-    T *o = static_cast<T *>(p.o) + (size_t)head * p.dv + col;
+    T *o = static_cast<T *>(p.o) + (size_t)head * DV + col;
     o[0] = from_f32<T>(o0); o[1] = from_f32<T>(o1);
     o[2] = from_f32<T>(o2); o[3] = from_f32<T>(o3);
   }
 }
 
-template <int DK, typename T>
+template <int DK, int DV, typename T>
 int launch_typed(const LinDecodeArgs &a, cudaStream_t s) {
-  const int slices = a.dv / 16;
-  const long tasks = (long)a.B * a.H * slices;
+  const long tasks = (long)a.B * a.H * (DV / 16);
   long warps = tasks / (148 * 4);
   warps = warps < 1 ? 1 : warps > 8 ? 8 : warps;
-  linattn_decode_kernel<DK, T><<<(unsigned)((tasks + warps - 1) / warps), (unsigned)(32 * warps), 0, s>>>(
-      a, slices, tasks);
+  linattn_decode_kernel<DK, DV, T><<<(unsigned)((tasks + warps - 1) / warps), (unsigned)(32 * warps), 0, s>>>(
+      a, tasks);
   return cudaGetLastError() == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
+}
+template <int DK, typename T>
+int launch_dv(const LinDecodeArgs &a, cudaStream_t s) {
+  switch (a.dv) {
+    case 16: return launch_typed<DK, 16, T>(a, s);
+    case 32: return launch_typed<DK, 32, T>(a, s);
+    case 64: return launch_typed<DK, 64, T>(a, s);
+    case 128: return launch_typed<DK, 128, T>(a, s);
+  }
+  return CKDA_ERR_DIM;
 }
 template <typename T>
 int launch_dk(const LinDecodeArgs &a, cudaStream_t s) {
   switch (a.dk) {
-    case 16: return launch_typed<16, T>(a, s);
-    case 32: return launch_typed<32, T>(a, s);
-    case 64: return launch_typed<64, T>(a, s);
-    case 128: return launch_typed<128, T>(a, s);
+    case 16: return launch_dv<16, T>(a, s);
+    case 32: return launch_dv<32, T>(a, s);
+    case 64: return launch_dv<64, T>(a, s);
+    case 128: return launch_dv<128, T>(a, s);
   }
   return CKDA_ERR_DIM;
 }

@@ -14,19 +14,25 @@
 // or a column of a product, so it is applied in fp32 to scores, to outputs as they leave, and
 // for the state to Z alone.  Per chunk of 64 tokens (all M = 128, fp32 accumulation in TMEM):
 //   scores  X Y^T            [64 x 64]   A, B from shared memory
-//   O1      M X^T            [z x 64]    A = M as bf16 from TMEM
-//   O2      Z^T P^T          [z x 64]    P as bf16 through shared memory
+//   O       M X^T + Z^T P^T  [z x 64]    M as bf16 from TMEM, P as bf16 through shared memory
 //   D       (tokf Z)^T Y     [z x x]     tokf Z in three bf16 terms
-// M is kept in fp32 registers.  Roundings to bf16: P, M as an operand of O1 (each 2^-9 of a
+// A row's factor rowf is common to both parts of O as long as P_ij / rowf_i stays in range (the
+// chunk decays by no more than 2^-100): P is formed as colb_j (x_i . y_j) and O is scaled once
+// as it leaves.  A chunk that decays faster takes its weights block by block, and one that
+// decays faster still pair by pair; then the second part has its own accumulator.
+//
+// M is kept in fp32 registers.  Roundings to bf16: P, M as an operand of O (each 2^-9 of a
 // term in the mean, the size of the output's own rounding); tokf Z is split into three terms
 // (24 bits), so M itself carries fp32 accuracy over any length.  Where row dots are wanted
-// (decay gradients, which cancel) M and P go into O1 and O2 in three terms too.
+// (decay gradients, which cancel) M and P go into O in three terms too.
 //
-// One CTA per (segment, head), 20 warps: 0-3 state (176 registers a thread, 128 of them M),
-// 4-11 outputs, 12-13 scores (TMEM lanes 0-63), 14 TMA loads and decays, 15 issue of scores and
-// O1, 16-18 tokf Z, 19 issue of D and O2 (two issuers: one thread's products take 50 cycles or
-// more each to issue).  The roles run the chunks at their own pace through mbarriers.  A
-// sequence may be cut into segments: a first launch computes every segment's own state, an
+// One CTA per (segment, head), 20 warps: 0-3 state (200 registers a thread, 128 of them M), 4-7
+// outputs, 8, 9 and one of 12, 13 scores (a 32 x 32 block each), 10 TMA loads and decays, 11
+// issue of O, 19 issue of scores and D (two issuers: one thread's products take 50 cycles or
+// more each to issue), the rest tokf Z.  The roles run the chunks at their own pace through
+// mbarriers; their loops are kept small, because together they have to stay in the instruction
+// caches (fully unrolled they ran at half the speed, 42 % of all stalls waiting for code).
+// A sequence may be cut into segments: a first launch computes every segment's own state, an
 // elementwise walk over a sequence's segments gives each its incoming state (the decay is a
 // scalar, so a segment's state map is one factor), and the main launch runs all segments side
 // by side.
@@ -65,11 +71,29 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+// 16 lanes x 32 columns as 8 x 8 blocks: registers 4 k, 4 k + 1 hold lane t / 4, columns 8 k + 2 (t % 4)
+// and the next; 4 k + 2, 4 k + 3 the same of lane t / 4 + 8
+__device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// four 8 x 8 blocks of 16-bit values, transposed: lane t's register i is column t / 4, rows 2 (t % 4)
+// and the next, of block i; lane 8 i + r gives the address of block i's row r
+__device__ __forceinline__ void stmatrix4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -105,40 +129,41 @@ __device__ __forceinline__ uint64_t f2bits(uint32_t a, uint32_t b) {
 
 // ------------------------------------------------------------------ shapes
 enum : int { kStates = 0, kOut = 1, kGrad = 2 };   // what a launch computes
+enum : int { kWhole = 0, kBlocks = 1, kPairs = 2 };   // how a chunk's weights are formed
 constexpr int kThreads = 640;
 constexpr uint32_t kPanel = 8192;                  // 64 tokens x 64 channels of bf16, 128-byte swizzle
 constexpr uint32_t kTileB = 2 * kPanel;            // 64 tokens x 128 channels
-// Registers a thread by role: 128 x 176 + 512 x 72 = 59,392 of the launch's 640 x 96 = 61,440.
-constexpr int kRegsState = 176, kRegsOther = 72;
+constexpr uint32_t kTokB = 3 * kPanel;             // tokf Z of 32 tokens: three terms x two panels of 4 KB
+// Registers a thread by role: 128 x 200 + 512 x 64 = 58,368 of the launch's 640 x 96 = 61,440.
+constexpr int kRegsState = 200, kRegsOther = 64;
 
 template <int KIND>
 struct Cfg {
   static constexpr int kTiles = KIND == kStates ? 2 : KIND == kOut ? 3 : 4;   // Y Z | X Y Z | X Y Z W
-  static constexpr int kStages = KIND == kStates ? 4 : KIND == kOut ? 3 : 2;
+  static constexpr int kStages = KIND == kGrad ? 2 : 3;
   static constexpr int kTerms = KIND == kGrad ? 3 : 1;                        // of M and P
-  static constexpr int kPBufs = KIND == kStates ? 0 : KIND == kOut ? 2 : 1;
+  static constexpr int kTokBufs = KIND == kStates ? 4 : 2;                    // half chunks of tokf Z
+  static constexpr int kOBufs = KIND == kOut ? 2 : 1;                         // O in TMEM
   static constexpr uint32_t kStage = kTiles * kTileB;
   static constexpr uint32_t oX = 0;
   static constexpr uint32_t oY = KIND == kStates ? 0 : kTileB;
   static constexpr uint32_t oZ = oY + kTileB;
   static constexpr uint32_t oW = oZ + kTileB;                                 // kGrad
-  static constexpr uint32_t offTok = kStages * kStage;                        // tokf Z, three terms
-  static constexpr uint32_t offP = offTok + 3 * kTileB;
-  static constexpr uint32_t kP = kTerms * kPanel;                             // one P
-  static constexpr uint32_t offGate = offP + kPBufs * kP;
-  static constexpr uint32_t kGate = 6 * 64 * 4 + 16;                          // one stage's decays
-  static constexpr uint32_t offDot = offGate + kStages * kGate;               // kGrad: 2 x 2 x 4 x 32 floats
+  static constexpr uint32_t offTok = kStages * kStage;
+  static constexpr uint32_t offP = offTok + kTokBufs * kTokB;
+  static constexpr uint32_t kP = KIND == kStates ? 0 : kTerms * kPanel;
+  static constexpr uint32_t offOut = offP + kP;                               // 4 warps x 2 x (32 tokens x 32 channels)
+  static constexpr uint32_t offGate = offOut + (KIND == kStates ? 0 : 8 * 2048);
+  static constexpr uint32_t kGate = 7 * 64 * 4 + 16;                          // one stage's decays
+  static constexpr uint32_t offDot = offGate + kStages * kGate;               // kGrad: 2 x 4 x 64 floats
   static constexpr uint32_t offBar = offDot + (KIND == kGrad ? 512 * 4 : 0);
-  static constexpr int kBars = 3 * kStages + 22;
+  static constexpr int kBars = 3 * kStages + 2 * kTokBufs + 20;
   static constexpr uint32_t kSmem = offBar + kBars * 8 + 64 + 1024;           // + slack to align
-  // tokf Z: three warps beside the other roles; alone, the eight that would write outputs
-  static constexpr int kTokWarp = KIND == kStates ? 4 : 16, kTokWarps = KIND == kStates ? 8 : 3;
-  // TMEM columns
-  static constexpr uint32_t cSc = 0, cO2 = 64, cM = 128, cO1 = cM + 64 * kTerms, cD = 384;
+  // TMEM columns: scores, M, O (kOut has room for two), the second part of O apart, D
+  static constexpr uint32_t cSc = 0, cM = 64, cO = KIND == kOut ? 128 : 256, cO2 = KIND == kOut ? 256 : 320, cD = 384;
 };
 static_assert(Cfg<kOut>::kSmem <= 232448 && Cfg<kGrad>::kSmem <= 232448 && Cfg<kStates>::kSmem <= 232448,
               "shared memory");
-static_assert(Cfg<kGrad>::cO1 + 64 <= Cfg<kGrad>::cD, "tensor memory");
 
 struct Pass {
   int ix, iy, iz, iw;             // tensor maps (iw < 0: no row dots)
@@ -152,12 +177,13 @@ struct Pass {
   float *end_slot;                // [slots, H, ..]: end state of every segment (kStates), or of the
                                   // last to the slot after it (kGrad), or NULL
   float *decay;                   // kStates: [slots, H] the segment's whole decay
-  void *out;                      // [rows, ho, dz]
-  int ho, part;                   // part: fp32 per-head sums, [rows, H, dz]
+  void *out;                      // [rows, H, dz]
+  int part;                       // out is fp32 per-head shares of a shared head's gradient
   float *dots;                    // [H, rows] row dots, or NULL
 };
 struct Params {
   CUtensorMap maps[4];            // q, k, v, dO
+  CUtensorMap outs[3];            // the passes' outputs (bf16)
   Pass pass[3];
   const float *g;
   int H, g_fixed, elems, no_dO;
@@ -182,21 +208,6 @@ __device__ __forceinline__ void give_up(volatile int *abort, int *status) {
   set_status(status, CKDA_ERR_TIMEOUT);
 }
 
-// The sum over the warp's lanes of d[t], t < 16: lane l returns token l % 16's.
-__device__ __forceinline__ float lane_sums16(float (&d)[16]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int step = 8; step >= 1; step >>= 1) {
-    const bool up = lane & step;
-#pragma unroll
-    for (int i = 0; i < step; ++i) {
-      const float send = up ? d[i] : d[i + step], keep = up ? d[i + step] : d[i];
-      d[i] = keep + __shfl_xor_sync(0xffffffffu, send, step);
-    }
-  }
-  return d[0] + __shfl_xor_sync(0xffffffffu, d[0], 16);
-}
-
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_constant__ Params p) {
   using C = Cfg<KIND>;
@@ -213,44 +224,57 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
   if (KIND == kStates && last_seg) return;
   const int nc = (u.len + kC - 1) / kC;
 
+  // Warps by role (the scores' off-diagonal block lies in the TMEM lanes of a quarter that goes
+  // with the direction: 13 forwards, 12 backwards; the other of the two takes part in tokf Z)
+  const int off_warp = rev ? 12 : 13;
+  const int tok_warps = KIND == kStates ? 8 : 6;
+  const int tok_index = KIND == kStates ? (warp < 8 ? warp - 4 : warp - 8) : warp >= 14 ? warp - 13 : 0;
+  const bool is_score = KIND != kStates && (warp == 8 || warp == 9 || warp == off_warp);
+  const bool is_tok = KIND == kStates ? (warp >= 4 && warp < 8) || (warp >= 12 && warp < 16)
+                                      : warp >= 12 && warp < 19 && warp != off_warp;
+
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::offBar);
   uint64_t *b_full = bars, *b_empty = bars + C::kStages, *b_gate = bars + 2 * C::kStages;
-  uint64_t *bx = bars + 3 * C::kStages;
-  uint64_t *b_zeroed = bx, *b_sc = bx + 1, *b_p = bx + 17 /* 2 */, *b_s = bx + 3, *b_o = bx + 4 /* 2 */,
-           *b_ofree = bx + 6, *b_d = bx + 7, *b_dfree = bx + 8, *b_drain = bx + 9 /* 2 */,
-           *b_red = bx + 11 /* 2 */, *b_w = bx + 13 /* 2 */, *b_wfree = bx + 15 /* 2 */;
-  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bx + 19);
-  volatile int *s_abort = reinterpret_cast<volatile int *>(bx + 20);
-  volatile int *s_issued = reinterpret_cast<volatile int *>(bx + 21);
+  uint64_t *b_w = bars + 3 * C::kStages, *b_wfree = b_w + C::kTokBufs;
+  uint64_t *bx = b_wfree + C::kTokBufs;
+  uint64_t *b_zeroed = bx, *b_sc = bx + 1, *b_p = bx + 2, *b_s = bx + 3, *b_o = bx + 4 /* 2 */,
+           *b_ofree = bx + 6 /* 2 */, *b_d = bx + 8, *b_dfree = bx + 9, *b_drain = bx + 10 /* 2 */,
+           *b_red = bx + 12 /* 2 */, *b_o1 = bx + 14;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bx + 16);
+  volatile int *s_abort = reinterpret_cast<volatile int *>(bx + 17);
+  volatile int *s_issued = reinterpret_cast<volatile int *>(bx + 18);
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(b_full + s, 1);
-      // state 4, tokf Z, and the products' commit; beside outputs 8, scores 2 and a second commit
-      mbar_init(b_empty + s, 4 + C::kTokWarps + 1 + (KIND == kStates ? 0 : 11));
+      // state 4, tokf Z, a commit; beside outputs 4, scores 3 and a second commit
+      mbar_init(b_empty + s, 4 + tok_warps + 1 + (KIND == kStates ? 0 : 8));
       mbar_init(b_gate + s, 1);
     }
-    mbar_init(b_zeroed, C::kTokWarps);
+    for (int s = 0; s < C::kTokBufs; ++s) {
+      mbar_init(b_w + s, tok_warps);
+      mbar_init(b_wfree + s, 1);
+    }
+    mbar_init(b_zeroed, tok_warps);
     mbar_init(b_sc, 1);
+    mbar_init(b_p, 3);
     mbar_init(b_s, 4);
-    mbar_init(b_ofree, 8);
     mbar_init(b_d, 1);
     mbar_init(b_dfree, 4);
+    mbar_init(b_o1, 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(b_o + s, 2);         // O1's commit and O2's
-      mbar_init(b_p + s, 2);
-      mbar_init(b_drain + s, 1);
+      mbar_init(b_o + s, 1);
+      mbar_init(b_ofree + s, 4);
       mbar_init(b_red + s, 4);
-      mbar_init(b_w + s, C::kTokWarps);
-      mbar_init(b_wfree + s, 1);
+      mbar_init(b_drain + s, 1);
     }
     *s_abort = 0;
     *s_issued = 0;
     mbar_fence_init();
   }
-  if (warp == 15) tmem_alloc(s_tmem, 512);
+  if (warp == 11) tmem_alloc(s_tmem, 512);
   // (scores on the acausal side are never written: they stay 0)
-  for (int i = tid; i < (int)(C::kPBufs * C::kP / 16); i += kThreads)
+  for (int i = tid; i < (int)(C::kP / 16); i += kThreads)
     reinterpret_cast<uint4 *>(sm + C::offP)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
   tc_fence_before();
@@ -266,15 +290,29 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
   const uint32_t sb = smem_u32(sm);
   constexpr uint64_t kHi = (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32;
   auto kmajor = [&](uint32_t at) { return kHi | (((sb + at) >> 4) | (1u << 16)); };
-  auto mnmajor = [&](uint32_t at) { return kHi | (((sb + at) >> 4) | ((kPanel >> 4) << 16)); };
+  auto mnmajor = [&](uint32_t at, uint32_t panel) { return kHi | (((sb + at) >> 4) | ((panel >> 4) << 16)); };
   auto gates = [&](int st) { return reinterpret_cast<float *>(sm + C::offGate + st * C::kGate); };
-  // gates (floats): [0] rowf, [64] tokf, [128] rowa, [192] colb, [256] G (64-bit fixed point),
-  // [384] e^{G_C}, [385] whether P_ij is formed as rowa_i (colb_j x_i . y_j)
+  // gates (floats): [0] rowf, [64] tokf, [128] colb, [192] rowb, [256] cross, [320] G (64-bit
+  // fixed point), [448] e^{G_C}, [449] mode.  P_ij is (x_i . y_j) times
+  //   kWhole : colb_j, its row's factor left to rowf (the chunk decays by at most 2^-100)
+  //   kBlocks: rowb_i colb_j on the diagonal 32 x 32 blocks, cross_i cross_j (through token 31) off
+  //            them (each half decays by at most 2^-100)
+  //   kPairs : each pair's own weight on the diagonal blocks, cross_i cross_j off them
   const bool exact = KIND == kGrad && ps.iw >= 0;   // row dots: M and P in three terms
   // a warp's wait (all lanes agree on the outcome) and a single thread's
-  auto wait = [&](uint64_t *b, int ph) { return __all_sync(0xffffffffu, bar_wait(b, (uint32_t)ph, s_abort)) != 0; };
-  auto need = [&](uint64_t *b, int ph) { return bar_wait(b, (uint32_t)ph, s_abort); };
-  bool done = KIND == kStates && warp == 15;        // this role reached its end (15: none there)
+  auto wait = [&](uint64_t *b, uint32_t ph) { return __all_sync(0xffffffffu, bar_wait(b, ph, s_abort)) != 0; };
+  auto need = [&](uint64_t *b, uint32_t ph) { return bar_wait(b, ph, s_abort); };
+  // Phases: chunk c's completion of a barrier used once a chunk has parity c & 1; of one used
+  // every other chunk (c >> 1) & 1; of a stage's, `ph`, which the roles carry along with `st`.
+  auto next = [&](int &st, uint32_t &ph) {
+    if (++st == C::kStages) {
+      st = 0;
+      ph ^= 1u;
+    }
+  };
+  int c = 0, st = 0;
+  uint32_t ph = 0;
+  bool ok = true;
 
   if (warp < 4) {
     // ---------------------------------------------------------------- state (warps 0-3)
@@ -310,25 +348,25 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     // M as the next chunk's operand
     auto put_state = [&]() {
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        if (16 * b >= ps.dx) break;
-        uint32_t r[C::kTerms][8];
+      for (int b = 0; b < 4; ++b) {
+        if (32 * b >= ps.dx) break;
+        uint32_t r[C::kTerms][16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          r[0][i] = pack_bf16(M[8 * b + i]);
+        for (int i = 0; i < 16; ++i) {
+          r[0][i] = pack_bf16(M[16 * b + i]);
           if constexpr (KIND == kGrad) {
             if (!exact) continue;
-            uint64_t x = f2sub(M[8 * b + i], unpack_bf16(r[0][i]));
+            uint64_t x = f2sub(M[16 * b + i], unpack_bf16(r[0][i]));
             r[1][i] = pack_bf16(x);
             x = f2sub(x, unpack_bf16(r[1][i]));
             r[2][i] = pack_bf16(x);
           }
         }
-        tmem_st8(lanes + C::cM + 8 * b, r[0]);
+        tmem_st16(lanes + C::cM + 16 * b, r[0]);
         if constexpr (KIND == kGrad) {
           if (exact) {
-            tmem_st8(lanes + C::cM + 64 + 8 * b, r[1]);
-            tmem_st8(lanes + C::cM + 128 + 8 * b, r[2]);
+            tmem_st16(lanes + C::cM + 64 + 16 * b, r[1]);
+            tmem_st16(lanes + C::cM + 128 + 16 * b, r[2]);
           }
         }
       }
@@ -338,15 +376,13 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       if (lane == 0) mbar_arrive(b_s);
     };
     if (KIND != kStates) put_state();
-    int c = 0;
-    for (; c < nc; ++c) {
-      const int st = c % C::kStages;
-      if (!wait(b_gate + st, c / C::kStages)) break;
-      const float a = gates(st)[384];
+    for (; c < nc; ++c, next(st, ph)) {
+      if (!(ok = wait(b_gate + st, ph))) break;
+      const float a = gates(st)[448];
       const uint64_t a2 = f2pk(a, a);
       __syncwarp();
       if (lane == 0) mbar_arrive(b_empty + st);
-      if (!wait(b_d, c)) break;
+      if (!(ok = wait(b_d, c))) break;
       tc_fence_after();
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
@@ -361,14 +397,12 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) mbar_arrive(b_dfree);
       if (KIND != kStates && c + 1 < nc) {
-        // (O1 of this chunk has read the operand)
-        if (!wait(b_o + (c & 1), c >> 1)) break;
+        if (!(ok = wait(b_o1, c))) break;           // (O1 of this chunk has read the operand)
         tc_fence_after();
         put_state();
       }
     }
-    done = c == nc;
-    if (done && live) {
+    if (ok && live) {
       auto store = [&](float *dst) {
         dst += (size_t)z * ps.sz;
 #pragma unroll
@@ -395,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 14) {
+    if (warp == 10) {
       // -------------------------------------------------------------- loads and decays
       const int px = (ps.dx + 63) / 64, pz = (ps.dz + 63) / 64;
       const uint32_t bytes = kPanel * ((KIND != kStates ? px : 0) + px + pz + (exact ? pz : 0));
@@ -415,10 +449,9 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         }
       };
       load_g(0);
-      int c = 0;
-      for (; c < nc; ++c) {
-        const int st = c % C::kStages, ci = chunk_at(c), len = rows_of(ci);
-        if (c >= C::kStages && !wait(b_empty + st, c / C::kStages - 1)) break;
+      for (; c < nc; ++c, next(st, ph)) {
+        const int ci = chunk_at(c), len = rows_of(ci);
+        if (c >= C::kStages && !(ok = wait(b_empty + st, ph ^ 1u))) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(b_full + st, bytes);
           *s_issued = c + 1;
@@ -437,146 +470,154 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
           const long long sum = scan_pairs(x0, x1);
           all = __shfl_sync(0xffffffffu, sum, 31);
           const long long mid = __shfl_sync(0xffffffffu, sum, 15);      // up to token 31
-          // weights as one product about token 31 while neither half decays by more than 2^-60
-          const long long lim = 60ll << 32;
-          const bool plain = mid >= -lim && all - mid >= -lim;
+          const long long lim = 100ll << 32;
+          const int mode = all >= -lim ? kWhole : mid >= -lim && all - mid >= -lim ? kBlocks : kPairs;
+          // where a block's factors start from: forwards its first token's past, backwards its end
+          const long long ref = mode == kWhole ? (rev ? all : 0) : (lane < 16) == rev ? mid : rev ? all : 0;
           float *gt = gates(st);
-          float2 rf, tf, ra, cb;
-          auto one = [&](long long G, int i, float &r, float &t, float &a, float &b) {
+          float2 rf, tf, cb, rb, cr;
+          auto one = [&](long long G, int i, float &r, float &t, float &c, float &b, float &x) {
             const float since = exp2_fixed(G), until = exp2_fixed(all - G);
             r = rev ? until : since;
             t = i < len ? (rev ? since : until) : 0.f;
             if (KIND == kStates) return;
-            const float up = exp2_fixed(G - mid), down = exp2_fixed(mid - G);
-            a = plain ? (rev ? down : up) : 1.f;
-            b = plain ? (rev ? up : down) : i < 32 ? down : up;   // (to / from token 31)
+            c = exp2_fixed(rev ? G - ref : ref - G);
+            b = exp2_fixed(rev ? ref - G : G - ref);
+            x = exp2_fixed(i < 32 ? mid - G : G - mid);
           };
-          one(sum - x1, 2 * lane, rf.x, tf.x, ra.x, cb.x);
-          one(sum, 2 * lane + 1, rf.y, tf.y, ra.y, cb.y);
+          one(sum - x1, 2 * lane, rf.x, tf.x, cb.x, rb.x, cr.x);
+          one(sum, 2 * lane + 1, rf.y, tf.y, cb.y, rb.y, cr.y);
           reinterpret_cast<float2 *>(gt)[lane] = rf;
           reinterpret_cast<float2 *>(gt + 64)[lane] = tf;
           if (KIND != kStates) {
-            reinterpret_cast<float2 *>(gt + 128)[lane] = ra;
-            reinterpret_cast<float2 *>(gt + 192)[lane] = cb;
-            reinterpret_cast<longlong2 *>(gt + 256)[lane] = make_longlong2(sum - x1, sum);
+            reinterpret_cast<float2 *>(gt + 128)[lane] = cb;
+            reinterpret_cast<float2 *>(gt + 192)[lane] = rb;
+            reinterpret_cast<float2 *>(gt + 256)[lane] = cr;
+            reinterpret_cast<longlong2 *>(gt + 320)[lane] = make_longlong2(sum - x1, sum);
           }
           if (lane == 0) {
-            gt[384] = exp2_fixed(all);
-            gt[385] = plain ? 1.f : 0.f;
+            gt[448] = exp2_fixed(all);
+            gt[449] = (float)mode;
           }
         }
         whole = max(whole + all, -(1ll << 52));
         __syncwarp();
         if (lane == 0) mbar_arrive(b_gate + st);
       }
-      done = c == nc;
       // (a backward walk's segments but the last belong to the forward walk too, which writes theirs)
       if (KIND == kStates && lane == 0 && (!rev || u.piece == u.pieces - 1))
         ps.decay[(size_t)blockIdx.x * p.H + h] = exp2_fixed(whole);
-    } else if (warp == 15) {
-      // -------------------------------------------------------------- issue of scores and O1
+    } else if (warp == 11) {
+      // -------------------------------------------------------------- issue of O
       if (KIND != kStates && lane == 0) {
-        const uint32_t id = idesc_bf16(128, 64, false, false);
-        auto tiles = [&](int c) {      // chunk c's tiles have landed (and rows past a ragged end are 0)
-          if (!need(b_full + c % C::kStages, c / C::kStages)) return false;
-          return rows_of(chunk_at(c)) == kC || need(b_zeroed, 0);
-        };
-        // sums over x channels, 16 at a time: of two K-major tiles, or of M's columns and a tile
-        const int kx = ps.dx / 16;
-        auto scores = [&](int c) {
-          uint64_t a = kmajor((c % C::kStages) * C::kStage + C::oX), b = kmajor((c % C::kStages) * C::kStage + C::oY);
-#pragma unroll 1
-          for (int k = 0; k < kx; ++k) {
-            mma_bf16_ss(tmem + C::cSc, a, b, id, k > 0);
-            const uint64_t step = k == 3 ? (kPanel >> 4) - 6 : 2;
-            a += step;
-            b += step;
-          }
-          mma_commit(b_sc);
-        };
-        auto out1 = [&](uint32_t m, uint64_t b, bool more) {
-#pragma unroll 1
-          for (int k = 0; k < kx; ++k) {
-            mma_bf16_ts(tmem + C::cO1, m, b, id, more || k > 0);
-            m += 8;
-            b += k == 3 ? (kPanel >> 4) - 6 : 2;
+        const uint32_t id1 = idesc_bf16(128, 64, false, false), id2 = idesc_bf16(128, 64, true, false);
+        // M's columns times X^T, 16 channels at a time
+        auto out1 = [&](uint32_t d, uint32_t m, uint64_t b, bool more) {
+          mma_bf16_ts(d, m, b, id1, more);
+          if (ps.dx >= 64) {
+#pragma unroll
+            for (int k = 1; k < 4; ++k) mma_bf16_ts(d, m + 8 * k, b + 2 * k, id1, true);
+            if (ps.dx == 128) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_bf16_ts(d, m + 32 + 8 * k, b + (kPanel >> 4) + 2 * k, id1, true);
+            }
+          } else if (ps.dx == 32) {
+            mma_bf16_ts(d, m + 8, b + 2, id1, true);
           }
         };
-        bool ok = tiles(0);
-        if (ok) {
+        for (; ok && c < nc; ++c, next(st, ph)) {
+          // (the outputs that were in this buffer have been read; X is there, for the scores read it)
+          const int ob = c & (C::kOBufs - 1);
+          if (!(ok = need(b_s, c) && (c < C::kOBufs || need(b_ofree + ob, (c - C::kOBufs) / C::kOBufs)))) break;
+          if (!(ok = need(b_full + st, ph) && need(b_gate + st, ph))) break;
           tc_fence_after();
-          scores(0);
-        }
-        for (int c = 0; ok && c < nc; ++c) {
-          if (!(ok = need(b_s, c) && (c == 0 || need(b_ofree, c - 1)))) break;
+          const uint64_t x = kmajor(st * C::kStage + C::oX);
+          const uint32_t d = tmem + C::cO + 64 * ob;
+          out1(d, tmem + C::cM, x, false);
+          if (exact) {
+            out1(d, tmem + C::cM + 64, x, true);
+            out1(d, tmem + C::cM + 128, x, true);
+          }
+          mma_commit(b_o1);
+          // the second part on top, or (weights not over the whole chunk) apart, in the one buffer
+          // there is: then the chunk before has been read too
+          const bool apart = gates(st)[449] != (float)kWhole;
+          if (!(ok = need(b_p, c) && (!apart || c == 0 || need(b_ofree + ((c - 1) & (C::kOBufs - 1)), (c - 1) / C::kOBufs))))
+            break;
           tc_fence_after();
-          const uint64_t x = kmajor((c % C::kStages) * C::kStage + C::oX);
-#pragma unroll 1
-          for (int t = 0; t < (exact ? 3 : 1); ++t) out1(tmem + C::cM + 64 * t, x, t > 0);
+          const uint64_t dz = mnmajor(st * C::kStage + C::oZ, kPanel), dp = kmajor(C::offP);
+          const uint32_t d2 = apart ? tmem + C::cO2 : d;
+          mma_bf16_ss(d2, dz, dp, id2, !apart);
+#pragma unroll
+          for (int k = 1; k < 4; ++k) mma_bf16_ss(d2, dz + 128 * k, dp + 2 * k, id2, true);
+          if (exact) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_bf16_ss(d2, dz + 128 * (k & 3), dp + (1 + (k >> 2)) * (kPanel >> 4) + 2 * (k & 3), id2, true);
+          }
           mma_commit(b_o + (c & 1));
-          mma_commit(b_empty + c % C::kStages);
-          if (c + 1 < nc) {
-            // (the scores of this chunk have been read)
-            if (!(ok = need(b_p + (c & 1), c >> 1) && tiles(c + 1))) break;
-            tc_fence_after();
-            scores(c + 1);
-          }
+          mma_commit(b_empty + st);
         }
-        done = ok;
         // every product issued has completed before the tensor memory is released
         mma_commit(b_drain);
         mbar_wait(b_drain, 0, kDrainNs);
       }
       __syncwarp();
     } else if (warp == 19) {
-      // -------------------------------------------------------------- issue of D and O2
+      // -------------------------------------------------------------- issue of scores and D
       if (lane == 0) {
-        const uint32_t id_d = idesc_bf16(128, ps.dx, true, true), id_o = idesc_bf16(128, 64, true, false);
-        bool ok = true;
-        for (int c = 0; ok && c < nc; ++c) {
-          const uint32_t st = (c % C::kStages) * C::kStage;
+        const uint32_t id_s = idesc_bf16(128, 64, false, false), id_d = idesc_bf16(128, ps.dx, true, true);
+        for (; ok && c < nc; ++c, next(st, ph)) {
+          if (KIND != kStates) {
+            // (tiles landed, rows past a ragged end 0, the scores before read)
+            if (!(ok = need(b_full + st, ph) && (rows_of(chunk_at(c)) == kC || need(b_zeroed, 0)) &&
+                       (c == 0 || need(b_p, c - 1))))
+              break;
+            tc_fence_after();
+            const uint64_t a = kmajor(st * C::kStage + C::oX), b = kmajor(st * C::kStage + C::oY);
+            mma_bf16_ss(tmem + C::cSc, a, b, id_s, false);
+            if (ps.dx >= 64) {
+#pragma unroll
+              for (int k = 1; k < 4; ++k) mma_bf16_ss(tmem + C::cSc, a + 2 * k, b + 2 * k, id_s, true);
+              if (ps.dx == 128) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_bf16_ss(tmem + C::cSc, a + (kPanel >> 4) + 2 * k, b + (kPanel >> 4) + 2 * k, id_s, true);
+              }
+            } else if (ps.dx == 32) {
+              mma_bf16_ss(tmem + C::cSc, a + 2, b + 2, id_s, true);
+            }
+            mma_commit(b_sc);
+          }
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
-            if (!(ok = need(b_w + half, c) && (half || c == 0 || need(b_dfree, c - 1)))) break;
+            const int hh = 2 * c + half, slot = hh % C::kTokBufs;
+            if (!(ok = need(b_w + slot, hh / C::kTokBufs) && (half || c == 0 || need(b_dfree, c - 1)))) break;
             tc_fence_after();
-            const uint64_t dy = mnmajor(st + C::oY) + 256 * half, dw = mnmajor(C::offTok) + 256 * half;
-#pragma unroll 1
-            for (int m = 0; m < 3; ++m)
+            const uint64_t dy = mnmajor(st * C::kStage + C::oY, kPanel) + 256 * half;
+            const uint64_t dw = mnmajor(C::offTok + slot * kTokB, kPanel / 2);
+            mma_bf16_ss(tmem + C::cD, dw, dy, id_d, half > 0);
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
-                mma_bf16_ss(tmem + C::cD, dw + m * (kTileB >> 4) + 128 * k, dy + 128 * k, id_d, half + m + k > 0);
-            mma_commit(b_wfree + half);
+            for (int m = 1; m < 6; ++m)              // (m >> 1)-th term, 16 tokens
+              mma_bf16_ss(tmem + C::cD, dw + (m >> 1) * (kPanel >> 4) + 128 * (m & 1), dy + 128 * (m & 1), id_d, true);
+            mma_commit(b_wfree + slot);
           }
           if (!ok) break;
           mma_commit(b_d);
-          if (KIND != kStates) {
-            if (!(ok = need(b_p + (c & 1), c >> 1) && (c == 0 || need(b_ofree, c - 1)))) break;
-            tc_fence_after();
-            const uint64_t dz = mnmajor(st + C::oZ);
-            const uint64_t dp = kmajor(C::offP + (C::kPBufs > 1 ? (c & 1) * C::kP : 0));
-#pragma unroll 1
-            for (int t = 0; t < (exact ? 3 : 1); ++t)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_bf16_ss(tmem + C::cO2, dz + 128 * k, dp + t * (kPanel >> 4) + 2 * k, id_o, t + k > 0);
-            mma_commit(b_o + (c & 1));
-          }
-          mma_commit(b_empty + c % C::kStages);
+          mma_commit(b_empty + st);
         }
-        done = ok;
         mma_commit(b_drain + 1);
         mbar_wait(b_drain + 1, 0, kDrainNs);
       }
       __syncwarp();
-    } else if (warp >= C::kTokWarp && warp < C::kTokWarp + C::kTokWarps) {
+    } else if (is_tok) {
       // -------------------------------------------------------------- tokf Z in three bf16 terms
-      constexpr int kT = 32 * C::kTokWarps;
-      const int t = tid - 32 * C::kTokWarp, n = 256 * ((ps.dz + 63) / 64);   // 16-byte pieces of half a tile
-      int c = 0;
-      for (; c < nc; ++c) {
-        const int st = c % C::kStages, len = rows_of(chunk_at(c));
+      const int kT = 32 * tok_warps;
+      const int t = 32 * tok_index + lane, n = 256 * ((ps.dz + 63) / 64);   // 16-byte pieces of half a tile
+      for (; c < nc; ++c, next(st, ph)) {
+        const int len = rows_of(chunk_at(c));
         uint8_t *base = sm + st * C::kStage;
-        if (!wait(b_full + st, c / C::kStages)) break;
+        if (!(ok = wait(b_full + st, ph))) break;
         if (len < kC) {
           // a ragged end: the rows that follow belong to another sequence
           for (int i = t; i < (int)(C::kStage / 16); i += kT)
@@ -584,21 +625,21 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(b_zeroed);
-          if (!wait(b_zeroed, 0)) break;
+          if (!(ok = wait(b_zeroed, 0))) break;
         }
-        if (!wait(b_gate + st, c / C::kStages)) break;
+        if (!(ok = wait(b_gate + st, ph))) break;
         const float *tokf = gates(st) + 64;
-        const uint4 *src = reinterpret_cast<const uint4 *>(base + C::oZ);
-        uint4 *dst = reinterpret_cast<uint4 *>(sm + C::offTok);
-        bool ok = true;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          if (c > 0 && !(ok = wait(b_wfree + half, c - 1))) break;
+          const int hh = 2 * c + half, slot = hh % C::kTokBufs;
+          if (hh >= C::kTokBufs && !(ok = wait(b_wfree + slot, hh / C::kTokBufs - 1))) break;
+          const uint4 *src = reinterpret_cast<const uint4 *>(base + C::oZ) + 256 * half;
+          uint4 *dst = reinterpret_cast<uint4 *>(sm + C::offTok + slot * kTokB);
 #pragma unroll 1
           for (int v = t; v < n; v += kT) {
-            const int i = v + 256 * half + (v & 256);                        // panel v / 256, this half's rows
-            const uint64_t w = f2pk(tokf[i >> 3 & 63], tokf[i >> 3 & 63]);
-            const uint4 z = src[i];
+            const float f = tokf[32 * half + (v >> 3 & 31)];
+            const uint64_t w = f2pk(f, f);
+            const uint4 z = src[v + (v & 256)];                              // panel v / 256, this half's rows
             const uint32_t zi[4] = {z.x, z.y, z.z, z.w};
             uint32_t r[3][4];
 #pragma unroll
@@ -612,75 +653,67 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             }
 #pragma unroll
             for (int t3 = 0; t3 < 3; ++t3)
-              dst[t3 * (kTileB / 16) + i] = make_uint4(r[t3][0], r[t3][1], r[t3][2], r[t3][3]);
+              dst[t3 * (kPanel / 16) + v] = make_uint4(r[t3][0], r[t3][1], r[t3][2], r[t3][3]);
           }
           fence_proxy_async();
           __syncwarp();
-          if (lane == 0) mbar_arrive(b_w + half);
+          if (lane == 0) mbar_arrive(b_w + slot);
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(b_empty + st);
       }
-      done = c == nc;
-    } else if (KIND != kStates && warp >= 12 && warp < 14) {
-      // -------------------------------------------------------------- scores (warps 12, 13)
-      const int wr = warp - 12, row = 32 * wr + lane;
-      const uint32_t lanes = tmem + ((uint32_t)(32 * wr) << 16);
-      const int other = rev ? 1 : 0;               // the column block a causal off-diagonal block has
-      int c = 0;
-      for (; c < nc; ++c) {
-        const int st = c % C::kStages;
-        if (!wait(b_gate + st, c / C::kStages)) break;
-        if (!wait(b_sc, c)) break;
-        tc_fence_after();
-        // (the scores two chunks back, or one, have been read)
-        if (c >= C::kPBufs && !wait(b_o + ((c - C::kPBufs) & 1), (c - C::kPBufs) >> 1)) break;
+    } else if (is_score) {
+      // -------------------------------------------------------------- scores, a 32 x 32 block each
+      const int rb = warp & 3, row = 32 * rb + lane;               // rows (TMEM lanes) of the block
+      const int cb = warp < 12 ? rb : 1 - rb;                      // its columns: the diagonal, or the causal other
+      const uint32_t lanes = tmem + ((uint32_t)(32 * rb) << 16);
+      uint8_t *P = sm + C::offP + row * 128;
+      const uint32_t mask = cb != rb ? ~0u : rev ? ~0u << lane : ~0u >> (31 - lane);   // the causal columns
+      for (; c < nc; ++c, next(st, ph)) {
+        if (!(ok = wait(b_gate + st, ph))) break;
         const float *gt = gates(st);
-        uint8_t *P = sm + C::offP + (C::kPBufs > 1 ? (c & 1) * C::kP : 0) + row * 128;
-        const bool plain = gt[385] != 0.f;
-        const float scale = plain ? 1.f : gt[192 + row];
-        const uint64_t mine = f2pk(scale, scale);
-        const long long *G = reinterpret_cast<const long long *>(gt + 256);
+        const int mode = (int)gt[449];
+        if (!(ok = wait(b_sc, c))) break;
+        if (c > 0 && !(ok = wait(b_o + ((c - 1) & 1), (c - 1) >> 1))) break;   // (the scores before have been read)
+        tc_fence_after();
+        if (mode == kPairs && cb == rb) {                          // every weight from its own difference of sums
+          const long long *G = reinterpret_cast<const long long *>(gt + 320);
+          const long long me = G[row];
 #pragma unroll 1
-        for (int b = wr == other ? wr : 0; b < (wr == other ? wr + 1 : 2); ++b) {
-          if (!plain && b == wr) {                  // every weight from its own difference of sums
-            const long long me = G[row];
-#pragma unroll 1
-            for (int j = 0; j < 32; ++j) {
-              uint32_t s1;
-              tmem_ld1(lanes + C::cSc + 32 * b + j, s1);
-              tmem_wait_ld();
-              const long long o = G[32 * b + j];
-              float x = (rev ? j >= lane : j <= lane) ? __uint_as_float(s1) * exp2_fixed(rev ? o - me : me - o) : 0.f;
+          for (int j = 0; j < 32; ++j) {
+            uint32_t s1;
+            tmem_ld1(lanes + C::cSc + 32 * cb + j, s1);
+            tmem_wait_ld();
+            const long long o = G[32 * cb + j];
+            float x = mask >> j & 1 ? __uint_as_float(s1) * exp2_fixed(rev ? o - me : me - o) : 0.f;
 #pragma unroll
-              for (int t = 0; t < C::kTerms; ++t) {
-                const __nv_bfloat16 v = __float2bfloat16_rn(x);
-                *reinterpret_cast<__nv_bfloat16 *>(P + t * kPanel + (((4 * b + j / 8) ^ (row & 7)) << 4) + 2 * (j & 7)) = v;
-                x -= __bfloat162float(v);
-              }
+            for (int t = 0; t < C::kTerms; ++t) {
+              const __nv_bfloat16 v = __float2bfloat16_rn(x);
+              *reinterpret_cast<__nv_bfloat16 *>(P + t * kPanel + (((4 * cb + j / 8) ^ (row & 7)) << 4) + 2 * (j & 7)) = v;
+              x -= __bfloat162float(v);
             }
-            continue;
           }
-          // the diagonal block's causal columns
-          const uint32_t mask = b != wr ? ~0u : rev ? ~0u << lane : ~0u >> (31 - lane);
+        } else {
+          const float *col = gt + (mode == kWhole || cb == rb ? 128 : 256);
+          const float scale = mode == kWhole ? 1.f : cb == rb ? gt[192 + row] : gt[256 + row];
+          const uint64_t mine = f2pk(scale, scale);
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
-            const int j0 = 32 * b + 8 * q;
+            const int j0 = 32 * cb + 8 * q;
             const uint32_t m = mask >> (8 * q);
             uint32_t s[8];
             tmem_ld8(lanes + C::cSc + j0, s);
-            const float4 f0 = *reinterpret_cast<const float4 *>(gt + 192 + j0);
-            const float4 f1 = *reinterpret_cast<const float4 *>(gt + 192 + j0 + 4);
+            const float4 f0 = *reinterpret_cast<const float4 *>(col + j0);
+            const float4 f1 = *reinterpret_cast<const float4 *>(col + j0 + 4);
             const uint64_t f[4] = {f2pk(f0.x, f0.y), f2pk(f0.z, f0.w), f2pk(f1.x, f1.y), f2pk(f1.z, f1.w)};
             tmem_wait_ld();
             uint32_t r[C::kTerms][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              // (`mine` is 1 but off the diagonal block through token 31; the mask selects, so that
-              // an infinite weight on the acausal side vanishes)
-              float a, c1;
-              f2up(f2mul(f2bits(s[2 * j], s[2 * j + 1]), f2mul(f[j], mine)), a, c1);
-              uint64_t x = f2pk(m & (1u << (2 * j)) ? a : 0.f, m & (2u << (2 * j)) ? c1 : 0.f);
+              // (the mask selects, so that whatever stands on the acausal side vanishes)
+              float a, b;
+              f2up(f2mul(f2bits(s[2 * j], s[2 * j + 1]), f2mul(f[j], mine)), a, b);
+              uint64_t x = f2pk(m & (1u << (2 * j)) ? a : 0.f, m & (2u << (2 * j)) ? b : 0.f);
               r[0][j] = pack_bf16(x);
               if constexpr (KIND == kGrad) {
                 if (!exact) continue;
@@ -704,104 +737,161 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(b_p + (c & 1));
+          mbar_arrive(b_p);
           mbar_arrive(b_empty + st);
         }
       }
-      done = c == nc;
-    } else if (KIND != kStates && warp < 12) {
-      // -------------------------------------------------------------- outputs (warps 4-11)
-      const int quad = warp & 3, hf = (warp >> 2) - 1;
-      const int z = 32 * quad + lane;
+    } else if (KIND != kStates && warp < 8) {
+      // -------------------------------------------------------------- outputs (warps 4-7)
+      // A warp holds 32 channels.  It reads O in 8 x 8 blocks, which are bf16 matrix fragments once
+      // two tokens are packed into a register, so four transposing stores put 32 channels of 8
+      // tokens into rows.  Whole chunks leave as two TMA stores a warp, through two buffers of its
+      // own (a store is read out of shared memory only when the loads issued before it have
+      // been, some 2,800 cycles later).
+      const int quad = warp & 3;
       const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-      float *red = reinterpret_cast<float *>(sm + C::offDot);      // [2][2 halves][4 quads][32]
-      const size_t ostr = (size_t)(ps.part ? p.H : ps.ho) * ps.dz;
-      int c = 0;
-      for (; c < nc; ++c) {
-        const int st = c % C::kStages, ci = chunk_at(c), len = rows_of(ci);
+      float *red = reinterpret_cast<float *>(sm + C::offDot);      // [2][4 quads][64]
+      const uint32_t mine = sb + C::offOut + (warp - 4) * 4096;
+      const int ch = 32 * quad + (lane >> 2), tk = 2 * (lane & 3); // this lane's first channel and token in a block
+      const bool any = 32 * quad < ps.dz && ps.out;
+      for (; c < nc; ++c, next(st, ph)) {
+        const int ci = chunk_at(c), len = rows_of(ci), ob = c & (C::kOBufs - 1);
         const float *gt = gates(st);
-        if (!wait(b_gate + st, c / C::kStages)) break;
-        if (!wait(b_o + (c & 1), c >> 1)) break;
+        const bool tma = len == kC && any && !(KIND == kGrad && ps.part);
+        if (!(ok = wait(b_gate + st, ph))) break;
+        const bool apart = gt[449] != (float)kWhole;
+        if (!(ok = wait(b_o + (c & 1), c >> 1))) break;
         tc_fence_after();
-        const size_t o0 = (size_t)(u.row0 + ci * kC + 32 * hf) * ostr + (size_t)h * ps.dz + z;
-        int lim = z < ps.dz && ps.out ? len - 32 * hf : 0;
-        const uint8_t *wt = sm + st * C::kStage + C::oW + (z >> 6) * kPanel + (32 * hf) * 128;
-        float *of = static_cast<float *>(ps.out) + o0;
-        __nv_bfloat16 *ob = static_cast<__nv_bfloat16 *>(ps.out) + o0;
-        float sums = 0.f;
+        float *rd = red + (c & 1) * 256 + quad * 64;
 #pragma unroll 1
-        for (int b = 0; b < 2; ++b, lim -= 16) {
-          uint32_t r1[16], r2[16];
-          tmem_ld16(lanes + C::cO1 + 32 * hf + 16 * b, r1);
-          tmem_ld16(lanes + C::cO2 + 32 * hf + 16 * b, r2);
+        for (int g = 0; g < 2; ++g) {                               // 32 tokens
+          uint32_t r[2][16];                                        // channels 0-15, 16-31
+          tmem_ld_blocks(lanes + C::cO + 64 * ob + 32 * g, r[0]);
+          tmem_ld_blocks(lanes + (16u << 16) + C::cO + 64 * ob + 32 * g, r[1]);
           tmem_wait_ld();
-          if (b == 1) {
+          uint64_t f[4];                                            // rowf of this lane's two tokens a block
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 x = *reinterpret_cast<const float2 *>(gt + 32 * g + 8 * k + tk);
+            f[k] = f2pk(x.x, x.y);
+          }
+          uint64_t v[2][8];                                         // [.][2 k + m]: block k, channel ch + 8 m (+ 16)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[y][i] = f2mul(f[i >> 1], f2bits(r[y][2 * i], r[y][2 * i + 1]));
+          if (apart) {
+#pragma unroll 1
+            for (int y = 0; y < 2; ++y) {
+              uint32_t r2[16];
+              tmem_ld_blocks(lanes + ((16u * y) << 16) + C::cO2 + 32 * g, r2);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint64_t b = f2bits(r2[2 * i], r2[2 * i + 1]);
+                if (y == 0) v[0][i] = f2add(v[0][i], b);
+                else v[1][i] = f2add(v[1][i], b);
+              }
+            }
+          }
+          if (g == 1) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(b_ofree);
+            if (lane == 0) mbar_arrive(b_ofree + ob);
           }
-          const float4 *rf = reinterpret_cast<const float4 *>(gt + 32 * hf + 16 * b);
-          const float4 *ra = reinterpret_cast<const float4 *>(gt + 128 + 32 * hf + 16 * b);
-          float v[16];
+          if (tma) {
+            // (the store before the last has been read)
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            __syncwarp();
+            // rows of 64 bytes, 16-byte pieces permuted by row / 2 % 4 (64-byte swizzle)
+            const int row = lane & 7;
+            const uint32_t at = mine + 2048 * g + row * 64 + (((lane >> 3) ^ (row >> 1)) << 4);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 f = rf[i], e = ra[i];
-            f2up(f2fma(f2pk(e.x, e.y), f2bits(r2[4 * i], r2[4 * i + 1]),
-                       f2mul(f2pk(f.x, f.y), f2bits(r1[4 * i], r1[4 * i + 1]))), v[4 * i], v[4 * i + 1]);
-            f2up(f2fma(f2pk(e.z, e.w), f2bits(r2[4 * i + 2], r2[4 * i + 3]),
-                       f2mul(f2pk(f.z, f.w), f2bits(r1[4 * i + 2], r1[4 * i + 3]))), v[4 * i + 2], v[4 * i + 3]);
-          }
-          if (KIND == kGrad && ps.part) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i, of += ostr)
-              if (i < lim) *of = v[i];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i, ob += ostr)
-              if (i < lim) *ob = __float2bfloat16_rn(v[i]);
-          }
-          if (exact) {
+            for (int k = 0; k < 4; ++k)
+              stmatrix4_t(at + 512 * k, pack_bf16(v[0][2 * k]), pack_bf16(v[0][2 * k + 1]), pack_bf16(v[1][2 * k]),
+                          pack_bf16(v[1][2 * k + 1]));
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&p.outs[blockIdx.z], sm + (mine - sb) + 2048 * g, 32 * quad, h, (int)(u.row0 + ci * kC + 32 * g));
+              bulk_commit();
+            }
+          } else if (any) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const int t = 16 * b + i;
-              const float w = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(
-                  wt + t * 128 + (((z & 63) * 2) ^ ((i & 7) << 4))));
-              v[i] = z < ps.dz ? v[i] * w : 0.f;
+              const int t = 32 * g + 8 * ((i & 7) >> 1) + tk, z = ch + 8 * (i & 1) + 16 * (i >> 3);
+              float a, b;
+              f2up(v[i >> 3][i & 7], a, b);
+              const size_t at = ((size_t)(u.row0 + ci * kC + t) * p.H + h) * ps.dz + z, step = (size_t)p.H * ps.dz;
+              if (z >= ps.dz) continue;
+              if (KIND == kGrad && ps.part) {
+                if (t < len) static_cast<float *>(ps.out)[at] = a;
+                if (t + 1 < len) static_cast<float *>(ps.out)[at + step] = b;
+              } else {
+                if (t < len) static_cast<__nv_bfloat16 *>(ps.out)[at] = __float2bfloat16_rn(a);
+                if (t + 1 < len) static_cast<__nv_bfloat16 *>(ps.out)[at + step] = __float2bfloat16_rn(b);
+              }
             }
-            const float s = lane_sums16(v);
-            if ((lane >> 4) == b) sums = s;         // lane t holds token t of this half
+          }
+          if (exact) {
+            // this lane's products with W, 8 tokens, summed over its channels; then over the lanes
+            // that hold the same tokens (bits 2-4), each of which ends up with one
+            const uint32_t wt = sb + st * C::kStage + C::oW + (quad >> 1) * kPanel;
+            uint64_t d[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row = 32 * g + 8 * k + (lane & 7);
+              uint32_t w[4];
+              ldmatrix4_t(wt + row * 128 + (((4 * (quad & 1) + (lane >> 3)) ^ (row & 7)) << 4), w);
+              d[k] = 0;
+#pragma unroll
+              for (int m = 0; m < 4; ++m)
+                if (32 * quad + 8 * m < ps.dz) d[k] = f2fma(v[m >> 1][2 * k + (m & 1)], unpack_bf16(w[m]), d[k]);
+            }
+            float s8[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f2up(d[k], s8[2 * k], s8[2 * k + 1]);
+#pragma unroll
+            for (int step = 4; step >= 1; step >>= 1) {
+              const bool up = lane & (4 * step);
+#pragma unroll
+              for (int i = 0; i < step; ++i) {
+                const float send = up ? s8[i] : s8[i + step], keep = up ? s8[i + step] : s8[i];
+                s8[i] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * step);
+              }
+            }
+            rd[32 * g + 8 * (lane >> 3) + tk + (lane >> 2 & 1)] = s8[0];
           }
         }
         if (exact) {
-          float *rd = red + ((c & 1) * 2 + hf) * 128;
-          rd[quad * 32 + lane] = sums;
           __syncwarp();
-          if (lane == 0) mbar_arrive(b_red + hf);
+          // (two barriers: a warp may be a chunk ahead of another that waits for its store)
+          if (lane == 0) mbar_arrive(b_red + (c & 1));
           if (quad == 0) {
-            if (!wait(b_red + hf, c)) break;
-            if (32 * hf + lane < len)
-              ps.dots[(size_t)h * p.rows + u.row0 + ci * kC + 32 * hf + lane] =
-                  (rd[lane] + rd[32 + lane]) + (rd[64 + lane] + rd[96 + lane]);
+            if (!(ok = wait(b_red + (c & 1), c >> 1))) break;
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+              if (32 * g + lane < len)
+                ps.dots[(size_t)h * p.rows + u.row0 + ci * kC + 32 * g + lane] =
+                    (rd[32 * g + lane] + rd[64 + 32 * g + lane]) + (rd[128 + 32 * g + lane] + rd[192 + 32 * g + lane]);
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(b_empty + st);
       }
-      done = c == nc;
-    } else {
-      done = true;                                  // (a role this launch has no use for)
+      if (lane == 0) bulk_wait_all();
     }
   }
-  if (!done && (lane == 0 || warp < 4)) give_up(s_abort, p.status);
+  if (!ok) give_up(s_abort, p.status);
   tc_fence_before();
   __syncthreads();
   if (tid == 0) {
     // loads that a role which gave up did not wait for have landed
-    for (int c = max(0, *s_issued - C::kStages); c < *s_issued; ++c)
-      mbar_wait(b_full + c % C::kStages, (c / C::kStages) & 1, kDrainNs);
+    for (int i = max(0, *s_issued - C::kStages); i < *s_issued; ++i)
+      mbar_wait(b_full + i % C::kStages, (i / C::kStages) & 1, kDrainNs);
   }
   __syncthreads();
-  if (warp == 15) {
+  if (warp == 11) {
     tc_fence_after();
     tmem_dealloc(*s_tmem, 512);
   }
@@ -920,17 +1010,19 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   }();
   return fn;
 }
-// [rows, heads, d] bf16 as (channel, head, token), box 64 x 1 x 64, 128-byte swizzle; channels
-// past d and tokens past rows read as 0
-bool make_map(CUtensorMap *map, const void *base, int heads, long rows, int d) {
+// [rows, heads, d] bf16 as (channel, head, token): loads take boxes of 64 x 1 x 64, 128-byte
+// swizzle (channels past d and tokens past rows read as 0), stores of 32 x 1 x 32, 64-byte swizzle
+bool make_map(CUtensorMap *map, const void *base, int heads, long rows, int d, bool store = false) {
   auto enc = encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
   cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
-  cuuint32_t box[3] = {64, 1, 64}, estr[3] = {1, 1, 1};
+  const cuuint32_t side = store ? 32 : 64;
+  cuuint32_t box[3] = {side, 1, side}, estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             store ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             store ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 constexpr int kSMs = 148;
@@ -1055,7 +1147,8 @@ int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
     Pass &f = p.pass[0];
     f.ix = 0; f.iy = 1; f.iz = 2; f.iw = -1;
     f.hx = a.Hq; f.hy = a.Hk; f.hz = a.Hv; f.dx = a.dk; f.dz = a.dv; f.sz = 1; f.sx = a.dv;
-    f.init = a.S0; f.seg_in = l.seg ? segS : nullptr; f.end = a.S_T; f.out = a.o; f.ho = a.H;
+    f.init = a.S0; f.seg_in = l.seg ? segS : nullptr; f.end = a.S_T; f.out = a.o;
+    if (a.o && !make_map(&p.outs[0], a.o, a.H, rows, a.dv, true)) return CKDA_ERR_CUDA;
     return launch<kOut>(p, dim3(slots, H, 1), s) ? CKDA_OK : CKDA_ERR_CUDA;
   }
   const bool part_q = a.Hq < a.H, part_k = a.Hk < a.H, part_v = a.Hv < a.H;
@@ -1064,22 +1157,24 @@ int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
   pq.ix = 3; pq.iy = 2; pq.iz = 1; pq.iw = 0;
   pq.hx = a.H; pq.hy = a.Hv; pq.hz = a.Hk; pq.hw = a.Hq; pq.dx = a.dv; pq.dz = a.dk;
   pq.sz = a.dv; pq.sx = 1; pq.seg_in = segS; pq.end_slot = segS;
-  pq.part = part_q; pq.out = part_q ? a.ws + l.pq : static_cast<uint8_t *>(b->dq); pq.ho = a.Hq;
+  pq.part = part_q; pq.out = part_q ? a.ws + l.pq : static_cast<uint8_t *>(b->dq);
   pq.dots = rho;
   Pass &pk = p.pass[1];
   pk = pq;
   pk.ix = 2; pk.iy = 3; pk.iz = 0; pk.iw = 1;
   pk.hx = a.Hv; pk.hy = a.H; pk.hz = a.Hq; pk.hw = a.Hk; pk.rev = 1;
   pk.seg_in = segX; pk.end_slot = nullptr;
-  pk.part = part_k; pk.out = part_k ? a.ws + l.pk : static_cast<uint8_t *>(b->dk); pk.ho = a.Hk;
+  pk.part = part_k; pk.out = part_k ? a.ws + l.pk : static_cast<uint8_t *>(b->dk);
   pk.dots = kappa;
   Pass &pv = p.pass[2];
   pv = pk;
   pv.ix = 1; pv.iy = 0; pv.iz = 3; pv.iw = -1;
   pv.hx = a.Hk; pv.hy = a.Hq; pv.hz = a.H; pv.dx = a.dk; pv.dz = a.dv; pv.sz = 1; pv.sx = a.dv;
   pv.end = b->dS0;
-  pv.part = part_v; pv.out = part_v ? a.ws + l.pv : static_cast<uint8_t *>(b->dv); pv.ho = a.Hv;
+  pv.part = part_v; pv.out = part_v ? a.ws + l.pv : static_cast<uint8_t *>(b->dv);
   pv.dots = nullptr;
+  for (int i = 0; i < 3; ++i)      // (a shared head's gradient goes through fp32 sums instead)
+    if (!p.pass[i].part && !make_map(&p.outs[i], p.pass[i].out, a.H, rows, p.pass[i].dz, true)) return CKDA_ERR_CUDA;
   if (!launch<kGrad>(p, dim3(slots, H, 3), s)) return CKDA_ERR_CUDA;
   DecayParams d = {};
   d.S = segS; d.X = segX; d.rho = rho; d.kappa = kappa;

@@ -22,7 +22,7 @@ namespace ckda {
 namespace {
 
 constexpr int kRotThreads = 256;
-constexpr int kRotItems = 4;       // items per thread held in registers at once
+constexpr int kRotItems = 2;       // items per thread held in registers at once
 constexpr int kRotTable = 2048;    // table entries (tokens of a block x frequencies)
 
 struct FastDiv {                   // n / d for n < 2^31 by one multiplication
@@ -57,7 +57,7 @@ struct alignas(sizeof(T) * V) Vec {
 // with the one of their partners (half layout), or one vector of adjacent pairs (interleaved,
 // V >= 2; V = 1 takes its two channels one by one), or one vector of copied channels.
 template <typename T, int V>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotParams p) {
+__global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const RotParams p) {
   __shared__ float2 table[kRotTable];
   const long t0 = (long)blockIdx.x * p.tokens;
   const int nt = (int)(p.n - t0 < p.tokens ? p.n - t0 : p.tokens);

@@ -334,68 +334,107 @@ def workspace_status(workspace: torch.Tensor) -> int:
 
 
 # ------------------------------------------------------------------ linear attention
-def _lin_heads(g, lead, **tensors):
+# These calls are short (a token of a small batch takes microseconds on the device), so their checks
+# build no message and no tuple unless one fails.
+def _lin_heads(g, lead, named):
     """(H, decay code, [heads of each tensor]) of linear attention tensors [*lead, Hx, d]."""
-    _need(g.dtype == torch.float32 and (g.dim() == 1 or (g.dim() == len(lead) + 1
-                                                         and tuple(g.shape[:-1]) == lead)),
-          f"g must be {lead + ('H',)} or [H] float32, got {tuple(g.shape)}, {g.dtype}")
+    n = len(lead)
+    if g.dtype != torch.float32 or not (g.dim() == 1 or (g.dim() == n + 1 and g.shape[:-1] == lead)):
+        raise ValueError(f"g must be {tuple(lead) + ('H',)} or [H] float32, got {tuple(g.shape)}, {g.dtype}")
     H = g.shape[-1]
-    _need(H >= 1, "g has no heads")
+    if H < 1:
+        raise ValueError("g has no heads")
     heads = []
-    for name, t in tensors.items():
-        _need(t.dim() == len(lead) + 2 and tuple(t.shape[:-2]) == lead,
-              f"{name} must be {lead + ('heads', 'channels')}, got {tuple(t.shape)}")
-        _need(t.shape[-2] >= 1 and H % t.shape[-2] == 0,
-              f"{name} has {t.shape[-2]} heads, which must divide g's {H}")
-        heads.append(t.shape[-2])
+    for name, t in named:
+        s = t.shape
+        if len(s) != n + 2 or s[:-2] != lead:
+            raise ValueError(f"{name} must be {tuple(lead) + ('heads', 'channels')}, got {tuple(s)}")
+        if s[-2] < 1 or H % s[-2]:
+            raise ValueError(f"{name} has {s[-2]} heads, which must divide g's {H}")
+        heads.append(s[-2])
     return H, (DECAY_PER_HEAD if g.dim() == 1 else DECAY_PER_TOKEN), heads
 
 
 def _lin_types(q, k, v):
-    _need(q.dtype in _DT, f"q must be float32 or bfloat16, got {q.dtype}")
-    _need(k.dtype == q.dtype and v.dtype == q.dtype,
-          f"k and v must be in q's dtype {q.dtype}, got {k.dtype}, {v.dtype}")
-    _need(k.shape[-1] == q.shape[-1], f"q has {q.shape[-1]} channels, k {k.shape[-1]}")
+    if q.dtype not in _DT:
+        raise ValueError(f"q must be float32 or bfloat16, got {q.dtype}")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError(f"k and v must be in q's dtype {q.dtype}, got {k.dtype}, {v.dtype}")
+    if k.shape[-1] != q.shape[-1]:
+        raise ValueError(f"q has {q.shape[-1]} channels, k {k.shape[-1]}")
 
 
-def check_linattn_args(q, k, v, g, S0=None, cu_seqlens=None, **states):
-    """Shapes, dtypes and devices that ``ckda_linattn_fwd`` and ``ckda_linattn_bwd`` cannot see.
-    Raises ValueError; returns (N, H, decay code, (Hq, Hk, Hv))."""
-    _need(q.dim() == 4, f"q must be [B,T,Hq,dk], got {tuple(q.shape)}")
-    lead = tuple(q.shape[:2])
-    H, decay, heads = _lin_heads(g, lead, q=q, k=k, v=v)
+def _lin_out(name, t, shape, dtype):
+    """A given tensor's shape and dtype (None passes)."""
+    if t is not None and (t.shape != shape or t.dtype != dtype):
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)}, {t.dtype}")
+
+
+def check_linattn_args(q, k, v, g, S0=None, cu_seqlens=None):
+    """Shapes and dtypes that ``ckda_linattn_fwd`` and ``ckda_linattn_bwd`` cannot see.  Raises
+    ValueError; returns (N, H, decay code, (Hq, Hk, Hv))."""
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B,T,Hq,dk], got {tuple(q.shape)}")
+    lead = q.shape[:2]
+    H, decay, heads = _lin_heads(g, lead, (("q", q), ("k", k), ("v", v)))
     _lin_types(q, k, v)
     N = lead[0]
     if cu_seqlens is not None:
-        _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 1 and cu_seqlens.dtype == torch.int32,
-              "cu_seqlens must be a 1-D int32 tensor of N+1 offsets")
-        _need(lead[0] == 1, "packed sequences (cu_seqlens) need B == 1")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or cu_seqlens.dtype != torch.int32:
+            raise ValueError("cu_seqlens must be a 1-D int32 tensor of N+1 offsets")
+        if lead[0] != 1:
+            raise ValueError("packed sequences (cu_seqlens) need B == 1")
         N = cu_seqlens.numel() - 1
-        _need(N > 0 or lead[1] == 0, "cu_seqlens names no sequence")
-    shape = (N, H, q.shape[-1], v.shape[-1])
-    for name, t in (("S0", S0), *states.items()):
-        _need(t is None or (tuple(t.shape) == shape and t.dtype == torch.float32),
-              f"{name} must be [N,H,dk,dv] = {shape} float32")
-    _same_device(q, k=k, v=v, g=g, S0=S0, cu_seqlens=cu_seqlens, **states)
-    return N, H, decay, tuple(heads)
+        if N == 0 and lead[1] > 0:
+            raise ValueError("cu_seqlens names no sequence")
+    _lin_out("S0", S0, (N, H, q.shape[-1], v.shape[-1]), torch.float32)
+    return N, H, decay, heads
+
+
+def _addresses(dev, *named):
+    """Device addresses of contiguous tensors on ``dev`` (None: no address)."""
+    out, index = [], dev.index
+    for name, t in named:
+        if t is None:
+            out.append(None)
+        elif t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, q on {dev}")
+        elif not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        else:
+            out.append(t.data_ptr())
+    return out
 
 
 def _call(dev, name, *args):
     """Calls an entry point on ``dev`` and its current stream (the last argument)."""
-    if dev.type != "cuda":
-        raise ValueError("tensors must be on a CUDA device")
-    fn = getattr(load(), name)
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, _stream(dev))
+    fn = getattr(_lib or load(), name)
+    index = dev.index
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _stream(dev))
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != 0:
         raise CkdaError(name, rc)
 
 
+def _on_cuda(q):
+    if not q.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    return q.device
+
+
+def _room(dev, workspace, n):
+    """The workspace's address and bytes, allocated when not given (and then returned, to be kept
+    until the call has been issued)."""
+    if workspace is None:
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    return workspace, _addresses(dev, ("workspace", workspace))[0], workspace.numel() * workspace.element_size()
+
+
 def linattn_fwd_workspace_size(B, T, H, dk, dv, dtype, n_seqs=0) -> int:
-    return int(load().ckda_linattn_fwd_workspace_size(B, T, H, dk, dv, _DT[dtype], n_seqs))
+    return (_lib or load()).ckda_linattn_fwd_workspace_size(B, T, H, dk, dv, _DT[dtype], n_seqs)
 
 
 def linattn_fwd(q, k, v, g, S0=None, cu_seqlens=None, o=None, S_T=None, workspace=None,
@@ -406,29 +445,30 @@ def linattn_fwd(q, k, v, g, S0=None, cu_seqlens=None, o=None, S_T=None, workspac
     q [B,T,Hq,dk], k [B,T,Hk,dk], v [B,T,Hv,dv] in one dtype (float32 or bfloat16); g: log
     decays <= 0, float32 [B,T,H], or [H] for fixed ones; Hq, Hk and Hv divide H; S0 [N,H,dk,dv]
     float32 or None; cu_seqlens int32 [N+1] on the device (B == 1) or None.  o [B,T,H,dv]."""
-    N, H, decay, heads = check_linattn_args(q, k, v, g, S0, cu_seqlens, S_T=S_T)
+    N, H, decay, heads = check_linattn_args(q, k, v, g, S0, cu_seqlens)
     B, T, _, dk = q.shape
-    dv, dev, packed = v.shape[-1], q.device, cu_seqlens is not None
-    _need(o is None or (tuple(o.shape) == (B, T, H, dv) and o.dtype == q.dtype and o.device == dev),
-          f"o must be [B,T,H,dv] = {(B, T, H, dv)} in {q.dtype} on {dev}")
-    if want_o and o is None:
+    dv, n_seqs = v.shape[-1], 0 if cu_seqlens is None else N
+    _lin_out("o", o, (B, T, H, dv), q.dtype)
+    _lin_out("S_T", S_T, (N, H, dk, dv), torch.float32)
+    dev = _on_cuda(q)
+    if not want_o:
+        o = None
+    elif o is None:
         o = torch.empty((B, T, H, dv), dtype=q.dtype, device=dev)
-    if want_state and S_T is None:
+    if not want_state:
+        S_T = None
+    elif S_T is None:
         S_T = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
-    if workspace is None:
-        n = linattn_fwd_workspace_size(B, T, H, dk, dv, q.dtype, N if packed else 0)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    _need(workspace.device == dev, f"workspace is on {workspace.device}, q on {dev}")
-    _call(dev, "ckda_linattn_fwd", _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(cu_seqlens),
-          N if packed else 0, B, T, H, *heads, dk, dv, decay, _DT[q.dtype],
-          _ptr(o if want_o else None), _ptr(S_T if want_state else None), _ptr(workspace),
-          workspace.numel() * workspace.element_size())
-    return (o if want_o else None), (S_T if want_state else None)
+    workspace, wp, wn = _room(dev, workspace, linattn_fwd_workspace_size(B, T, H, dk, dv, q.dtype, n_seqs))
+    p = _addresses(dev, ("q", q), ("k", k), ("v", v), ("g", g), ("S0", S0), ("cu_seqlens", cu_seqlens),
+                   ("o", o), ("S_T", S_T))
+    _call(dev, "ckda_linattn_fwd", *p[:6], n_seqs, B, T, H, *heads, dk, dv, decay, _DT[q.dtype], *p[6:], wp, wn)
+    return o, S_T
 
 
 def linattn_bwd_workspace_size(B, T, H, Hq, Hk, Hv, dk, dv, decay, dtype, n_seqs=0) -> int:
-    return int(load().ckda_linattn_bwd_workspace_size(B, T, H, Hq, Hk, Hv, dk, dv, decay,
-                                                      _DT[dtype], n_seqs))
+    return (_lib or load()).ckda_linattn_bwd_workspace_size(B, T, H, Hq, Hk, Hv, dk, dv, decay,
+                                                            _DT[dtype], n_seqs)
 
 
 def linattn_bwd(q, k, v, g, S0=None, cu_seqlens=None, dO=None, dS_T=None, want_dS0: bool = True,
@@ -438,51 +478,52 @@ def linattn_bwd(q, k, v, g, S0=None, cu_seqlens=None, dO=None, dS_T=None, want_d
     Returns (dq, dk, dv, dg, dS0): dq, dk, dv as q, k, v; dg as g; dS0 [N,H,dk,dv] float32
     (None when not wanted).  dO [B,T,H,dv] in q's dtype or None (zero); dS_T [N,H,dk,dv]
     float32 or None (zero).  ``grads`` may supply the five output tensors."""
-    N, H, decay, heads = check_linattn_args(q, k, v, g, S0, cu_seqlens, dS_T=dS_T)
+    N, H, decay, heads = check_linattn_args(q, k, v, g, S0, cu_seqlens)
     B, T, _, dk = q.shape
-    dv, dev, packed = v.shape[-1], q.device, cu_seqlens is not None
-    _need(dO is None or (tuple(dO.shape) == (B, T, H, dv) and dO.dtype == q.dtype),
-          f"dO must be [B,T,H,dv] = {(B, T, H, dv)} in {q.dtype}")
+    dv, n_seqs, state = v.shape[-1], 0 if cu_seqlens is None else N, (N, H, dk, v.shape[-1])
+    _lin_out("dO", dO, (B, T, H, dv), q.dtype)
+    _lin_out("dS_T", dS_T, state, torch.float32)
+    if grads is not None:
+        for name, t, like in zip(("dq", "dk", "dv", "dg"), grads, (q, k, v, g)):
+            if t is None:
+                raise ValueError(f"{name} buffer missing")
+            _lin_out(name, t, like.shape, like.dtype)
+        if want_dS0 and grads[4] is None:
+            raise ValueError("dS0 buffer missing")
+        _lin_out("dS0", grads[4], state, torch.float32)
+    dev = _on_cuda(q)
     if grads is None:
-        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g),
-                 torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if want_dS0 else None)
-    gq, gk, gv, gg, gS0 = grads
-    for name, t, like in (("dq", gq, q), ("dk", gk, k), ("dv", gv, v), ("dg", gg, g)):
-        _need(t is not None and t.shape == like.shape and t.dtype == like.dtype,
-              f"{name} must be {tuple(like.shape)} in {like.dtype}")
-    _need(gS0 is None or (tuple(gS0.shape) == (N, H, dk, dv) and gS0.dtype == torch.float32),
-          f"dS0 must be [N,H,dk,dv] = {(N, H, dk, dv)} float32")
-    _need(gS0 is not None or not want_dS0, "dS0 buffer missing")
-    _same_device(q, dO=dO, dq=gq, dk=gk, dv=gv, dg=gg, dS0=gS0)
-    if workspace is None:
-        n = linattn_bwd_workspace_size(B, T, H, *heads, dk, dv, decay, q.dtype, N if packed else 0)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    _need(workspace.device == dev, f"workspace is on {workspace.device}, q on {dev}")
-    _call(dev, "ckda_linattn_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(cu_seqlens),
-          N if packed else 0, B, T, H, *heads, dk, dv, decay, _DT[q.dtype], _ptr(dO), _ptr(dS_T),
-          _ptr(gq), _ptr(gk), _ptr(gv), _ptr(gg), _ptr(gS0 if want_dS0 else None), _ptr(workspace),
-          workspace.numel() * workspace.element_size())
-    return gq, gk, gv, gg, (gS0 if want_dS0 else None)
+        gq, gk, gv, gg = (torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (q, k, v, g))
+        gS0 = torch.empty(state, dtype=torch.float32, device=dev) if want_dS0 else None
+    else:
+        gq, gk, gv, gg, gS0 = grads
+        gS0 = gS0 if want_dS0 else None
+    workspace, wp, wn = _room(dev, workspace, linattn_bwd_workspace_size(
+        B, T, H, *heads, dk, dv, decay, q.dtype, n_seqs))
+    p = _addresses(dev, ("q", q), ("k", k), ("v", v), ("g", g), ("S0", S0), ("cu_seqlens", cu_seqlens),
+                   ("dO", dO), ("dS_T", dS_T), ("dq", gq), ("dk", gk), ("dv", gv), ("dg", gg), ("dS0", gS0))
+    _call(dev, "ckda_linattn_bwd", *p[:6], n_seqs, B, T, H, *heads, dk, dv, decay, _DT[q.dtype], *p[6:], wp, wn)
+    return gq, gk, gv, gg, gS0
 
 
 def linattn_decode_step(q, k, v, g, S, o=None, want_o: bool = True):
     """One token of ``linattn_fwd``: S [B,H,dk,dv] float32 is updated in place; returns o
     [B,H,dv] (None when not wanted).  q [B,Hq,dk], k [B,Hk,dk], v [B,Hv,dv]; g [B,H] or [H]."""
-    _need(q.dim() == 3, f"q must be [B,Hq,dk], got {tuple(q.shape)}")
-    B, dk, dev = q.shape[0], q.shape[-1], q.device
-    H, decay, heads = _lin_heads(g, (B,), q=q, k=k, v=v)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [B,Hq,dk], got {tuple(q.shape)}")
+    B, dk, dv = q.shape[0], q.shape[-1], v.shape[-1]
+    H, decay, heads = _lin_heads(g, q.shape[:1], (("q", q), ("k", k), ("v", v)))
     _lin_types(q, k, v)
-    dv = v.shape[-1]
-    _need(tuple(S.shape) == (B, H, dk, dv) and S.dtype == torch.float32,
-          f"S must be [B,H,dk,dv] = {(B, H, dk, dv)} float32")
-    _need(o is None or (tuple(o.shape) == (B, H, dv) and o.dtype == q.dtype),
-          f"o must be [B,H,dv] = {(B, H, dv)} in {q.dtype}")
-    _same_device(q, k=k, v=v, g=g, S=S, o=o)
-    if want_o and o is None:
+    _lin_out("S", S, (B, H, dk, dv), torch.float32)
+    _lin_out("o", o, (B, H, dv), q.dtype)
+    dev = _on_cuda(q)
+    if not want_o:
+        o = None
+    elif o is None:
         o = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
-    _call(dev, "ckda_linattn_decode_step", _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S), B, H,
-          *heads, dk, dv, decay, _DT[q.dtype], _ptr(o if want_o else None))
-    return o if want_o else None
+    p = _addresses(dev, ("q", q), ("k", k), ("v", v), ("g", g), ("S", S), ("o", o))
+    _call(dev, "ckda_linattn_decode_step", *p[:5], B, H, *heads, dk, dv, decay, _DT[q.dtype], p[5])
+    return o
 
 
 # ------------------------------------------------------------------ rotary positions
@@ -524,27 +565,30 @@ def rotary(q, k, pos, freqs, layout: str = "half", inverse: bool = False, scale:
     freqs float64 [n], 2 n <= d: pair i is channels (i, i + n) ("half") or (2 i, 2 i + 1)
     ("interleaved"); channels from 2 n on are copied.  ``inverse`` turns back (with the same
     scale: the gradient).  An output may be its input."""
-    _need(layout in ROTARY_LAYOUTS, f"layout must be one of {sorted(ROTARY_LAYOUTS)}, got {layout!r}")
-    _need(q.dim() >= 2, f"q must be [*lead,Hq,d], got {tuple(q.shape)}")
-    _need(q.dtype in _DT, f"q must be float32 or bfloat16, got {q.dtype}")
-    lead, (Hq, d), dev = tuple(q.shape[:-2]), q.shape[-2:], q.device
-    _need(k is None or (k.dim() == q.dim() and tuple(k.shape[:-2]) == lead and k.shape[-1] == d
-                        and k.dtype == q.dtype),
-          f"k must be {lead + ('Hk', d)} in q's dtype")
-    _need(tuple(pos.shape) == lead and pos.dtype in (torch.int32, torch.int64),
-          f"pos must be {lead} int32 or int64, got {tuple(pos.shape)}, {pos.dtype}")
-    _need(freqs.dim() == 1 and freqs.dtype == torch.float64 and 2 * freqs.numel() <= d,
-          f"freqs must be float64 [n] with 2 n <= {d}")
-    q_out = torch.empty_like(q) if q_out is None else q_out
-    if k is None:
-        _need(k_out is None, "k_out without k")
-    elif k_out is None:
-        k_out = torch.empty_like(k)
-    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
-        _need(t is None or (t.shape == like.shape and t.dtype == like.dtype),
-              f"{name} must be shaped and typed as its input")
-    _same_device(q, k=k, pos=pos, freqs=freqs, q_out=q_out, k_out=k_out)
-    _call(dev, "ckda_rotary", _ptr(q), _ptr(k), _ptr(pos), _ptr(freqs), pos.numel(), Hq,
-          k.shape[-2] if k is not None else 0, d, freqs.numel(), ROTARY_LAYOUTS[layout],
-          int(pos.dtype == torch.int64), scale, int(inverse), _DT[q.dtype], _ptr(q_out), _ptr(k_out))
+    if layout not in ROTARY_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROTARY_LAYOUTS)}, got {layout!r}")
+    if q.dim() < 2:
+        raise ValueError(f"q must be [*lead,Hq,d], got {tuple(q.shape)}")
+    if q.dtype not in _DT:
+        raise ValueError(f"q must be float32 or bfloat16, got {q.dtype}")
+    lead, d = q.shape[:-2], q.shape[-1]
+    if k is not None and (k.dim() != q.dim() or k.shape[:-2] != lead or k.shape[-1] != d or k.dtype != q.dtype):
+        raise ValueError(f"k must be {tuple(lead) + ('Hk', d)} in q's dtype, got {tuple(k.shape)}, {k.dtype}")
+    if pos.shape != lead or pos.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"pos must be {tuple(lead)} int32 or int64, got {tuple(pos.shape)}, {pos.dtype}")
+    if freqs.dim() != 1 or freqs.dtype != torch.float64 or 2 * freqs.shape[0] > d:
+        raise ValueError(f"freqs must be float64 [n] with 2 n <= {d}, got {tuple(freqs.shape)}, {freqs.dtype}")
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    _lin_out("q_out", q_out, q.shape, q.dtype)
+    if k is not None:
+        _lin_out("k_out", k_out, k.shape, k.dtype)
+    dev = _on_cuda(q)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    p = _addresses(dev, ("q", q), ("k", k), ("pos", pos), ("freqs", freqs), ("q_out", q_out), ("k_out", k_out))
+    _call(dev, "ckda_rotary", *p[:4], pos.numel(), q.shape[-2], 0 if k is None else k.shape[-2], d, freqs.shape[0],
+          ROTARY_LAYOUTS[layout], int(pos.dtype == torch.int64), scale, int(inverse), _DT[q.dtype], p[4], p[5])
     return q_out, k_out
