@@ -83,10 +83,12 @@ void launch_fixed(const float *part, float *dg, long rows, int H, const int *sta
 __device__ __forceinline__ long long fixed_log2(float g) {
   return __double2ll_rn((double)fmaxf(g, -140.f) * 6196328018.8645515);   // log2(e) 2^32
 }
-// 2^x, 0 below 2^-126
+// 2^x, 0 below 2^-126 (the fraction's power lies in [1, 2], where the approximation's fast form
+// is as good as any)
 __device__ __forceinline__ float exp2_fixed(long long x) {
   const int n = (int)(x >> 32);
-  const float r = exp2f(__uint2float_rn((uint32_t)x) * 2.3283064365386963e-10f);
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__uint2float_rn((uint32_t)x) * 2.3283064365386963e-10f));
   return n < -126 ? 0.f : r * __int_as_float((min(n, 126) + 127) << 23);
 }
 // Sums over the warp's tokens, two per lane (x0, x1): returns the sum up to and with the second.

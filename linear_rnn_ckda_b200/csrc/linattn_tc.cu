@@ -24,11 +24,11 @@
 // M is kept in fp32 registers.  Roundings to bf16: P, M as an operand of O (each 2^-9 of a
 // term in the mean, the size of the output's own rounding); tokf Z is split into three terms
 // (24 bits), so M itself carries fp32 accuracy over any length.  Where row dots are wanted
-// (decay gradients, which cancel) M and P go into O in three terms too.
+// (decay gradients, which cancel) M and P go into O in three terms too (two leave dg 2.7e-5 off).
 //
-// One CTA per (segment, head), 20 warps: 0-3 state (200 registers a thread, 128 of them M), 4-7
-// outputs, 8, 9 and one of 12, 13 scores (a 32 x 32 block each), 10 TMA loads and decays, 11
-// issue of O, 19 issue of scores and D (two issuers: one thread's products take 50 cycles or
+// One CTA per (segment, head), 24 warps: 0-3 state (200 registers a thread, 128 of them M), 4-11
+// outputs, 12, 13 and one of 16, 17 scores (a 32 x 32 block each), 14 TMA loads and decays, 15
+// issue of O, 23 issue of scores and D (two issuers: one thread's products take 50 cycles or
 // more each to issue), the rest tokf Z.  The roles run the chunks at their own pace through
 // mbarriers; their loops are kept small, because together they have to stay in the instruction
 // caches (fully unrolled they ran at half the speed, 42 % of all stalls waiting for code).
@@ -130,12 +130,12 @@ __device__ __forceinline__ uint64_t f2bits(uint32_t a, uint32_t b) {
 // ------------------------------------------------------------------ shapes
 enum : int { kStates = 0, kOut = 1, kGrad = 2 };   // what a launch computes
 enum : int { kWhole = 0, kBlocks = 1, kPairs = 2 };   // how a chunk's weights are formed
-constexpr int kThreads = 640;
+constexpr int kThreads = 768;
 constexpr uint32_t kPanel = 8192;                  // 64 tokens x 64 channels of bf16, 128-byte swizzle
 constexpr uint32_t kTileB = 2 * kPanel;            // 64 tokens x 128 channels
 constexpr uint32_t kTokB = 3 * kPanel;             // tokf Z of 32 tokens: three terms x two panels of 4 KB
-// Registers a thread by role: 128 x 200 + 512 x 64 = 58,368 of the launch's 640 x 96 = 61,440.
-constexpr int kRegsState = 200, kRegsOther = 64;
+// Registers a thread by role: 128 x 200 + 640 x 56 = 61,440, the launch's 768 x 80.
+constexpr int kRegsState = 200, kRegsOther = 56;
 
 template <int KIND>
 struct Cfg {
@@ -143,7 +143,6 @@ struct Cfg {
   static constexpr int kStages = KIND == kGrad ? 2 : 3;
   static constexpr int kTerms = KIND == kGrad ? 3 : 1;                        // of M and P
   static constexpr int kTokBufs = KIND == kStates ? 4 : 2;                    // half chunks of tokf Z
-  static constexpr int kOBufs = KIND == kOut ? 2 : 1;                         // O in TMEM
   static constexpr uint32_t kStage = kTiles * kTileB;
   static constexpr uint32_t oX = 0;
   static constexpr uint32_t oY = KIND == kStates ? 0 : kTileB;
@@ -152,16 +151,18 @@ struct Cfg {
   static constexpr uint32_t offTok = kStages * kStage;
   static constexpr uint32_t offP = offTok + kTokBufs * kTokB;
   static constexpr uint32_t kP = KIND == kStates ? 0 : kTerms * kPanel;
-  static constexpr uint32_t offOut = offP + kP;                               // 4 warps x 2 x (32 tokens x 32 channels)
+  static constexpr uint32_t offOut = offP + kP;                               
   static constexpr uint32_t offGate = offOut + (KIND == kStates ? 0 : 8 * 2048);
   static constexpr uint32_t kGate = 7 * 64 * 4 + 16;                          // one stage's decays
   static constexpr uint32_t offDot = offGate + kStages * kGate;               // kGrad: 2 x 4 x 64 floats
   static constexpr uint32_t offBar = offDot + (KIND == kGrad ? 512 * 4 : 0);
-  static constexpr int kBars = 3 * kStages + 2 * kTokBufs + 20;
+  static constexpr int kBars = 3 * kStages + 2 * kTokBufs + 21;
   static constexpr uint32_t kSmem = offBar + kBars * 8 + 64 + 1024;           // + slack to align
-  // TMEM columns: scores, M, O (kOut has room for two), the second part of O apart, D
-  static constexpr uint32_t cSc = 0, cM = 64, cO = KIND == kOut ? 128 : 256, cO2 = KIND == kOut ? 256 : 320, cD = 384;
+  // TMEM columns: scores, M, O twice, D (twice where there is room)
+  static constexpr int kDBufs = KIND == kGrad ? 1 : 2;
+  static constexpr uint32_t cSc = 0, cM = 64, cO = cM + 64 * kTerms, cD = 512 - 128 * kDBufs;
 };
+static_assert(Cfg<kGrad>::cO + 128 <= Cfg<kGrad>::cD && Cfg<kOut>::cO + 128 <= Cfg<kOut>::cD, "tensor memory");
 static_assert(Cfg<kOut>::kSmem <= 232448 && Cfg<kGrad>::kSmem <= 232448 && Cfg<kStates>::kSmem <= 232448,
               "shared memory");
 
@@ -192,14 +193,13 @@ struct Params {
   int *status;
 };
 
-// Waits are bounded by a count of tries, each of which may sleep for a microsecond: some seconds,
-// after which every role ends and the status word says so.  (The code is kept small: twenty warps
-// run six roles, and their loops together have to stay in the instruction caches.)
-constexpr uint32_t kTryNs = 1000, kTries = 4000000;
+// Waits are bounded by a count of tries, each of which the hardware lets sleep for a while: some
+// seconds, after which every role ends and the status word says so.
+constexpr uint32_t kTries = 2000000;
 constexpr uint64_t kDrainNs = 2000000000ull;
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
   uint32_t n = 0;
-  while (!mbar_try_wait_sleep(bar, parity & 1u, kTryNs))
+  while (!mbar_try_wait(bar, parity & 1u))
     if (*abort || ++n > kTries) return false;
   return true;
 }
@@ -225,30 +225,29 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
   const int nc = (u.len + kC - 1) / kC;
 
   // Warps by role (the scores' off-diagonal block lies in the TMEM lanes of a quarter that goes
-  // with the direction: 13 forwards, 12 backwards; the other of the two takes part in tokf Z)
-  const int off_warp = rev ? 12 : 13;
-  const int tok_warps = KIND == kStates ? 8 : 6;
-  const int tok_index = KIND == kStates ? (warp < 8 ? warp - 4 : warp - 8) : warp >= 14 ? warp - 13 : 0;
-  const bool is_score = KIND != kStates && (warp == 8 || warp == 9 || warp == off_warp);
-  const bool is_tok = KIND == kStates ? (warp >= 4 && warp < 8) || (warp >= 12 && warp < 16)
-                                      : warp >= 12 && warp < 19 && warp != off_warp;
+  // with the direction: 17 forwards, 16 backwards; the other of the two takes part in tokf Z)
+  const int off_warp = rev ? 16 : 17;
+  const int tok_warps = KIND == kStates ? 16 : 6;
+  const int tok_index = KIND == kStates ? (warp < 14 ? warp - 4 : warp - 6) : warp >= 18 ? warp - 17 : 0;
+  const bool is_score = KIND != kStates && (warp == 12 || warp == 13 || warp == off_warp);
+  const bool is_tok = KIND == kStates ? (warp >= 4 && warp < 14) || (warp >= 16 && warp < 22) : warp >= 16 && warp < 23 && warp != off_warp;
 
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::offBar);
   uint64_t *b_full = bars, *b_empty = bars + C::kStages, *b_gate = bars + 2 * C::kStages;
   uint64_t *b_w = bars + 3 * C::kStages, *b_wfree = b_w + C::kTokBufs;
   uint64_t *bx = b_wfree + C::kTokBufs;
   uint64_t *b_zeroed = bx, *b_sc = bx + 1, *b_p = bx + 2, *b_s = bx + 3, *b_o = bx + 4 /* 2 */,
-           *b_ofree = bx + 6 /* 2 */, *b_d = bx + 8, *b_dfree = bx + 9, *b_drain = bx + 10 /* 2 */,
+           *b_ofree = bx + 6 /* 2 */, *b_d = bx + 8 /* 2 */, *b_dfree = bx + 16 /* 2 */, *b_drain = bx + 10 /* 2 */,
            *b_red = bx + 12 /* 2 */, *b_o1 = bx + 14;
-  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bx + 16);
-  volatile int *s_abort = reinterpret_cast<volatile int *>(bx + 17);
-  volatile int *s_issued = reinterpret_cast<volatile int *>(bx + 18);
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bx + 18);
+  volatile int *s_abort = reinterpret_cast<volatile int *>(bx + 19);
+  volatile int *s_issued = reinterpret_cast<volatile int *>(bx + 20);
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(b_full + s, 1);
-      // state 4, tokf Z, a commit; beside outputs 4, scores 3 and a second commit
-      mbar_init(b_empty + s, 4 + tok_warps + 1 + (KIND == kStates ? 0 : 8));
+      // state 4, tokf Z, a commit; beside outputs 8, scores 3 and a second commit
+      mbar_init(b_empty + s, 4 + tok_warps + 1 + (KIND == kStates ? 0 : 12));
       mbar_init(b_gate + s, 1);
     }
     for (int s = 0; s < C::kTokBufs; ++s) {
@@ -259,20 +258,20 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     mbar_init(b_sc, 1);
     mbar_init(b_p, 3);
     mbar_init(b_s, 4);
-    mbar_init(b_d, 1);
-    mbar_init(b_dfree, 4);
     mbar_init(b_o1, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(b_o + s, 1);
-      mbar_init(b_ofree + s, 4);
-      mbar_init(b_red + s, 4);
+      mbar_init(b_d + s, 1);
+      mbar_init(b_dfree + s, 4);
+      mbar_init(b_ofree + s, 8);
+      mbar_init(b_red + s, 8);
       mbar_init(b_drain + s, 1);
     }
     *s_abort = 0;
     *s_issued = 0;
     mbar_fence_init();
   }
-  if (warp == 11) tmem_alloc(s_tmem, 512);
+  if (warp == 15) tmem_alloc(s_tmem, 512);
   // (scores on the acausal side are never written: they stay 0)
   for (int i = tid; i < (int)(C::kP / 16); i += kThreads)
     reinterpret_cast<uint4 *>(sm + C::offP)[i] = make_uint4(0, 0, 0, 0);
@@ -382,20 +381,21 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       const uint64_t a2 = f2pk(a, a);
       __syncwarp();
       if (lane == 0) mbar_arrive(b_empty + st);
-      if (!(ok = wait(b_d, c))) break;
+      const int db = c & (C::kDBufs - 1);
+      if (!(ok = wait(b_d + db, c / C::kDBufs))) break;
       tc_fence_after();
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         if (32 * b >= ps.dx) break;
         uint32_t r[32];
-        tmem_ld32(lanes + C::cD + 32 * b, r);
+        tmem_ld32(lanes + C::cD + 128 * (c & (C::kDBufs - 1)) + 32 * b, r);
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; ++i) M[16 * b + i] = f2fma(a2, M[16 * b + i], f2bits(r[2 * i], r[2 * i + 1]));
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(b_dfree);
+      if (lane == 0) mbar_arrive(b_dfree + db);
       if (KIND != kStates && c + 1 < nc) {
         if (!(ok = wait(b_o1, c))) break;           // (O1 of this chunk has read the operand)
         tc_fence_after();
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 10) {
+    if (warp == 14) {
       // -------------------------------------------------------------- loads and decays
       const int px = (ps.dx + 63) / 64, pz = (ps.dz + 63) / 64;
       const uint32_t bytes = kPanel * ((KIND != kStates ? px : 0) + px + pz + (exact ? pz : 0));
@@ -482,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             t = i < len ? (rev ? since : until) : 0.f;
             if (KIND == kStates) return;
             c = exp2_fixed(rev ? G - ref : ref - G);
+            if (mode == kWhole) return;
             b = exp2_fixed(rev ? ref - G : G - ref);
             x = exp2_fixed(i < 32 ? mid - G : G - mid);
           };
@@ -491,9 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
           reinterpret_cast<float2 *>(gt + 64)[lane] = tf;
           if (KIND != kStates) {
             reinterpret_cast<float2 *>(gt + 128)[lane] = cb;
-            reinterpret_cast<float2 *>(gt + 192)[lane] = rb;
-            reinterpret_cast<float2 *>(gt + 256)[lane] = cr;
-            reinterpret_cast<longlong2 *>(gt + 320)[lane] = make_longlong2(sum - x1, sum);
+            if (mode != kWhole) {
+              reinterpret_cast<float2 *>(gt + 192)[lane] = rb;
+              reinterpret_cast<float2 *>(gt + 256)[lane] = cr;
+              reinterpret_cast<longlong2 *>(gt + 320)[lane] = make_longlong2(sum - x1, sum);
+            }
           }
           if (lane == 0) {
             gt[448] = exp2_fixed(all);
@@ -507,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       // (a backward walk's segments but the last belong to the forward walk too, which writes theirs)
       if (KIND == kStates && lane == 0 && (!rev || u.piece == u.pieces - 1))
         ps.decay[(size_t)blockIdx.x * p.H + h] = exp2_fixed(whole);
-    } else if (warp == 11) {
+    } else if (warp == 15) {
       // -------------------------------------------------------------- issue of O
       if (KIND != kStates && lane == 0) {
         const uint32_t id1 = idesc_bf16(128, 64, false, false), id2 = idesc_bf16(128, 64, true, false);
@@ -525,11 +528,12 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             mma_bf16_ts(d, m + 8, b + 2, id1, true);
           }
         };
+        bool both = false;             // the chunk before took both buffers
         for (; ok && c < nc; ++c, next(st, ph)) {
           // (the outputs that were in this buffer have been read; X is there, for the scores read it)
-          const int ob = c & (C::kOBufs - 1);
-          if (!(ok = need(b_s, c) && (c < C::kOBufs || need(b_ofree + ob, (c - C::kOBufs) / C::kOBufs)))) break;
-          if (!(ok = need(b_full + st, ph) && need(b_gate + st, ph))) break;
+          const int ob = c & 1;
+          if (!(ok = need(b_s, c) && (c < 2 || need(b_ofree + ob, (c >> 1) - 1)))) break;
+          if (!(ok = need(b_full + st, ph) && need(b_gate + st, ph) && (!both || need(b_ofree + (ob ^ 1), (c - 1) >> 1)))) break;
           tc_fence_after();
           const uint64_t x = kmajor(st * C::kStage + C::oX);
           const uint32_t d = tmem + C::cO + 64 * ob;
@@ -539,14 +543,13 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             out1(d, tmem + C::cM + 128, x, true);
           }
           mma_commit(b_o1);
-          // the second part on top, or (weights not over the whole chunk) apart, in the one buffer
-          // there is: then the chunk before has been read too
+          // the second part on top, or (weights not over the whole chunk) in the other buffer
           const bool apart = gates(st)[449] != (float)kWhole;
-          if (!(ok = need(b_p, c) && (!apart || c == 0 || need(b_ofree + ((c - 1) & (C::kOBufs - 1)), (c - 1) / C::kOBufs))))
-            break;
+          if (!(ok = need(b_p, c) && (!apart || c == 0 || need(b_ofree + (ob ^ 1), (c - 1) >> 1)))) break;
           tc_fence_after();
           const uint64_t dz = mnmajor(st * C::kStage + C::oZ, kPanel), dp = kmajor(C::offP);
-          const uint32_t d2 = apart ? tmem + C::cO2 : d;
+          const uint32_t d2 = apart ? tmem + C::cO + 64 * (ob ^ 1) : d;
+          both = apart;
           mma_bf16_ss(d2, dz, dp, id2, !apart);
 #pragma unroll
           for (int k = 1; k < 4; ++k) mma_bf16_ss(d2, dz + 128 * k, dp + 2 * k, id2, true);
@@ -555,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             for (int k = 0; k < 8; ++k)
               mma_bf16_ss(d2, dz + 128 * (k & 3), dp + (1 + (k >> 2)) * (kPanel >> 4) + 2 * (k & 3), id2, true);
           }
-          mma_commit(b_o + (c & 1));
+          mma_commit(b_o + ob);
           mma_commit(b_empty + st);
         }
         // every product issued has completed before the tensor memory is released
@@ -563,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         mbar_wait(b_drain, 0, kDrainNs);
       }
       __syncwarp();
-    } else if (warp == 19) {
+    } else if (warp == 23) {
       // -------------------------------------------------------------- issue of scores and D
       if (lane == 0) {
         const uint32_t id_s = idesc_bf16(128, 64, false, false), id_d = idesc_bf16(128, ps.dx, true, true);
@@ -589,21 +592,23 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             }
             mma_commit(b_sc);
           }
+          const int db = c & (C::kDBufs - 1);
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             const int hh = 2 * c + half, slot = hh % C::kTokBufs;
-            if (!(ok = need(b_w + slot, hh / C::kTokBufs) && (half || c == 0 || need(b_dfree, c - 1)))) break;
+            if (!(ok = need(b_w + slot, hh / C::kTokBufs) && (half || c < C::kDBufs || need(b_dfree + db, c / C::kDBufs - 1)))) break;
             tc_fence_after();
             const uint64_t dy = mnmajor(st * C::kStage + C::oY, kPanel) + 256 * half;
             const uint64_t dw = mnmajor(C::offTok + slot * kTokB, kPanel / 2);
-            mma_bf16_ss(tmem + C::cD, dw, dy, id_d, half > 0);
+            const uint32_t d = tmem + C::cD + 128 * db;
+            mma_bf16_ss(d, dw, dy, id_d, half > 0);
 #pragma unroll
             for (int m = 1; m < 6; ++m)              // (m >> 1)-th term, 16 tokens
-              mma_bf16_ss(tmem + C::cD, dw + (m >> 1) * (kPanel >> 4) + 128 * (m & 1), dy + 128 * (m & 1), id_d, true);
+              mma_bf16_ss(d, dw + (m >> 1) * (kPanel >> 4) + 128 * (m & 1), dy + 128 * (m & 1), id_d, true);
             mma_commit(b_wfree + slot);
           }
           if (!ok) break;
-          mma_commit(b_d);
+          mma_commit(b_d + db);
           mma_commit(b_empty + st);
         }
         mma_commit(b_drain + 1);
@@ -665,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     } else if (is_score) {
       // -------------------------------------------------------------- scores, a 32 x 32 block each
       const int rb = warp & 3, row = 32 * rb + lane;               // rows (TMEM lanes) of the block
-      const int cb = warp < 12 ? rb : 1 - rb;                      // its columns: the diagonal, or the causal other
+      const int cb = warp < 16 ? rb : 1 - rb;                      // its columns: the diagonal, or the causal other
       const uint32_t lanes = tmem + ((uint32_t)(32 * rb) << 16);
       uint8_t *P = sm + C::offP + row * 128;
       const uint32_t mask = cb != rb ? ~0u : rev ? ~0u << lane : ~0u >> (31 - lane);   // the causal columns
@@ -741,88 +746,64 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
           mbar_arrive(b_empty + st);
         }
       }
-    } else if (KIND != kStates && warp < 8) {
-      // -------------------------------------------------------------- outputs (warps 4-7)
-      // A warp holds 32 channels.  It reads O in 8 x 8 blocks, which are bf16 matrix fragments once
-      // two tokens are packed into a register, so four transposing stores put 32 channels of 8
-      // tokens into rows.  Whole chunks leave as two TMA stores a warp, through two buffers of its
-      // own (a store is read out of shared memory only when the loads issued before it have
-      // been, some 2,800 cycles later).
-      const int quad = warp & 3;
-      const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-      float *red = reinterpret_cast<float *>(sm + C::offDot);      // [2][4 quads][64]
-      const uint32_t mine = sb + C::offOut + (warp - 4) * 4096;
-      const int ch = 32 * quad + (lane >> 2), tk = 2 * (lane & 3); // this lane's first channel and token in a block
+    } else if (KIND != kStates && warp < 12) {
+      // -------------------------------------------------------------- outputs (warps 4-11)
+      // A warp holds 32 channels of 32 tokens.  It reads O in 8 x 8 blocks, which are bf16 matrix
+      // fragments once two tokens are packed into a register, so four transposing stores put 32
+      // channels of 8 tokens into rows.  Whole chunks leave as one TMA store a warp (read out of
+      // shared memory only when the loads issued before it have been, some 2,800 cycles later:
+      // still within a chunk's time).
+      const int quad = warp & 3, g = (warp >> 2) - 1;
+      const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + 32 * g;
+      float *red = reinterpret_cast<float *>(sm + C::offDot) + 32 * g;   // [2][4 quads][64]
+      const uint32_t mine = C::offOut + (warp - 4) * 2048;
+      const int ch = 32 * quad + (lane >> 2), tk = 2 * (lane & 3);  // this lane's first channel and token in a block
       const bool any = 32 * quad < ps.dz && ps.out;
       for (; c < nc; ++c, next(st, ph)) {
-        const int ci = chunk_at(c), len = rows_of(ci), ob = c & (C::kOBufs - 1);
+        const int ci = chunk_at(c), len = rows_of(ci) - 32 * g, ob = c & 1;
         const float *gt = gates(st);
-        const bool tma = len == kC && any && !(KIND == kGrad && ps.part);
+        const bool tma = len >= 32 && any && !(KIND == kGrad && ps.part);
+        const long row0 = u.row0 + ci * kC + 32 * g;
         if (!(ok = wait(b_gate + st, ph))) break;
         const bool apart = gt[449] != (float)kWhole;
-        if (!(ok = wait(b_o + (c & 1), c >> 1))) break;
+        uint64_t f[4], d[4];                                        // rowf of this lane's two tokens a block; dots
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 x = *reinterpret_cast<const float2 *>(gt + 32 * g + 8 * k + tk);
+          f[k] = f2pk(x.x, x.y);
+          d[k] = 0;
+        }
+        if (!(ok = wait(b_o + ob, c >> 1))) break;
         tc_fence_after();
-        float *rd = red + (c & 1) * 256 + quad * 64;
-#pragma unroll 1
-        for (int g = 0; g < 2; ++g) {                               // 32 tokens
-          uint32_t r[2][16];                                        // channels 0-15, 16-31
-          tmem_ld_blocks(lanes + C::cO + 64 * ob + 32 * g, r[0]);
-          tmem_ld_blocks(lanes + (16u << 16) + C::cO + 64 * ob + 32 * g, r[1]);
+        uint32_t pk[2][8];                                          // [y][2 k + m]: block k, channel ch + 16 y + 8 m
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          uint32_t r[16];
+          tmem_ld_blocks(lanes + ((16u * y) << 16) + C::cO + 64 * ob, r);
           tmem_wait_ld();
-          uint64_t f[4];                                            // rowf of this lane's two tokens a block
+          uint64_t v[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 x = *reinterpret_cast<const float2 *>(gt + 32 * g + 8 * k + tk);
-            f[k] = f2pk(x.x, x.y);
-          }
-          uint64_t v[2][8];                                         // [.][2 k + m]: block k, channel ch + 8 m (+ 16)
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[y][i] = f2mul(f[i >> 1], f2bits(r[y][2 * i], r[y][2 * i + 1]));
+          for (int i = 0; i < 8; ++i) v[i] = f2mul(f[i >> 1], f2bits(r[2 * i], r[2 * i + 1]));
           if (apart) {
-#pragma unroll 1
-            for (int y = 0; y < 2; ++y) {
-              uint32_t r2[16];
-              tmem_ld_blocks(lanes + ((16u * y) << 16) + C::cO2 + 32 * g, r2);
-              tmem_wait_ld();
+            tmem_ld_blocks(lanes + ((16u * y) << 16) + C::cO + 64 * (ob ^ 1), r);
+            tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint64_t b = f2bits(r2[2 * i], r2[2 * i + 1]);
-                if (y == 0) v[0][i] = f2add(v[0][i], b);
-                else v[1][i] = f2add(v[1][i], b);
-              }
-            }
+            for (int i = 0; i < 8; ++i) v[i] = f2add(v[i], f2bits(r[2 * i], r[2 * i + 1]));
           }
-          if (g == 1) {
+          if (y == 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(b_ofree + ob);
           }
-          if (tma) {
-            // (the store before the last has been read)
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-            __syncwarp();
-            // rows of 64 bytes, 16-byte pieces permuted by row / 2 % 4 (64-byte swizzle)
-            const int row = lane & 7;
-            const uint32_t at = mine + 2048 * g + row * 64 + (((lane >> 3) ^ (row >> 1)) << 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              stmatrix4_t(at + 512 * k, pack_bf16(v[0][2 * k]), pack_bf16(v[0][2 * k + 1]), pack_bf16(v[1][2 * k]),
-                          pack_bf16(v[1][2 * k + 1]));
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_3d(&p.outs[blockIdx.z], sm + (mine - sb) + 2048 * g, 32 * quad, h, (int)(u.row0 + ci * kC + 32 * g));
-              bulk_commit();
-            }
-          } else if (any) {
+          for (int i = 0; i < 8; ++i) pk[y][i] = pack_bf16(v[i]);
+          if (!tma && any) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int t = 32 * g + 8 * ((i & 7) >> 1) + tk, z = ch + 8 * (i & 1) + 16 * (i >> 3);
+            for (int i = 0; i < 8; ++i) {
+              const int t = 8 * (i >> 1) + tk, z = ch + 16 * y + 8 * (i & 1);
               float a, b;
-              f2up(v[i >> 3][i & 7], a, b);
-              const size_t at = ((size_t)(u.row0 + ci * kC + t) * p.H + h) * ps.dz + z, step = (size_t)p.H * ps.dz;
+              f2up(v[i], a, b);
+              const size_t step = (size_t)p.H * ps.dz, at = ((size_t)(row0 + t) * p.H + h) * ps.dz + z;
               if (z >= ps.dz) continue;
               if (KIND == kGrad && ps.part) {
                 if (t < len) static_cast<float *>(ps.out)[at] = a;
@@ -833,21 +814,42 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
               }
             }
           }
-          if (exact) {
-            // this lane's products with W, 8 tokens, summed over its channels; then over the lanes
-            // that hold the same tokens (bits 2-4), each of which ends up with one
-            const uint32_t wt = sb + st * C::kStage + C::oW + (quad >> 1) * kPanel;
-            uint64_t d[4];
+          if constexpr (KIND == kGrad) {
+            if (exact) {
+              // products with W, two 8 x 8 blocks of two channel groups at a time
+              const uint32_t wt = sb + st * C::kStage + C::oW + (quad >> 1) * kPanel;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int row = 32 * g + 8 * k + (lane & 7);
-              uint32_t w[4];
-              ldmatrix4_t(wt + row * 128 + (((4 * (quad & 1) + (lane >> 3)) ^ (row & 7)) << 4), w);
-              d[k] = 0;
+              for (int k = 0; k < 4; k += 2) {
+                const int row = 32 * g + 8 * (k + (lane >> 4)) + (lane & 7);
+                uint32_t w[4];
+                ldmatrix4_t(wt + row * 128 + (((4 * (quad & 1) + 2 * y + (lane >> 3 & 1)) ^ (row & 7)) << 4), w);
 #pragma unroll
-              for (int m = 0; m < 4; ++m)
-                if (32 * quad + 8 * m < ps.dz) d[k] = f2fma(v[m >> 1][2 * k + (m & 1)], unpack_bf16(w[m]), d[k]);
+                for (int e = 0; e < 4; ++e)
+                  if (32 * quad + 16 * y < ps.dz) d[k + (e >> 1)] = f2fma(v[2 * k + e], unpack_bf16(w[e]), d[k + (e >> 1)]);
+              }
             }
+          }
+        }
+        if (tma) {
+          if (lane == 0) bulk_wait_read();                         // (the last store has been read)
+          __syncwarp();
+          // rows of 64 bytes, 16-byte pieces permuted by row / 2 % 4 (64-byte swizzle)
+          const int row = lane & 7;
+          const uint32_t at = sb + mine + row * 64 + (((lane >> 3) ^ (row >> 1)) << 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            stmatrix4_t(at + 512 * k, pk[0][2 * k], pk[0][2 * k + 1], pk[1][2 * k], pk[1][2 * k + 1]);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&p.outs[blockIdx.z], sm + mine, 32 * quad, h, (int)row0);
+            bulk_commit();
+          }
+        }
+        if constexpr (KIND == kGrad) {
+          if (exact) {
+            // 8 tokens' sums over this lane's channels, then over the lanes that hold the same
+            // tokens (bits 2-4), each of which ends up with one token
             float s8[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) f2up(d[k], s8[2 * k], s8[2 * k + 1]);
@@ -860,20 +862,16 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 s8[i] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * step);
               }
             }
-            rd[32 * g + 8 * (lane >> 3) + tk + (lane >> 2 & 1)] = s8[0];
-          }
-        }
-        if (exact) {
-          __syncwarp();
-          // (two barriers: a warp may be a chunk ahead of another that waits for its store)
-          if (lane == 0) mbar_arrive(b_red + (c & 1));
-          if (quad == 0) {
-            if (!(ok = wait(b_red + (c & 1), c >> 1))) break;
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-              if (32 * g + lane < len)
-                ps.dots[(size_t)h * p.rows + u.row0 + ci * kC + 32 * g + lane] =
-                    (rd[32 * g + lane] + rd[64 + 32 * g + lane]) + (rd[128 + 32 * g + lane] + rd[192 + 32 * g + lane]);
+            float *rd = red + ob * 256;
+            rd[quad * 64 + 8 * (lane >> 3) + tk + (lane >> 2 & 1)] = s8[0];
+            __syncwarp();
+            // (two barriers: a warp may be a chunk ahead of another that waits for its store)
+            if (lane == 0) mbar_arrive(b_red + ob);
+            if (quad == 0) {
+              if (!(ok = wait(b_red + ob, c >> 1))) break;
+              if (lane < len)
+                ps.dots[(size_t)h * p.rows + row0 + lane] = (rd[lane] + rd[64 + lane]) + (rd[128 + lane] + rd[192 + lane]);
+            }
           }
         }
         __syncwarp();
@@ -891,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       mbar_wait(b_full + i % C::kStages, (i / C::kStages) & 1, kDrainNs);
   }
   __syncthreads();
-  if (warp == 11) {
+  if (warp == 15) {
     tc_fence_after();
     tmem_dealloc(*s_tmem, 512);
   }
