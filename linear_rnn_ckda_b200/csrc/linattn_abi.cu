@@ -136,7 +136,7 @@ int ckda_linattn_decode_step(const void *q, const void *k, const void *v, const 
   if ((B != 0 && (!q || !k || !v || !S)) || !has_decays(g, B, 1, decay)) return CKDA_ERR_NULL;
   int rc = check_sizes(B, 1, H, Hq, Hk, Hv, dk, dv, decay, io_dtype);
   if (rc != CKDA_OK) return rc;
-  if ((long long)B * H > INT32_MAX) return CKDA_ERR_DIM;
+  if ((long long)B * H * (dv / 16) > INT32_MAX) return CKDA_ERR_DIM;   // (a warp takes 16 state columns)
   const uintptr_t es = io_dtype == CKDA_BF16 ? 2 : 4;
   if (!aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(g, 4) || !aligned(S, 16) ||
       !aligned(o, es))

@@ -13,28 +13,27 @@ namespace ckda {
 namespace {
 
 template <int DK, int DV, typename T>
-__global__ void __launch_bounds__(256, 2) linattn_decode_kernel(const LinDecodeArgs p, long tasks) {
+__global__ void __launch_bounds__(256, 2) linattn_decode_kernel(const LinDecodeArgs p, uint32_t tasks) {
   constexpr int slices = DV / 16;
   __shared__ float2 s_kq[8][DK];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long task = (long)blockIdx.x * (blockDim.x >> 5) + warp;
+  const uint32_t task = blockIdx.x * (blockDim.x >> 5) + warp;   // below 2^31: B H dv / 16 is checked
   if (task >= tasks) return;
-  const long head = task / slices;                 // b * H + h
-  const int slice = (int)(task - head * slices);
-  const long b = head / p.H;
-  const int h = (int)(head - b * p.H);
+  const uint32_t head = task / slices, slice = task % slices;    // head = b * H + h
   const int col = slice * 16 + (lane & 3) * 4, r0 = lane >> 2;
   float *S = p.S + (size_t)head * DK * DV + col;
   constexpr int kRows = DK / 8;
   float4 st[kRows];
 #pragma unroll
   for (int m = 0; m < kRows; ++m)
-    st[m] = *reinterpret_cast<const float4 *>(S + (size_t)(r0 + 8 * m) * DV);
-  const T *q = static_cast<const T *>(p.q) + ((size_t)b * p.Hq + (long)h * p.Hq / p.H) * DK;
-  const T *k = static_cast<const T *>(p.k) + ((size_t)b * p.Hk + (long)h * p.Hk / p.H) * DK;
-  const T *v = static_cast<const T *>(p.v) + ((size_t)b * p.Hv + (long)h * p.Hv / p.H) * DV + col;
+    st[m] = __ldcs(reinterpret_cast<const float4 *>(S + (r0 + 8 * m) * DV));
+  const uint32_t b = head / (uint32_t)p.H;
+  const int h = (int)(head - b * p.H);
+  const T *q = static_cast<const T *>(p.q) + ((size_t)b * p.Hq + h * p.Hq / p.H) * DK;
+  const T *k = static_cast<const T *>(p.k) + ((size_t)b * p.Hk + h * p.Hk / p.H) * DK;
+  const T *v = static_cast<const T *>(p.v) + ((size_t)b * p.Hv + h * p.Hv / p.H) * DV + col;
   for (int i = lane; i < DK; i += 32) s_kq[warp][i] = make_float2(to_f32(k[i]), to_f32(q[i]));
-  const float al = expf(p.g[p.g_fixed ? (long)h : head]);
+  const float al = expf(p.g[p.g_fixed ? (uint32_t)h : head]);
   const float v0 = to_f32(v[0]), v1 = to_f32(v[1]), v2 = to_f32(v[2]), v3 = to_f32(v[3]);
   __syncwarp();
   float o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
@@ -43,7 +42,7 @@ __global__ void __launch_bounds__(256, 2) linattn_decode_kernel(const LinDecodeA
     const float2 kq = s_kq[warp][r0 + 8 * m];
     st[m].x = fmaf(al, st[m].x, kq.x * v0); st[m].y = fmaf(al, st[m].y, kq.x * v1);
     st[m].z = fmaf(al, st[m].z, kq.x * v2); st[m].w = fmaf(al, st[m].w, kq.x * v3);
-    *reinterpret_cast<float4 *>(S + (size_t)(r0 + 8 * m) * DV) = st[m];
+    __stcs(reinterpret_cast<float4 *>(S + (r0 + 8 * m) * DV), st[m]);
     o0 = fmaf(kq.y, st[m].x, o0); o1 = fmaf(kq.y, st[m].y, o1);
     o2 = fmaf(kq.y, st[m].z, o2); o3 = fmaf(kq.y, st[m].w, o3);
   }
@@ -68,7 +67,7 @@ int launch_typed(const LinDecodeArgs &a, cudaStream_t s) {
   long warps = tasks / (148 * 4);
   warps = warps < 1 ? 1 : warps > 8 ? 8 : warps;
   linattn_decode_kernel<DK, DV, T><<<(unsigned)((tasks + warps - 1) / warps), (unsigned)(32 * warps), 0, s>>>(
-      a, tasks);
+      a, (uint32_t)tasks);
   return cudaGetLastError() == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
 }
 template <int DK, typename T>

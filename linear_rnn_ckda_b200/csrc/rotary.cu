@@ -12,9 +12,12 @@
 // (an fp32 product is a tenth of a radian off at a million tokens), and no range reduction
 // follows.  One fp32 rounding of the fraction costs 2^-25 of half a turn.
 //
-// Bound: HBM, q and k read and written once.  A block takes a few tokens: its threads put
-// their loads in flight, fill a table of cos and sin in shared memory (one pair per token and
-// frequency, shared by all heads), and turn 16-byte vectors from registers.
+// Bound: HBM, q and k read and written once.  A warp takes a token (or some of its heads, when
+// tokens are few): its first loads are in flight while it fills a table of the token's cos and
+// sin in shared memory; then each lane keeps the entries of its own 16-byte vector in
+// registers and turns that vector of one head after another.  Warps share nothing but the
+// fixed-point frequencies, formed once a block.  (With a table per block, a block barrier per
+// token pair and table entries read for every vector, 268 MB took 66 us.)
 #include "common.cuh"
 #include "linattn.h"
 
@@ -22,150 +25,190 @@ namespace ckda {
 namespace {
 
 constexpr int kRotThreads = 256;
-constexpr int kRotItems = 2;       // items per thread held in registers at once
-constexpr int kRotTable = 2048;    // table entries (tokens of a block x frequencies)
-
-struct FastDiv {                   // n / d for n < 2^31 by one multiplication
-  uint32_t d, mul, shift;
-};
-FastDiv fast_div(uint32_t d) {
-  FastDiv f{d, 0, 0};
-  while ((1ull << f.shift) < d) ++f.shift;
-  f.mul = (uint32_t)(((1ull << 32) * ((1ull << f.shift) - d)) / d + 1);
-  return f;
-}
-__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv &f) {
-  return (uint32_t)(((uint64_t)__umulhi(n, f.mul) + n) >> f.shift);
-}
+constexpr int kRotWarps = kRotThreads / 32;
+constexpr int kRotItems = 4;       // vectors (pairs of them) per lane in flight
+// Blocks per SM: the registers of four bf16 items (eight table entries each) leave room for two
+// (46.6 us against 52 with three and 59 with four, 268 MB), those of fp32 for four (19.0 us
+// against 21.8 with three, 84 MB).
+template <typename T>
+constexpr int kRotBlocks = sizeof(T) == 2 ? 2 : 4;
 
 struct RotParams {
   const void *q, *k, *pos;
   void *q_out, *k_out;
   const double *freqs;
-  long n;
-  int nf, Hq, Hk, d, interleaved, pos64, inverse, tokens;
+  long tasks;                      // tokens x groups
+  int nf, Hq, Hk, d, pos64, inverse, groups, per_group, turn_items, iph;
   float scale;
-  FastDiv by_iph, by_heads, by_nf;
 };
 
+// A vector as 32-bit words (two bf16 values or one float each), or one element.
 template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec {
-  T x[V];
+struct Vec {
+  using Type = uint4;
 };
-
-// V: elements per vector (1: any size and alignment).  An item is one vector of first channels
-// with the one of their partners (half layout), or one vector of adjacent pairs (interleaved,
-// V >= 2; V = 1 takes its two channels one by one), or one vector of copied channels.
-template <typename T, int V>
-__global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const RotParams p) {
-  __shared__ float2 table[kRotTable];
-  const long t0 = (long)blockIdx.x * p.tokens;
-  const int nt = (int)(p.n - t0 < p.tokens ? p.n - t0 : p.tokens);
-  const int heads = p.Hq + p.Hk;
-  const bool inter = p.interleaved != 0;
-  const int turn_items = inter ? (V == 1 ? p.nf : 2 * p.nf / V) : p.nf / V;
-  const int iph = (int)p.by_iph.d;
-  const uint32_t items = (uint32_t)nt * heads * iph;
-  using VT = Vec<T, V>;
-
-  for (uint32_t base = 0; base < items || base == 0; base += kRotThreads * kRotItems) {
-    VT a[kRotItems], b[kRotItems];
-    T *dst[kRotItems];
-    int at[kRotItems], tok[kRotItems];   // first frequency (-1: copied, -2: none), token
-    int ca[kRotItems], cb[kRotItems];
-#pragma unroll
-    for (int u = 0; u < kRotItems; ++u) {
-      const uint32_t it = base + u * kRotThreads + threadIdx.x;
-      at[u] = -2;
-      tok[u] = 0; ca[u] = cb[u] = 0; dst[u] = nullptr;
-      if (it >= items) continue;
-      const uint32_t row = div_by(it, p.by_iph), iv = it - row * iph;
-      const uint32_t tk = div_by(row, p.by_heads), h = row - tk * heads;
-      tok[u] = (int)tk;
-      const bool is_q = (int)h < p.Hq;
-      const size_t off = is_q ? ((size_t)(t0 + tk) * p.Hq + h) * p.d
-                              : ((size_t)(t0 + tk) * p.Hk + (h - p.Hq)) * p.d;
-      const T *src = static_cast<const T *>(is_q ? p.q : p.k) + off;
-      dst[u] = static_cast<T *>(is_q ? p.q_out : p.k_out) + off;
-      if ((int)iv < turn_items) {
-        at[u] = inter ? (V == 1 ? (int)iv : (int)iv * (V / 2)) : (int)iv * V;
-        ca[u] = inter ? (V == 1 ? 2 * (int)iv : (int)iv * V) : (int)iv * V;
-        cb[u] = inter ? (V == 1 ? ca[u] + 1 : -1) : ca[u] + p.nf;
-      } else {
-        at[u] = -1;
-        ca[u] = 2 * p.nf + ((int)iv - turn_items) * V;
-        cb[u] = -1;
-      }
-      a[u] = *reinterpret_cast<const VT *>(src + ca[u]);
-      if (cb[u] >= 0) b[u] = *reinterpret_cast<const VT *>(src + cb[u]);
-    }
-    if (base == 0) {
-      for (uint32_t i = threadIdx.x; i < (uint32_t)nt * p.nf; i += kRotThreads) {
-        const uint32_t tk = div_by(i, p.by_nf), fi = i - tk * p.nf;
-        const double turns = p.freqs[fi] * 0.15915494309189533577;   // 1 / (2 pi)
-        const double frac = (turns - floor(turns)) * 4294967296.0;
-        const double hi = floor(frac);
-        const uint64_t F = ((uint64_t)hi << 32) + (uint64_t)((frac - hi) * 4294967296.0);
-        const long long at_pos = p.pos64 ? static_cast<const long long *>(p.pos)[t0 + tk]
-                                         : (long long)static_cast<const int *>(p.pos)[t0 + tk];
-        const uint64_t u = (uint64_t)at_pos * F;
-        // half turns in [-1, 1)
-        float sn, cs;
-        sincospif((float)(long long)u * 1.0842021724855044e-19f, &sn, &cs);   // 2^-63
-        table[i] = make_float2(cs * p.scale, (p.inverse ? -sn : sn) * p.scale);
-      }
-      __syncthreads();
-    }
-#pragma unroll
-    for (int u = 0; u < kRotItems; ++u) {
-      if (at[u] == -2) continue;
-      if (at[u] >= 0) {
-        const float2 *cs = table + tok[u] * p.nf + at[u];
-        if (inter && V > 1) {
-#pragma unroll
-          for (int e = 0; e + 1 < V; e += 2) {
-            const float2 c = cs[e / 2];
-            const float x = to_f32(a[u].x[e]), y = to_f32(a[u].x[e + 1]);
-            a[u].x[e] = from_f32<T>(x * c.x - y * c.y);
-            a[u].x[e + 1] = from_f32<T>(y * c.x + x * c.y);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float2 c = cs[e];
-            const float x = to_f32(a[u].x[e]), y = to_f32(b[u].x[e]);
-            a[u].x[e] = from_f32<T>(x * c.x - y * c.y);
-            b[u].x[e] = from_f32<T>(y * c.x + x * c.y);
-          }
-        }
-      }
-      *reinterpret_cast<VT *>(dst[u] + ca[u]) = a[u];
-      if (cb[u] >= 0) *reinterpret_cast<VT *>(dst[u] + cb[u]) = b[u];
-    }
+template <typename T>
+struct Vec<T, 1> {
+  using Type = T;
+};
+__device__ __forceinline__ void turn(float &x, float &y, float2 c) {
+  // (fused as written, so that every path rounds alike)
+  const float u = fmaf(x, c.x, -__fmul_rn(y, c.y));
+  y = fmaf(y, c.x, __fmul_rn(x, c.y));
+  x = u;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// a word of first channels with the word of their partners
+template <typename T>
+__device__ __forceinline__ void turn_words(uint32_t &a, uint32_t &b, const float2 *c) {
+  if constexpr (sizeof(T) == 2) {
+    float x0 = low(a), y0 = low(b), x1 = high(a), y1 = high(b);
+    turn(x0, y0, c[0]);
+    turn(x1, y1, c[1]);
+    a = pack2(x0, x1);
+    b = pack2(y0, y1);
+  } else {
+    float x = __uint_as_float(a), y = __uint_as_float(b);
+    turn(x, y, c[0]);
+    a = __float_as_uint(x);
+    b = __float_as_uint(y);
   }
 }
 
-template <typename T, int V>
+// V: elements per vector (1: any size and alignment).  An item is one vector of first channels
+// with the one of their partners (half layout), or one vector of adjacent pairs (INTER, V >= 2;
+// V = 1 takes its two channels one by one), or one vector of copied channels.  A head has iph
+// items, turn_items of them turned; lane l takes item l % iph (iph <= 32) of every (32 / iph)-th
+// head, or items l, l + 32, .. of every head.
+template <typename T, int V, bool INTER>
+__global__ void __launch_bounds__(kRotThreads, kRotBlocks<T>) rotary_kernel(const RotParams p) {
+  extern __shared__ uint64_t rot_smem[];
+  uint64_t *freq = rot_smem;                                     // [nf]
+  float2 *table = reinterpret_cast<float2 *>(rot_smem + p.nf) + (threadIdx.x >> 5) * p.nf;
+  const int lane = threadIdx.x & 31;
+  using VT = typename Vec<T, V>::Type;
+  constexpr bool kTwo = !INTER || V == 1;                        // an item has a second vector
+  constexpr int kE = INTER && V > 1 ? V / 2 : V;                 // table entries of an item
+  for (int i = threadIdx.x; i < p.nf; i += kRotThreads) {
+    const double turns = p.freqs[i] * 0.15915494309189533577;   // 1 / (2 pi)
+    const double frac = (turns - floor(turns)) * 4294967296.0;
+    const double hi = floor(frac);
+    freq[i] = ((uint64_t)hi << 32) + (uint64_t)((frac - hi) * 4294967296.0);
+  }
+  __syncthreads();
+  const int rows = p.iph <= 32 ? 32 / p.iph : 1;                 // heads a warp takes at once
+  const int sub = p.iph <= 32 ? lane / p.iph : 0;
+  const bool idle = sub >= rows;
+
+  for (long task = (long)blockIdx.x * kRotWarps + (threadIdx.x >> 5); task < p.tasks;
+       task += (long)gridDim.x * kRotWarps) {
+    const long tok = p.groups == 1 ? task : task / p.groups;
+    const int grp = p.groups == 1 ? 0 : (int)(task - tok * p.groups);
+    const int h0 = grp * p.per_group, h1 = min(p.Hq + p.Hk, h0 + p.per_group);
+    bool filled = false;
+    for (int iv = p.iph <= 32 ? lane - sub * p.iph : lane; iv - lane < p.iph || !filled; iv += 32) {
+      const bool on = !idle && iv < p.iph, turned = iv < p.turn_items;
+      const int ca = turned ? (kTwo && INTER ? 2 * iv : iv * V) : 2 * p.nf + (iv - p.turn_items) * V;
+      const int cb = INTER ? ca + 1 : ca + p.nf;
+      float2 cs[kE];
+      for (int h = h0; h < h1 || !filled; h += rows * kRotItems) {
+        VT a[kRotItems], b[kRotItems];
+        T *dst[kRotItems];
+#pragma unroll
+        for (int u = 0; u < kRotItems; ++u) {
+          const int hh = h + sub + u * rows;
+          dst[u] = nullptr;
+          if (!on || hh >= h1) continue;
+          const bool is_q = hh < p.Hq;
+          const size_t off = is_q ? ((size_t)tok * p.Hq + hh) * p.d : ((size_t)tok * p.Hk + (hh - p.Hq)) * p.d;
+          const T *src = static_cast<const T *>(is_q ? p.q : p.k) + off;
+          dst[u] = static_cast<T *>(is_q ? p.q_out : p.k_out) + off;
+          a[u] = *reinterpret_cast<const VT *>(src + ca);
+          if (kTwo && turned) b[u] = *reinterpret_cast<const VT *>(src + cb);
+        }
+        if (!filled) {
+          filled = true;
+          const long long at = p.pos64 ? static_cast<const long long *>(p.pos)[tok]
+                                       : (long long)static_cast<const int *>(p.pos)[tok];
+          for (int i = lane; i < p.nf; i += 32) {
+            float sn, cn;                                        // half turns in [-1, 1)
+            sincospif((float)(long long)((uint64_t)at * freq[i]) * 1.0842021724855044e-19f, &sn, &cn);   // 2^-63
+            table[i] = make_float2(cn * p.scale, (p.inverse ? -sn : sn) * p.scale);
+          }
+          __syncwarp();
+        }
+        if (h == h0 && on && turned) {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) cs[e] = table[iv * kE + e];
+        }
+#pragma unroll
+        for (int u = 0; u < kRotItems; ++u) {
+          if (!dst[u]) continue;
+          if (turned) {
+            if constexpr (V == 1) {
+              float x = to_f32(a[u]), y = to_f32(b[u]);
+              turn(x, y, cs[0]);
+              a[u] = from_f32<T>(x);
+              b[u] = from_f32<T>(y);
+            } else if constexpr (INTER) {
+              if constexpr (sizeof(T) == 2) {
+                uint32_t *w[4] = {&a[u].x, &a[u].y, &a[u].z, &a[u].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float x = low(*w[e]), y = high(*w[e]);
+                  turn(x, y, cs[e]);
+                  *w[e] = pack2(x, y);
+                }
+              } else {
+                turn_words<T>(a[u].x, a[u].y, cs);
+                turn_words<T>(a[u].z, a[u].w, cs + 1);
+              }
+            } else {
+              constexpr int n = 4 / sizeof(T);
+              turn_words<T>(a[u].x, b[u].x, cs);
+              turn_words<T>(a[u].y, b[u].y, cs + n);
+              turn_words<T>(a[u].z, b[u].z, cs + 2 * n);
+              turn_words<T>(a[u].w, b[u].w, cs + 3 * n);
+            }
+          }
+          *reinterpret_cast<VT *>(dst[u] + ca) = a[u];
+          if (kTwo && turned) *reinterpret_cast<VT *>(dst[u] + cb) = b[u];
+        }
+      }
+      if (p.iph <= 32) break;
+    }
+    __syncwarp();                                                // (the table is free)
+  }
+}
+
+template <typename T, int V, bool INTER>
 int launch_typed(const RotaryArgs &a, cudaStream_t s) {
   RotParams p;
   p.q = a.q; p.k = a.k; p.pos = a.pos; p.q_out = a.q_out; p.k_out = a.k_out; p.freqs = a.freqs;
-  p.n = a.n; p.nf = a.n_freqs; p.Hq = a.Hq; p.Hk = a.Hk; p.d = a.d;
-  p.interleaved = a.interleaved; p.pos64 = a.pos64; p.inverse = a.inverse; p.scale = a.scale;
-  const int turn_items = a.interleaved ? (V == 1 ? a.n_freqs : 2 * a.n_freqs / V) : a.n_freqs / V;
-  const int iph = turn_items + (a.d - 2 * a.n_freqs) / V;
-  const int heads = p.Hq + p.Hk;
-  // tokens per block: enough items to fill the block's registers once, while the table holds
-  // them and every SM still has a few blocks
-  long tokens = (long)kRotThreads * kRotItems / ((long)heads * iph);
-  if (a.n_freqs > 0 && tokens > kRotTable / a.n_freqs) tokens = kRotTable / a.n_freqs;
-  if (tokens > a.n / 592) tokens = a.n / 592;
-  if (tokens < 1) tokens = 1;
-  p.tokens = (int)tokens;
-  p.by_iph = fast_div((uint32_t)iph);
-  p.by_heads = fast_div((uint32_t)heads);
-  p.by_nf = fast_div((uint32_t)(a.n_freqs > 0 ? a.n_freqs : 1));
-  const long blocks = (a.n + tokens - 1) / tokens;
-  rotary_kernel<T, V><<<(unsigned)blocks, kRotThreads, 0, s>>>(p);
+  p.nf = a.n_freqs; p.Hq = a.Hq; p.Hk = a.Hk; p.d = a.d;
+  p.pos64 = a.pos64; p.inverse = a.inverse; p.scale = a.scale;
+  p.turn_items = INTER && V > 1 ? 2 * a.n_freqs / V : a.n_freqs / V;
+  p.iph = p.turn_items + (a.d - 2 * a.n_freqs) / V;
+  const int heads = a.Hq + a.Hk;
+  // a token's heads go to several warps while there are fewer warps than the GPU holds, down to
+  // what one pass of a warp takes
+  const int pass = (p.iph <= 32 ? 32 / p.iph : 1) * kRotItems, most = (heads + pass - 1) / pass;
+  const long room = 148L * kRotBlocks<T> * kRotWarps;
+  long groups = a.n >= room ? 1 : room / a.n;
+  if (groups > most) groups = most;
+  p.per_group = (int)((heads + groups - 1) / groups);
+  p.groups = (heads + p.per_group - 1) / p.per_group;
+  p.tasks = a.n * p.groups;
+  long blocks = (p.tasks + kRotWarps - 1) / kRotWarps;
+  if (blocks > 148 * kRotBlocks<T>) blocks = 148 * kRotBlocks<T>;
+  const size_t smem = (size_t)p.nf * 8 * (1 + kRotWarps);
+  rotary_kernel<T, V, INTER><<<(unsigned)blocks, kRotThreads, smem, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
 }
 
@@ -178,7 +221,8 @@ int launch_vec(const RotaryArgs &a, cudaStream_t s) {
   // in the half layout, its half
   const bool wide = (any & 15) == 0 && a.d % V == 0 &&
                     (a.interleaved ? 2 * a.n_freqs : a.n_freqs) % V == 0;
-  return wide ? launch_typed<T, V>(a, s) : launch_typed<T, 1>(a, s);
+  if (a.interleaved) return wide ? launch_typed<T, V, true>(a, s) : launch_typed<T, 1, true>(a, s);
+  return wide ? launch_typed<T, V, false>(a, s) : launch_typed<T, 1, false>(a, s);
 }
 
 }  // namespace

@@ -338,21 +338,22 @@ def workspace_status(workspace: torch.Tensor) -> int:
 # build no message and no tuple unless one fails.
 def _lin_heads(g, lead, named):
     """(H, decay code, [heads of each tensor]) of linear attention tensors [*lead, Hx, d]."""
-    n = len(lead)
-    if g.dtype != torch.float32 or not (g.dim() == 1 or (g.dim() == n + 1 and g.shape[:-1] == lead)):
-        raise ValueError(f"g must be {tuple(lead) + ('H',)} or [H] float32, got {tuple(g.shape)}, {g.dtype}")
-    H = g.shape[-1]
+    gs, n = g.shape, len(lead)
+    fixed = len(gs) == 1
+    if g.dtype != torch.float32 or not (fixed or gs[:-1] == lead):
+        raise ValueError(f"g must be {tuple(lead) + ('H',)} or [H] float32, got {tuple(gs)}, {g.dtype}")
+    H, heads = gs[-1], []
     if H < 1:
         raise ValueError("g has no heads")
-    heads = []
     for name, t in named:
         s = t.shape
-        if len(s) != n + 2 or s[:-2] != lead:
+        if len(s) != n + 2 or s[:n] != lead:
             raise ValueError(f"{name} must be {tuple(lead) + ('heads', 'channels')}, got {tuple(s)}")
-        if s[-2] < 1 or H % s[-2]:
-            raise ValueError(f"{name} has {s[-2]} heads, which must divide g's {H}")
-        heads.append(s[-2])
-    return H, (DECAY_PER_HEAD if g.dim() == 1 else DECAY_PER_TOKEN), heads
+        x = s[n]
+        if x < 1 or H % x:
+            raise ValueError(f"{name} has {x} heads, which must divide g's {H}")
+        heads.append(x)
+    return H, (DECAY_PER_HEAD if fixed else DECAY_PER_TOKEN), heads
 
 
 def _lin_types(q, k, v):
@@ -391,46 +392,47 @@ def check_linattn_args(q, k, v, g, S0=None, cu_seqlens=None):
     return N, H, decay, heads
 
 
-def _addresses(dev, *named):
-    """Device addresses of contiguous tensors on ``dev`` (None: no address)."""
-    out, index = [], dev.index
-    for name, t in named:
+def _addresses(index, names, *tensors):
+    """Device addresses of contiguous tensors on CUDA device ``index`` (None: no address);
+    ``names`` names them for a refusal."""
+    out = []
+    for t in tensors:
         if t is None:
             out.append(None)
-        elif t.get_device() != index:
-            raise ValueError(f"{name} is on {t.device}, q on {dev}")
-        elif not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+        elif t.get_device() != index or not t.is_contiguous():
+            name = names.split()[len(out)]
+            raise ValueError(f"{name} is on {t.device}, q on cuda:{index}" if t.get_device() != index
+                             else f"{name} must be contiguous")
         else:
             out.append(t.data_ptr())
     return out
 
 
-def _call(dev, name, *args):
-    """Calls an entry point on ``dev`` and its current stream (the last argument)."""
+def _call(index, name, *args):
+    """Calls an entry point on CUDA device ``index`` and its current stream (the last argument)."""
     fn = getattr(_lib or load(), name)
-    index = dev.index
     if torch._C._cuda_getDevice() == index:
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != 0:
         raise CkdaError(name, rc)
 
 
 def _on_cuda(q):
-    if not q.is_cuda:
+    index = q.get_device()
+    if index < 0:
         raise ValueError("tensors must be on a CUDA device")
-    return q.device
+    return index
 
 
-def _room(dev, workspace, n):
-    """The workspace's address and bytes, allocated when not given (and then returned, to be kept
-    until the call has been issued)."""
+def _room(q, workspace, n):
+    """A workspace of n bytes when none is given; returns it (to be kept until the call has been
+    issued), its address and its bytes."""
     if workspace is None:
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    return workspace, _addresses(dev, ("workspace", workspace))[0], workspace.numel() * workspace.element_size()
+        workspace = q.new_empty(n, dtype=torch.uint8)
+    return workspace, _addresses(q.get_device(), "workspace", workspace)[0], workspace.numel() * workspace.element_size()
 
 
 def linattn_fwd_workspace_size(B, T, H, dk, dv, dtype, n_seqs=0) -> int:
@@ -450,19 +452,18 @@ def linattn_fwd(q, k, v, g, S0=None, cu_seqlens=None, o=None, S_T=None, workspac
     dv, n_seqs = v.shape[-1], 0 if cu_seqlens is None else N
     _lin_out("o", o, (B, T, H, dv), q.dtype)
     _lin_out("S_T", S_T, (N, H, dk, dv), torch.float32)
-    dev = _on_cuda(q)
+    index = _on_cuda(q)
     if not want_o:
         o = None
     elif o is None:
-        o = torch.empty((B, T, H, dv), dtype=q.dtype, device=dev)
+        o = q.new_empty((B, T, H, dv))
     if not want_state:
         S_T = None
     elif S_T is None:
-        S_T = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
-    workspace, wp, wn = _room(dev, workspace, linattn_fwd_workspace_size(B, T, H, dk, dv, q.dtype, n_seqs))
-    p = _addresses(dev, ("q", q), ("k", k), ("v", v), ("g", g), ("S0", S0), ("cu_seqlens", cu_seqlens),
-                   ("o", o), ("S_T", S_T))
-    _call(dev, "ckda_linattn_fwd", *p[:6], n_seqs, B, T, H, *heads, dk, dv, decay, _DT[q.dtype], *p[6:], wp, wn)
+        S_T = q.new_empty((N, H, dk, dv), dtype=torch.float32)
+    workspace, wp, wn = _room(q, workspace, linattn_fwd_workspace_size(B, T, H, dk, dv, q.dtype, n_seqs))
+    p = _addresses(index, "q k v g S0 cu_seqlens o S_T", q, k, v, g, S0, cu_seqlens, o, S_T)
+    _call(index, "ckda_linattn_fwd", *p[:6], n_seqs, B, T, H, *heads, dk, dv, decay, _DT[q.dtype], *p[6:], wp, wn)
     return o, S_T
 
 
@@ -491,38 +492,42 @@ def linattn_bwd(q, k, v, g, S0=None, cu_seqlens=None, dO=None, dS_T=None, want_d
         if want_dS0 and grads[4] is None:
             raise ValueError("dS0 buffer missing")
         _lin_out("dS0", grads[4], state, torch.float32)
-    dev = _on_cuda(q)
+    index = _on_cuda(q)
     if grads is None:
-        gq, gk, gv, gg = (torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (q, k, v, g))
-        gS0 = torch.empty(state, dtype=torch.float32, device=dev) if want_dS0 else None
+        gq, gk, gv, gg = (t.new_empty(t.shape) for t in (q, k, v, g))
+        gS0 = q.new_empty(state, dtype=torch.float32) if want_dS0 else None
     else:
         gq, gk, gv, gg, gS0 = grads
         gS0 = gS0 if want_dS0 else None
-    workspace, wp, wn = _room(dev, workspace, linattn_bwd_workspace_size(
+    workspace, wp, wn = _room(q, workspace, linattn_bwd_workspace_size(
         B, T, H, *heads, dk, dv, decay, q.dtype, n_seqs))
-    p = _addresses(dev, ("q", q), ("k", k), ("v", v), ("g", g), ("S0", S0), ("cu_seqlens", cu_seqlens),
-                   ("dO", dO), ("dS_T", dS_T), ("dq", gq), ("dk", gk), ("dv", gv), ("dg", gg), ("dS0", gS0))
-    _call(dev, "ckda_linattn_bwd", *p[:6], n_seqs, B, T, H, *heads, dk, dv, decay, _DT[q.dtype], *p[6:], wp, wn)
+    p = _addresses(index, "q k v g S0 cu_seqlens dO dS_T dq dk dv dg dS0", q, k, v, g, S0, cu_seqlens, dO, dS_T,
+                   gq, gk, gv, gg, gS0)
+    _call(index, "ckda_linattn_bwd", *p[:6], n_seqs, B, T, H, *heads, dk, dv, decay, _DT[q.dtype], *p[6:], wp, wn)
     return gq, gk, gv, gg, gS0
 
 
 def linattn_decode_step(q, k, v, g, S, o=None, want_o: bool = True):
     """One token of ``linattn_fwd``: S [B,H,dk,dv] float32 is updated in place; returns o
     [B,H,dv] (None when not wanted).  q [B,Hq,dk], k [B,Hk,dk], v [B,Hv,dv]; g [B,H] or [H]."""
-    if q.dim() != 3:
-        raise ValueError(f"q must be [B,Hq,dk], got {tuple(q.shape)}")
-    B, dk, dv = q.shape[0], q.shape[-1], v.shape[-1]
-    H, decay, heads = _lin_heads(g, q.shape[:1], (("q", q), ("k", k), ("v", v)))
+    qs, dt = q.shape, q.dtype
+    if len(qs) != 3:
+        raise ValueError(f"q must be [B,Hq,dk], got {tuple(qs)}")
+    B, _, dk = qs
+    H, decay, heads = _lin_heads(g, qs[:1], (("q", q), ("k", k), ("v", v)))
     _lin_types(q, k, v)
-    _lin_out("S", S, (B, H, dk, dv), torch.float32)
-    _lin_out("o", o, (B, H, dv), q.dtype)
-    dev = _on_cuda(q)
+    dv = v.shape[2]
+    if S.shape != (B, H, dk, dv) or S.dtype != torch.float32:
+        raise ValueError(f"S must be [B,H,dk,dv] = {(B, H, dk, dv)} float32")
+    index = _on_cuda(q)
     if not want_o:
         o = None
     elif o is None:
-        o = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
-    p = _addresses(dev, ("q", q), ("k", k), ("v", v), ("g", g), ("S", S), ("o", o))
-    _call(dev, "ckda_linattn_decode_step", *p[:5], B, H, *heads, dk, dv, decay, _DT[q.dtype], p[5])
+        o = q.new_empty((B, H, dv))
+    else:
+        _lin_out("o", o, (B, H, dv), dt)
+    p = _addresses(index, "q k v g S o", q, k, v, g, S, o)
+    _call(index, "ckda_linattn_decode_step", *p[:5], B, H, *heads, dk, dv, decay, _DT[dt], p[5])
     return o
 
 
@@ -580,15 +585,16 @@ def rotary(q, k, pos, freqs, layout: str = "half", inverse: bool = False, scale:
         raise ValueError(f"freqs must be float64 [n] with 2 n <= {d}, got {tuple(freqs.shape)}, {freqs.dtype}")
     if k is None and k_out is not None:
         raise ValueError("k_out without k")
-    _lin_out("q_out", q_out, q.shape, q.dtype)
-    if k is not None:
+    if q_out is not None:
+        _lin_out("q_out", q_out, q.shape, q.dtype)
+    if k is not None and k_out is not None:
         _lin_out("k_out", k_out, k.shape, k.dtype)
-    dev = _on_cuda(q)
+    index = _on_cuda(q)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        q_out = q.new_empty(q.shape)
     if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-    p = _addresses(dev, ("q", q), ("k", k), ("pos", pos), ("freqs", freqs), ("q_out", q_out), ("k_out", k_out))
-    _call(dev, "ckda_rotary", *p[:4], pos.numel(), q.shape[-2], 0 if k is None else k.shape[-2], d, freqs.shape[0],
-          ROTARY_LAYOUTS[layout], int(pos.dtype == torch.int64), scale, int(inverse), _DT[q.dtype], p[4], p[5])
+        k_out = k.new_empty(k.shape)
+    p = _addresses(index, "q k pos freqs q_out k_out", q, k, pos, freqs, q_out, k_out)
+    _call(index, "ckda_rotary", *p[:4], pos.numel(), q.shape[-2], 0 if k is None else k.shape[-2], d, freqs.shape[0],
+          ROTARY_LAYOUTS[layout], pos.dtype == torch.int64, scale, inverse, _DT[q.dtype], p[4], p[5])
     return q_out, k_out
