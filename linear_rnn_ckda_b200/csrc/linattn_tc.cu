@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
   auto mnmajor = [&](uint32_t at, uint32_t panel) { return kHi | (((sb + at) >> 4) | ((panel >> 4) << 16)); };
   auto gates = [&](int st) { return reinterpret_cast<float *>(sm + C::offGate + st * C::kGate); };
   // gates (floats): [0] rowf, [64] tokf, [128] colb, [192] rowb, [256] cross, [320] G (64-bit
-  // fixed point), [448] e^{G_C}, [449] mode.  P_ij is (x_i . y_j) times
+  // fixed point), [448] e^{G_C}, [449] mode, [450] G_C.  P_ij is (x_i . y_j) times
   //   kWhole : colb_j, its row's factor left to rowf (the chunk decays by at most 2^-100)
   //   kBlocks: rowb_i colb_j on the diagonal 32 x 32 blocks, cross_i cross_j (through token 31) off
   //            them (each half decays by at most 2^-100)
@@ -375,9 +375,11 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       if (lane == 0) mbar_arrive(b_s);
     };
     if (KIND != kStates) put_state();
+    long long whole = 0;                            // kStates: the segment's decay
     for (; c < nc; ++c, next(st, ph)) {
       if (!(ok = wait(b_gate + st, ph))) break;
       const float a = gates(st)[448];
+      if (KIND == kStates) whole = max(whole + *reinterpret_cast<const long long *>(gates(st) + 450), -(1ll << 52));
       const uint64_t a2 = f2pk(a, a);
       __syncwarp();
       if (lane == 0) mbar_arrive(b_empty + st);
@@ -402,6 +404,9 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         put_state();
       }
     }
+    // (a backward walk's segments but the last belong to the forward walk too, which writes theirs)
+    if (KIND == kStates && ok && tid == 0 && (!rev || u.piece == u.pieces - 1))
+      ps.decay[(size_t)blockIdx.x * p.H + h] = exp2_fixed(whole);
     if (ok && live) {
       auto store = [&](float *dst) {
         dst += (size_t)z * ps.sz;
@@ -429,8 +434,10 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 14) {
-      // -------------------------------------------------------------- loads and decays
+    if (warp == 14 || (KIND == kStates && warp == 22)) {
+      // -------------------------------------------------------------- loads (14) and decays
+      // (kStates, whose chunks are short: 14 and 22 take turns at the chunks' decays, which take a
+      // warp some 2,000 cycles)
       const int px = (ps.dx + 63) / 64, pz = (ps.dz + 63) / 64;
       const uint32_t bytes = kPanel * ((KIND != kStates ? px : 0) + px + pz + (exact ? pz : 0));
       // lane 2 t + q loads panel q of tile t (Y Z, X Y Z, or X Y Z W)
@@ -438,37 +445,35 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       const bool load = lane < 2 * C::kTiles && (lane & 1) < (tile < 2 ? px : pz) && (tile < 3 || exact);
       const int map = tile == 0 ? ps.ix : tile == 1 ? ps.iy : tile == 2 ? ps.iz : ps.iw;
       const int head = h * (tile == 0 ? ps.hx : tile == 1 ? ps.hy : tile == 2 ? ps.hz : ps.hw) / p.H;
-      long long whole = 0, all = 0;
-      float gv[2];
-      auto load_g = [&](int c) {
-        const int ci = chunk_at(c), len = rows_of(ci);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int i = 2 * lane + e;
-          gv[e] = i < len ? p.g[p.g_fixed ? (size_t)h : (size_t)(u.row0 + ci * kC + i) * p.H + h] : 0.f;
-        }
-      };
-      load_g(0);
       for (; c < nc; ++c, next(st, ph)) {
         const int ci = chunk_at(c), len = rows_of(ci);
-        if (c >= C::kStages && !(ok = wait(b_empty + st, ph ^ 1u))) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(b_full + st, bytes);
-          *s_issued = c + 1;
+        const bool turn = KIND != kStates || (c & 1) == (warp == 14 ? 0 : 1);
+        float g0 = 0.f, g1 = 0.f;
+        if (turn) {                                  // (in flight while the stage is waited for)
+          const size_t r = (size_t)(u.row0 + ci * kC) + 2 * lane;
+          if (2 * lane < len) g0 = p.g[p.g_fixed ? (size_t)h : r * p.H + h];
+          if (2 * lane + 1 < len) g1 = p.g[p.g_fixed ? (size_t)h : (r + 1) * p.H + h];
         }
-        __syncwarp();
-        if (load) {
-          // (no dO: its loads start past the tensor's end, where TMA reads 0)
-          const int row = map == 3 && p.no_dO ? 1 << 30 : (int)(u.row0 + ci * kC);
-          tma_load_3d(sm + st * C::kStage + lane * kPanel, &p.maps[map], b_full + st, 64 * (lane & 1), head, row);
+        if (c >= C::kStages && (turn || warp == 14) && !(ok = wait(b_empty + st, ph ^ 1u))) break;
+        if (warp == 14) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(b_full + st, bytes);
+            *s_issued = c + 1;
+          }
+          __syncwarp();
+          if (load) {
+            // (no dO: its loads start past the tensor's end, where TMA reads 0)
+            const int row = map == 3 && p.no_dO ? 1 << 30 : (int)(u.row0 + ci * kC);
+            tma_load_3d(sm + st * C::kStage + lane * kPanel, &p.maps[map], b_full + st, 64 * (lane & 1), head, row);
+          }
         }
+        if (!turn) continue;
         // (fixed decays: a stage that held as many rows holds the same decays)
         if (!p.g_fixed || c < C::kStages || rows_of(chunk_at(c - C::kStages)) != len) {
-          const long long x0 = 2 * lane < len ? fixed_log2(gv[0]) : 0;
-          const long long x1 = 2 * lane + 1 < len ? fixed_log2(gv[1]) : 0;
-          if (c + 1 < nc) load_g(c + 1);
+          const long long x0 = 2 * lane < len ? fixed_log2(g0) : 0;
+          const long long x1 = 2 * lane + 1 < len ? fixed_log2(g1) : 0;
           const long long sum = scan_pairs(x0, x1);
-          all = __shfl_sync(0xffffffffu, sum, 31);
+          const long long all = __shfl_sync(0xffffffffu, sum, 31);
           const long long mid = __shfl_sync(0xffffffffu, sum, 15);      // up to token 31
           const long long lim = 100ll << 32;
           const int mode = all >= -lim ? kWhole : mid >= -lim && all - mid >= -lim ? kBlocks : kPairs;
@@ -488,9 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
           };
           one(sum - x1, 2 * lane, rf.x, tf.x, cb.x, rb.x, cr.x);
           one(sum, 2 * lane + 1, rf.y, tf.y, cb.y, rb.y, cr.y);
-          reinterpret_cast<float2 *>(gt)[lane] = rf;
           reinterpret_cast<float2 *>(gt + 64)[lane] = tf;
           if (KIND != kStates) {
+            reinterpret_cast<float2 *>(gt)[lane] = rf;
             reinterpret_cast<float2 *>(gt + 128)[lane] = cb;
             if (mode != kWhole) {
               reinterpret_cast<float2 *>(gt + 192)[lane] = rb;
@@ -501,15 +506,12 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
           if (lane == 0) {
             gt[448] = exp2_fixed(all);
             gt[449] = (float)mode;
+            *reinterpret_cast<long long *>(gt + 450) = all;
           }
         }
-        whole = max(whole + all, -(1ll << 52));
         __syncwarp();
         if (lane == 0) mbar_arrive(b_gate + st);
       }
-      // (a backward walk's segments but the last belong to the forward walk too, which writes theirs)
-      if (KIND == kStates && lane == 0 && (!rev || u.piece == u.pieces - 1))
-        ps.decay[(size_t)blockIdx.x * p.H + h] = exp2_fixed(whole);
     } else if (warp == 15) {
       // -------------------------------------------------------------- issue of O
       if (KIND != kStates && lane == 0) {
