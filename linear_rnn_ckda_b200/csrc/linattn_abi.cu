@@ -77,7 +77,9 @@ int ckda_linattn_fwd(const void *q, const void *k, const void *v, const float *g
   rc = ckda::check_device();
   if (rc != CKDA_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, ckda::kWorkspaceHeader, s) != cudaSuccess) return CKDA_ERR_CUDA;
+  // the status word: a packed batch's plan and an fp32 batch's first kernel write it themselves
+  if ((!cu_seqlens && io_dtype == CKDA_BF16) || (cu_seqlens && n_seqs == 0) || (long long)B * T == 0)
+    if (cudaMemsetAsync(workspace, 0, ckda::kWorkspaceHeader, s) != cudaSuccess) return CKDA_ERR_CUDA;
   ckda::LinArgs a = {};
   a.q = q; a.k = k; a.v = v; a.g = g; a.S0 = S0; a.cu = cu_seqlens; a.o = o; a.S_T = S_T;
   a.N = cu_seqlens ? n_seqs : B;
@@ -111,7 +113,9 @@ int ckda_linattn_bwd(const void *q, const void *k, const void *v, const float *g
   rc = ckda::check_device();
   if (rc != CKDA_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, ckda::kWorkspaceHeader, s) != cudaSuccess) return CKDA_ERR_CUDA;
+  // the status word: a packed batch's plan and an fp32 batch's first kernel write it themselves
+  if ((!cu_seqlens && io_dtype == CKDA_BF16) || (cu_seqlens && n_seqs == 0) || (long long)B * T == 0)
+    if (cudaMemsetAsync(workspace, 0, ckda::kWorkspaceHeader, s) != cudaSuccess) return CKDA_ERR_CUDA;
   ckda::LinBwdArgs b = {};
   ckda::LinArgs &a = b.f;
   a.q = q; a.k = k; a.v = v; a.g = g; a.S0 = S0; a.cu = cu_seqlens;

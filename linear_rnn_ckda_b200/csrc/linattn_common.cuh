@@ -69,6 +69,17 @@ int launch_plan(const int32_t *cu, int N, int T, const PlanTable *tables, int n_
 size_t tc_workspace(bool packed, int N, int B, int T, int H, int Hq, int Hk, int Hv, int dk, int dv,
                     bool g_fixed, bool back);
 int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s);
+// dg from the row dots rho = q . dq and kappa = k . dk, each [slices, H, rows] (slices summed in
+// order), and the states after every piece and their gradients (linattn_simt.cu).
+struct DecayParams {
+  const float *S, *X;       // [slots, H, elems]: incoming states (and each sequence's end), gradients
+  const float *rho, *kappa;
+  float *dg;                // [rows, H]
+  int H, elems, slices;
+  long rows;
+  Slots slots;
+};
+void launch_decay(const DecayParams &p, long slots, cudaStream_t s);
 // Sums over the heads that share one head of x [rows, Hx, d], and of a fixed decay's gradient
 // over the rows (linattn_simt.cu).
 void launch_share(const void *part, void *out, long rows, int H, int Hx, int d, bool bf16,

@@ -1,23 +1,22 @@
 // linattn_simt.cu -- linear attention with a decay for each head in exact fp32 on CUDA cores:
-// forward and gradients, chunks of 64 tokens, three launches each way.
+// forward and gradients, chunks of 64 tokens.
 //
 //   1. lin_local_kernel: every chunk's own state  sum_j e^{G_C - G_j} k_j v_j^T  (and, backwards,
 //      its own state gradient  sum_i e^{G_i} q_i dO_i^T), all chunks side by side;
 //   2. lin_scan_kernel: the walk over a sequence's chunks, S <- e^{G_C} S + own, elementwise:
 //      one thread per four state entries, the next chunks' loads in flight;
-//   3. lin_out_kernel / lin_grad_kernel: outputs or gradients of every chunk from the state it
-//      starts with (and the state gradient it ends with), all chunks side by side.
+//   3. lin_pass_kernel: outputs or one gradient of every chunk, all chunks side by side.
 //
-// Gradients: with X the gradient with respect to the state after the chunk,
-//   dq_i = e^{G_i} S_in dO_i + sum_{j <= i} e^{G_i - G_j} (dO_i . v_j) k_j
-//   dk_j = e^{G_C - G_j} X v_j + sum_{i >= j} e^{G_i - G_j} (dO_i . v_j) q_i
-//   dv_j = e^{G_C - G_j} X^T k_j + sum_{i >= j} e^{G_i - G_j} (q_i . k_j) dO_i
-//   dg_t = <S_out, X> + sum_{s >= t, s in the chunk} (q_s . dq_s - k_s . dk_s)
-// The last follows from each G_i's derivative: outputs and gradients are sums of terms
-// e^{G_a - G_b}, the q side carrying +G and the k side -G.
+// As on the tensor cores (linattn_tc.cu) the output and the three gradients are one product with
+// the roles exchanged, X the queries, Y the keys, Z the values, M the state the chunk starts with
+// (o, dq) or the state gradient it ends with (dk, dv):
+//   out_i = rowf_i M^T x_i + sum_j e^{+-(G_i - G_j)} (x_i . y_j) z_j
+//   o : q, k, v forwards    dq : dO, v, k forwards    dk : v, dO, q    dv : k, q, dO backwards
+// and q . dq, k . dk of each token go to lin_decay_kernel for the decays' gradients.  A sequence
+// of one chunk (a short prompt) is one launch: the pass reads S0 itself and writes S_T.
 //
-// Bound: fp32 FMA and shared-memory loads (64 x d x d products per chunk and head); the states
-// between chunks add 64 KB written and read three times per 64 tokens at d = 128.
+// Bound: fp32 FMA and shared-memory loads; few chunks are split over columns of the output, which
+// repeats the scores, so that a small call occupies more SMs.
 #include "linattn_common.cuh"
 
 namespace ckda {
@@ -30,29 +29,17 @@ constexpr int kLdP = 68;     // of a 64 x 64 one
 constexpr int kTile = kC * kLd;
 constexpr int kTileP = kC * kLdP;
 
-struct ChunkParams {
-  const void *q, *k, *v, *dO;
-  const float *g;
-  float *own_S, *own_X;      // [slots, H, dk, dv]: chunks' own states, then states at the borders
-  float *decay;              // [slots, H]: e^{G_C}
-  void *o;
-  float *dq, *dk, *dv;       // gradients, or per-head shares of them (shared heads)
-  float *dg;                 // [rows, H]
-  int part_q, part_k, part_v;
-  int H, Hq, Hk, Hv, ndk, ndv, g_fixed;
-  Slots slots;
-};
-
-// Loads rows [0, len) of head `hx` of x [rows, Hx, d] into a 64 x 128 fp32 tile, zeros elsewhere.
-__device__ void load_tile(float *t, const void *x, long row0, int len, int Hx, int hx, int d) {
-  const float *src = static_cast<const float *>(x) + ((size_t)row0 * Hx + hx) * d;
-  for (int i = threadIdx.x; i < kC * 32; i += kThreads) {
-    const int r = i >> 5, c = (i & 31) * 4;
+// Loads rows [0, len) x columns [c0, c0 + cols) of head hx of x [rows, Hx, d] into a tile of row
+// stride ld, zeros past len, d or where x is NULL.
+__device__ void load_tile(float *t, int ld, const float *x, long row0, int len, int Hx, int hx, int d,
+                          int c0, int cols) {
+  const float *src = x + ((size_t)row0 * Hx + hx) * d + c0;
+  const int n4 = cols / 4;
+  for (int i = threadIdx.x; i < kC * n4; i += kThreads) {
+    const int r = i / n4, c = (i - r * n4) * 4;
     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (x && r < len && c < d) {
-      f = *reinterpret_cast<const float4 *>(src + (size_t)r * Hx * d + c);
-    }
-    *reinterpret_cast<float4 *>(t + r * kLd + c) = f;
+    if (x && r < len && c0 + c < d) f = *reinterpret_cast<const float4 *>(src + (size_t)r * Hx * d + c);
+    *reinterpret_cast<float4 *>(t + r * ld + c) = f;
   }
 }
 
@@ -66,7 +53,7 @@ __device__ __forceinline__ float pair_weight(float2 a, float2 b) {     // 2^(a -
   return exp2f((a.x - b.x) + (a.y - b.y));
 }
 // The chunk's sums G_i (hi, lo; base 2) to sG[0 .. 63], rows past len continuing the last;
-// e^{G_i} to sE and e^{G_C - G_i} to sW.  One warp; the caller synchronises.
+// e^{G_i} to sE and e^{G_C - G_i} (0 past len) to sW.  One warp; the caller synchronises.
 __device__ void chunk_gates(float2 *sG, float *sE, float *sW, const float *g, long row0, int len,
                             int H, int h, int g_fixed) {
   const int lane = threadIdx.x;
@@ -89,13 +76,12 @@ __device__ void chunk_gates(float2 *sG, float *sE, float *sW, const float *g, lo
   }
 }
 
-// acc[4][NJ] += A (64 x K) B (K x 16 NJ) for this thread's rows 4 ty .. 4 ty + 3.  KC: the
-// operand is stored [row][k] (k contiguous); else [k][row].  Columns: tx + 16 j with a KC B,
-// 4 tx + 64 (j / 4) + j % 4 otherwise (both free of bank conflicts).
-template <int NJ, bool AKC, bool BKC>
-__device__ __forceinline__ void mm(float (&acc)[4][NJ], const float *A, int lda, const float *B,
-                                   int ldb, int K, int jmax) {
+// acc[4][NJ] += A (64 x K) B (K x 16 NJ) for this thread's rows 4 ty .. 4 ty + 3.  A is stored
+// [row][k] (AKC: k contiguous) or [k][row]; B [k][column], columns NJ tx .. NJ tx + NJ - 1.
+template <int NJ, bool AKC>
+__device__ __forceinline__ void mm(float (&acc)[4][NJ], const float *A, int lda, const float *B, int ldb, int K) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 2
   for (int k = 0; k < K; k += 4) {
     float a[4][4], b[4][NJ];       // [k][..]
 #pragma unroll
@@ -107,22 +93,14 @@ __device__ __forceinline__ void mm(float (&acc)[4][NJ], const float *A, int lda,
       } else {
         a[i][0] = f.x; a[i][1] = f.y; a[i][2] = f.z; a[i][3] = f.w;
       }
-    }
-    if (BKC) {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j < jmax) f = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * ldb + k);
-        b[0][j] = f.x; b[1][j] = f.y; b[2][j] = f.z; b[3][j] = f.w;
+      const float *bp = B + (k + i) * ldb + NJ * tx;
+      if constexpr (NJ == 4) {
+        const float4 e = *reinterpret_cast<const float4 *>(bp);
+        b[i][0] = e.x; b[i][1] = e.y; b[i][2] = e.z; b[i][3] = e.w;
+      } else {
+        const float2 e = *reinterpret_cast<const float2 *>(bp);
+        b[i][0] = e.x; b[i][1] = e.y;
       }
-    } else {
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-        for (int j = 0; j < NJ; j += 4) {
-          const float4 f = *reinterpret_cast<const float4 *>(B + (k + kk) * ldb + 4 * tx + 16 * j);
-          b[kk][j] = f.x; b[kk][j + 1] = f.y; b[kk][j + 2] = f.z; b[kk][j + 3] = f.w;
-        }
     }
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
@@ -132,6 +110,28 @@ __device__ __forceinline__ void mm(float (&acc)[4][NJ], const float *A, int lda,
         for (int j = 0; j < NJ; ++j) acc[i][j] = fmaf(a[kk][i], b[kk][j], acc[i][j]);
   }
 }
+// the same with B stored [column][k], columns tx + 16 j (free of bank conflicts)
+__device__ __forceinline__ void mm_scores(float (&acc)[4][4], const float *A, const float *B, int K) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 2
+  for (int k = 0; k < K; k += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = *reinterpret_cast<const float4 *>(A + (4 * ty + i) * kLd + k);
+      b[i] = *reinterpret_cast<const float4 *>(B + (tx + 16 * i) * kLd + k);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
+        acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
+        acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
+        acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+      }
+  }
+}
 template <int NJ>
 __device__ __forceinline__ void zero(float (&acc)[4][NJ]) {
 #pragma unroll
@@ -139,79 +139,88 @@ __device__ __forceinline__ void zero(float (&acc)[4][NJ]) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = 0.f;
 }
-// column of acc[.][j]
-template <bool BKC>
-__device__ __forceinline__ int col_of(int j) {
-  const int tx = threadIdx.x & 15;
-  return BKC ? tx + 16 * j : 4 * tx + 64 * (j >> 2) + (j & 3);
+template <int NJ>
+__device__ __forceinline__ void put_row(float *dst, const float (&v)[NJ]) {
+  if constexpr (NJ == 4) *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+  else *reinterpret_cast<float2 *>(dst) = make_float2(v[0], v[1]);
+}
+
+// The status word of an unpacked batch (a packed one's plan writes it).
+__device__ __forceinline__ void clear_status(const Slots &s, int *status) {
+  if (!s.cu && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *status = 0;
 }
 
 // ---------------------------------------------------------------- chunks' own states
-// blockIdx: (slot, head, direction); direction 1: own_X from q, dO with weights e^{G_i}.
-__global__ void __launch_bounds__(kThreads) lin_local_kernel(const ChunkParams p) {
-  extern __shared__ __align__(16) float sm[];
-  float *sY = sm, *sZ = sm + kTile;
-  float2 *sG = reinterpret_cast<float2 *>(sZ + kTile);
-  float *sE = reinterpret_cast<float *>(sG + kC), *sW = sE + kC;
+struct LocalParams {
+  const float *y[2], *z[2];  // k, v; q, dO
+  int hy[2], hz[2];
+  const float *g;
+  float *own[2];             // [slots, H, dk, dv]
+  float *decay;              // [slots, H]: e^{G_C}
+  int *status;
+  int H, ndk, ndv, g_fixed, cols;
+  Slots slots;
+};
+// blockIdx: (slot, head, (direction, block of 64 rows, slice of 16 NJ columns)); direction 1: own
+// state gradients, with weights e^{G_i}.
+template <int NJ>
+__global__ void __launch_bounds__(kThreads) lin_local_kernel(const LocalParams p) {
+  __shared__ __align__(16) float sY[kTileP], sZ[kTileP];
+  __shared__ float2 sG[kC];
+  __shared__ float sE[kC], sW[kC];
+  clear_status(p.slots, p.status);
   Piece u;
   if (!find_piece(p.slots, blockIdx.x, u)) return;
-  const int h = blockIdx.y, back = blockIdx.z;
+  const int h = blockIdx.y, blocks = (p.ndk + 63) / 64;
+  const int slice = blockIdx.z % p.cols, m0 = 64 * (blockIdx.z / p.cols % blocks), back = blockIdx.z / (p.cols * blocks);
+  const int c0 = 16 * NJ * slice, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   chunk_gates(sG, sE, sW, p.g, u.row0, u.len, p.H, h, p.g_fixed);
-  const int Hy = back ? p.Hq : p.Hk, Hz = back ? p.H : p.Hv;
-  load_tile(sY, back ? p.q : p.k, u.row0, u.len, Hy, h * Hy / p.H, p.ndk);
-  load_tile(sZ, back ? p.dO : p.v, u.row0, u.len, Hz, h * Hz / p.H, p.ndv);
+  load_tile(sY, kLdP, p.y[back], u.row0, u.len, p.hy[back], h * p.hy[back] / p.H, p.ndk, m0, 64);
+  load_tile(sZ, kLdP, p.z[back], u.row0, u.len, p.hz[back], h * p.hz[back] / p.H, p.ndv, c0, 16 * NJ);
   __syncthreads();
   const float *w = back ? sE : sW;
-  for (int i = threadIdx.x; i < kC * 32; i += kThreads) {
-    const int r = i >> 5, c = (i & 31) * 4;
-    float4 *z = reinterpret_cast<float4 *>(sZ + r * kLd + c);
-    const float s = r < u.len ? w[r] : 0.f;
-    *z = make_float4(z->x * s, z->y * s, z->z * s, z->w * s);
+  for (int i = threadIdx.x; i < kC * 4 * NJ; i += kThreads) {
+    const int r = i / (4 * NJ);
+    float4 *z = reinterpret_cast<float4 *>(sZ + r * kLdP + (i - r * 4 * NJ) * 4);
+    *z = make_float4(z->x * w[r], z->y * w[r], z->z * w[r], z->w * w[r]);
   }
   __syncthreads();
   const size_t at = (size_t)blockIdx.x * p.H + h;
-  if (threadIdx.x == 0 && !back) p.decay[at] = sE[kC - 1];
-  float *out = (back ? p.own_X : p.own_S) + at * p.ndk * p.ndv;
-  const int ty = threadIdx.x >> 4;
-  for (int m0 = 0; m0 < p.ndk; m0 += 64) {
-    float acc[4][8];
-    zero(acc);
-    mm<8, false, false>(acc, sY + m0, kLd, sZ, kLd, kC, 8);
+  if (threadIdx.x == 0 && blockIdx.z == 0) p.decay[at] = sE[kC - 1];
+  float acc[4][NJ];
+  zero(acc);
+  mm<NJ, false>(acc, sY, kLdP, sZ, kLdP, kC);
+  float *out = p.own[back] + at * p.ndk * p.ndv + c0 + NJ * tx;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = m0 + 4 * ty + i;
-      if (r >= p.ndk) continue;
-#pragma unroll
-      for (int j = 0; j < 8; j += 4) {
-        const int c = col_of<false>(j);
-        if (c < p.ndv)
-          *reinterpret_cast<float4 *>(out + (size_t)r * p.ndv + c) =
-              make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
-      }
-    }
-  }
+  for (int i = 0; i < 4; ++i)
+    if (m0 + 4 * ty + i < p.ndk && c0 + NJ * tx < p.ndv) put_row<NJ>(out + (size_t)(m0 + 4 * ty + i) * p.ndv, acc[i]);
 }
 
 // ---------------------------------------------------------------- walk over the chunks
-// blockIdx: (sequence, head, block of 4 x 128 entries); replaces each chunk's own state by the
-// state before it (back: after it).  keep_end: the end state also goes to the spare slot.
+// blockIdx: (sequence, head, direction x block of 4 x 128 entries); replaces each chunk's own state
+// by the state before it (direction 1: after it).  keep: the forward end state also goes to the
+// spare slot.
 struct ScanParams {
-  float *own;
-  const float *decay, *init;
-  float *end;
-  int H, elems, back, keep_end;
+  float *own[2];
+  const float *init[2];
+  float *end[2];
+  const float *decay;
+  int H, elems, blocks, keep;
   Slots slots;
 };
 __global__ void __launch_bounds__(128) lin_scan_kernel(const ScanParams p) {
   if (p.slots.cu && *p.slots.status) return;
-  const int n = blockIdx.x, h = blockIdx.y;
-  const int e = (blockIdx.z * 128 + threadIdx.x) * 4;
+  const int n = blockIdx.x, h = blockIdx.y, back = blockIdx.z >= p.blocks;
+  const int e = ((blockIdx.z - (back ? p.blocks : 0)) * 128 + threadIdx.x) * 4;
   if (e >= p.elems) return;
+  float *const own = back ? p.own[1] : p.own[0];
+  const float *const init = back ? p.init[1] : p.init[0];
+  float *const end = back ? p.end[1] : p.end[0];
   const int len = p.slots.cu ? p.slots.cu[n + 1] - p.slots.cu[n] : p.slots.T;
   const int nc = (len + kC - 1) / kC;
   const long base = p.slots.base(n);
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (p.init) S = *reinterpret_cast<const float4 *>(p.init + ((size_t)n * p.H + h) * p.elems + e);
+  if (init) S = *reinterpret_cast<const float4 *>(init + ((size_t)n * p.H + h) * p.elems + e);
   constexpr int kAhead = 4;
   for (int c0 = 0; c0 < nc; c0 += kAhead) {
     float4 d[kAhead];
@@ -219,245 +228,199 @@ __global__ void __launch_bounds__(128) lin_scan_kernel(const ScanParams p) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (c0 + u >= nc) continue;
-      const size_t at = (size_t)(base + (p.back ? nc - 1 - c0 - u : c0 + u)) * p.H + h;
-      d[u] = *reinterpret_cast<const float4 *>(p.own + at * p.elems + e);
+      const size_t at = (size_t)(base + (back ? nc - 1 - c0 - u : c0 + u)) * p.H + h;
+      d[u] = *reinterpret_cast<const float4 *>(own + at * p.elems + e);
       a[u] = p.decay[at];
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (c0 + u >= nc) continue;
-      const size_t at = (size_t)(base + (p.back ? nc - 1 - c0 - u : c0 + u)) * p.H + h;
-      *reinterpret_cast<float4 *>(p.own + at * p.elems + e) = S;
+      const size_t at = (size_t)(base + (back ? nc - 1 - c0 - u : c0 + u)) * p.H + h;
+      *reinterpret_cast<float4 *>(own + at * p.elems + e) = S;
       S.x = fmaf(a[u], S.x, d[u].x); S.y = fmaf(a[u], S.y, d[u].y);
       S.z = fmaf(a[u], S.z, d[u].z); S.w = fmaf(a[u], S.w, d[u].w);
     }
   }
-  if (p.keep_end) *reinterpret_cast<float4 *>(p.own + ((size_t)(base + nc) * p.H + h) * p.elems + e) = S;
-  if (p.end) *reinterpret_cast<float4 *>(p.end + ((size_t)n * p.H + h) * p.elems + e) = S;
+  if (!back && p.keep) *reinterpret_cast<float4 *>(own + ((size_t)(base + nc) * p.H + h) * p.elems + e) = S;
+  if (end) *reinterpret_cast<float4 *>(end + ((size_t)n * p.H + h) * p.elems + e) = S;
 }
 
-// Copies rows [r0, r0 + 64) x all columns of a [R][Cc] state into a tile (zeros outside).
-__device__ void load_state(float *t, const float *S, int r0, int R, int Cc) {
-  for (int i = threadIdx.x; i < 64 * 32; i += kThreads) {
-    const int r = i >> 5, c = (i & 31) * 4;
-    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r0 + r < R && c < Cc) f = *reinterpret_cast<const float4 *>(S + (size_t)(r0 + r) * Cc + c);
-    *reinterpret_cast<float4 *>(t + r * kLd + c) = f;
-  }
-}
+// ---------------------------------------------------------------- outputs and gradients
+struct SimtPass {
+  const float *x, *y, *z, *w;  // w: partner of the row dots, or NULL
+  int hx, hy, hz, hw, dx, dz;
+  int rev, across;             // across: z channels are the state's rows (dq, dk), else its columns
+  const float *state;          // [slots, H, dk, dv], or (one chunk a sequence) [N, H, dk, dv] or NULL
+  float *out;                  // [rows, H, dz]
+  float *dots;                 // [slices, H, rows]
+  float *end;                  // one chunk a sequence: S_T
+};
+struct PassParams {
+  SimtPass pass[3];
+  const float *g;
+  int *status;
+  int H, g_fixed, elems, single, slices;
+  long rows;
+  Slots slots;
+};
+constexpr int kPassSmem = (3 * kTile + kTileP + 4 * kC) * 4;
+constexpr int kSingleSmem = kPassSmem + kTile * 4;
 
-// P[i][j] = acc o 2^{G_i - G_j} for j <= i (columns of a KC product), 0 above the diagonal.
-__device__ __forceinline__ void store_scores(float *P, const float (&acc)[4][4], const float2 *sG) {
-  const int ty = threadIdx.x >> 4;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = 4 * ty + i, c = col_of<true>(j);
-      P[r * kLdP + c] = c <= r ? acc[i][j] * pair_weight(sG[r], sG[c]) : 0.f;
-    }
-}
-
-// ---------------------------------------------------------------- outputs
-__global__ void __launch_bounds__(kThreads) lin_out_kernel(const ChunkParams p) {
+// blockIdx: (slot, head, pass x slice of 16 NJ output columns)
+template <int NJ>
+__global__ void __launch_bounds__(kThreads) lin_pass_kernel(const PassParams p) {
   extern __shared__ __align__(16) float sm[];
-  float *sQ = sm, *sK = sQ + kTile, *sV = sK + kTile, *sP = sV + kTile;
+  float *sX = sm, *sY = sX + kTile, *sZ = sY + kTile, *sP = sZ + kTile;
   float2 *sG = reinterpret_cast<float2 *>(sP + kTileP);
   float *sE = reinterpret_cast<float *>(sG + kC), *sW = sE + kC;
+  float *sS = p.single ? sW + kC : sY;           // the state's rows, over Y once the scores are done
+  if (p.single) clear_status(p.slots, p.status);
   Piece u;
   if (!find_piece(p.slots, blockIdx.x, u)) return;
-  const int h = blockIdx.y, ty = threadIdx.x >> 4;
+  const int pi = blockIdx.z / p.slices;
+  const SimtPass &ps = p.pass[pi];
+  const int h = blockIdx.y, c0 = 16 * NJ * (blockIdx.z - pi * p.slices), tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  if (c0 >= ps.dz) return;
   chunk_gates(sG, sE, sW, p.g, u.row0, u.len, p.H, h, p.g_fixed);
-  load_tile(sQ, p.q, u.row0, u.len, p.Hq, h * p.Hq / p.H, p.ndk);
-  load_tile(sK, p.k, u.row0, u.len, p.Hk, h * p.Hk / p.H, p.ndk);
-  load_tile(sV, p.v, u.row0, u.len, p.Hv, h * p.Hv / p.H, p.ndv);
+  load_tile(sX, kLd, ps.x, u.row0, u.len, ps.hx, h * ps.hx / p.H, ps.dx, 0, ps.dx);
+  load_tile(sY, kLd, ps.y, u.row0, u.len, ps.hy, h * ps.hy / p.H, ps.dx, 0, ps.dx);
+  load_tile(sZ, kLd, ps.z, u.row0, u.len, ps.hz, h * ps.hz / p.H, ps.dz, c0, 16 * NJ);
   __syncthreads();
   {
     float acc[4][4];
     zero(acc);
-    mm<4, true, true>(acc, sQ, kLd, sK, kLd, p.ndk, 4);
-    store_scores(sP, acc, sG);
+    mm_scores(acc, sX, sY, ps.dx);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 4 * ty + i, c = tx + 16 * j;
+        const float w = ps.rev ? pair_weight(sG[c], sG[r]) : pair_weight(sG[r], sG[c]);
+        sP[r * kLdP + c] = (ps.rev ? c >= r && c < u.len : c <= r) ? acc[i][j] * w : 0.f;
+      }
   }
-  float acc[4][8];
+  float acc[4][NJ];
   zero(acc);
-  const float *S = p.own_S + ((size_t)blockIdx.x * p.H + h) * p.ndk * p.ndv;
-  for (int m0 = 0; m0 < p.ndk; m0 += 64) {      // e^{G} (q S), the state's rows 64 at a time
-    __syncthreads();                            // (sK's scores are done)
-    load_state(sK, S, m0, p.ndk, p.ndv);
+  const float *S = ps.state;
+  if (S) S += ((size_t)(p.single ? u.n : blockIdx.x) * p.H + h) * p.elems;
+  for (int m0 = 0; S && m0 < ps.dx; m0 += 64) {    // rowf (x M): the state's x channels 64 at a time
+    const int nr = min(64, ps.dx - m0);
+    __syncthreads();                               // (sY's scores, or the rows before, are done)
+    if (ps.across) {
+      // [z][x] rows, transposed on the way: lanes take rows, so the stores are free of conflicts
+      for (int i = tid; i < 16 * NJ * (nr / 4); i += kThreads) {
+        const int n = i % (16 * NJ), k = i / (16 * NJ) * 4;
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c0 + n < ps.dz) f = *reinterpret_cast<const float4 *>(S + (size_t)(c0 + n) * ps.dx + m0 + k);
+        sS[k * kLd + n] = f.x; sS[(k + 1) * kLd + n] = f.y; sS[(k + 2) * kLd + n] = f.z; sS[(k + 3) * kLd + n] = f.w;
+      }
+    } else {
+      for (int i = tid; i < nr * 4 * NJ; i += kThreads) {
+        const int r = i / (4 * NJ), c = (i - r * 4 * NJ) * 4;
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c0 + c < ps.dz) f = *reinterpret_cast<const float4 *>(S + (size_t)(m0 + r) * ps.dz + c0 + c);
+        *reinterpret_cast<float4 *>(sS + r * kLd + c) = f;
+      }
+    }
     __syncthreads();
-    mm<8, true, false>(acc, sQ + m0, kLd, sK, kLd, min(64, p.ndk - m0), 8);
+    mm<NJ, true>(acc, sX + m0, kLd, sS, kLd, nr);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] *= sE[4 * ty + i];
-  mm<8, true, false>(acc, sP, kLdP, sV, kLd, kC, 8);
+    for (int j = 0; j < NJ; ++j) acc[i][j] *= (ps.rev ? sW : sE)[4 * ty + i];
+  __syncthreads();                                 // (sP)
+  mm<NJ, true>(acc, sP, kLdP, sZ, kLd, kC);
+  const int col = c0 + NJ * tx;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 4 * ty + i;
-    if (r >= u.len) continue;
-    float *o = static_cast<float *>(p.o) + ((size_t)(u.row0 + r) * p.H + h) * p.ndv;
+    if (ps.out && r < u.len && col < ps.dz) put_row<NJ>(ps.out + ((size_t)(u.row0 + r) * p.H + h) * ps.dz + col, acc[i]);
+    if (ps.dots) {                                 // over the 16 threads of a row, then the slices
+      float d = 0.f;
+      if (r < u.len && col < ps.dz) {
+        const float *w = ps.w + ((size_t)(u.row0 + r) * ps.hw + h * ps.hw / p.H) * ps.dz + col;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (col_of<false>(j) < p.ndv) o[col_of<false>(j)] = acc[i][j];
+        for (int j = 0; j < NJ; ++j) d = fmaf(w[j], acc[i][j], d);
+      }
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+      if (tx == 0 && r < u.len)
+        ps.dots[((size_t)(blockIdx.z - pi * p.slices) * p.H + h) * p.rows + u.row0 + r] = d;
+    }
   }
-}
-
-// ---------------------------------------------------------------- gradients
-// Writes one gradient, or this head's share of it (part).  Columns of an NC product.
-__device__ __forceinline__ void store_grad(float *out, int part, const float (&acc)[4][8], const Piece &u,
-                                           int Hx, int H, int h, int d) {
-  const int ty = threadIdx.x >> 4;
+  if (!p.single || !ps.end) return;
+  // S_T = e^{G_C} S0 + sum_j e^{G_C - G_j} k_j v_j^T
+  __syncthreads();
+  for (int i = tid; i < kC * 4 * NJ; i += kThreads) {
+    const int r = i / (4 * NJ);
+    float4 *z = reinterpret_cast<float4 *>(sZ + r * kLd + (i - r * 4 * NJ) * 4);
+    *z = make_float4(z->x * sW[r], z->y * sW[r], z->z * sW[r], z->w * sW[r]);
+  }
+  __syncthreads();
+  float *end = ps.end + ((size_t)u.n * p.H + h) * p.elems;
+  for (int m0 = 0; m0 < ps.dx; m0 += 64) {
+    zero(acc);
+    mm<NJ, false>(acc, sY + m0, kLd, sZ, kLd, kC);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * ty + i;
-    if (r >= u.len) continue;
-    const size_t off = part ? ((size_t)(u.row0 + r) * H + h) * d
-                            : ((size_t)(u.row0 + r) * Hx + h) * d;
+    for (int i = 0; i < 4; ++i) {
+      const int r = m0 + 4 * ty + i;
+      if (r >= ps.dx || col >= ps.dz) continue;
+      if (S) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = col_of<false>(j);
-      if (c >= d) continue;
-      out[off + c] = acc[i][j];
+        for (int j = 0; j < NJ; ++j) acc[i][j] = fmaf(sE[kC - 1], S[(size_t)r * ps.dz + col + j], acc[i][j]);
+      }
+      put_row<NJ>(end + (size_t)r * ps.dz + col, acc[i]);
     }
   }
 }
-// rows' dot products x_r . acc_r, summed over the 16 threads of a row, added to s[r] * sign
-__device__ __forceinline__ void row_dots(float *s, const float *X, const float (&acc)[4][8], float sign) {
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float d = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) d = fmaf(X[(4 * ty + i) * kLd + col_of<false>(j)], acc[i][j], d);
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-    if (tx == 0) s[4 * ty + i] += sign * d;
-  }
-}
 
-__global__ void __launch_bounds__(kThreads) lin_grad_kernel(const ChunkParams p) {
-  extern __shared__ __align__(16) float sm[];
-  float *sQ = sm, *sK = sQ + kTile, *sV = sK + kTile, *sD = sV + kTile, *sS = sD + kTile;
-  float *sP = sS + kTile;                      // scores' gradients, then scores
-  float2 *sG = reinterpret_cast<float2 *>(sP + kTileP);
-  float *sE = reinterpret_cast<float *>(sG + kC), *sW = sE + kC, *sR = sW + kC;
-  __shared__ float s_red[kThreads / 32];
+// ---------------------------------------------------------------- decay gradients
+// dg_t = <S_out, X> + sum_{s >= t} (q_s . dq_s - k_s . dk_s) over a segment, S_out the state
+// after it and X its gradient.  One block per (segment or chunk, head).
+__global__ void __launch_bounds__(256) lin_decay_kernel(const DecayParams p) {
+  __shared__ double s_sum[8];
   Piece u;
   if (!find_piece(p.slots, blockIdx.x, u)) return;
-  const int h = blockIdx.y, tid = threadIdx.x, ty = tid >> 4;
-  const int dk = p.ndk, dv = p.ndv;
-  chunk_gates(sG, sE, sW, p.g, u.row0, u.len, p.H, h, p.g_fixed);
-  if (tid < kC) sR[tid] = 0.f;
-  load_tile(sQ, p.q, u.row0, u.len, p.Hq, h * p.Hq / p.H, dk);
-  load_tile(sK, p.k, u.row0, u.len, p.Hk, h * p.Hk / p.H, dk);
-  load_tile(sV, p.v, u.row0, u.len, p.Hv, h * p.Hv / p.H, dv);
-  load_tile(sD, p.dO, u.row0, u.len, p.H, h, dv);
-  const size_t elems = (size_t)dk * dv;
-  const float *S = p.own_S + ((size_t)blockIdx.x * p.H + h) * elems;
-  const float *S_out = p.own_S + ((size_t)(blockIdx.x + 1) * p.H + h) * elems;
-  const float *X = p.own_X + ((size_t)blockIdx.x * p.H + h) * elems;
-  // <S_out, X>, the part of dg that every token of the chunk shares
-  float dot = 0.f;
-  for (size_t e = tid; e < elems; e += kThreads) dot = fmaf(S_out[e], X[e], dot);
+  const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float4 *S = reinterpret_cast<const float4 *>(p.S + ((size_t)(blockIdx.x + 1) * p.H + h) * p.elems);
+  const float4 *X = reinterpret_cast<const float4 *>(p.X + ((size_t)blockIdx.x * p.H + h) * p.elems);
+  float part = 0.f;
+  for (int e = tid; e < p.elems / 4; e += 256) {
+    const float4 a = S[e], b = X[e];
+    part = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, part))));
+  }
+  double dot = part;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-  if ((tid & 31) == 0) s_red[tid >> 5] = dot;
+  if (lane == 0) s_sum[warp] = dot;
   __syncthreads();
-  {
-    float acc[4][4];
-    zero(acc);
-    mm<4, true, true>(acc, sD, kLd, sV, kLd, dv, 4);
-    store_scores(sP, acc, sG);
-  }
-  float acc[4][8];
-  // dq: dO S^T (column n = key channel, 64 state rows at a time), then the chunk's own part
-  zero(acc);
-  for (int m0 = 0; m0 < dk; m0 += 64) {
-    __syncthreads();
-    load_state(sS, S, m0, dk, dv);
-    __syncthreads();
-    float part[4][4];
-    zero(part);
-    mm<4, true, true>(part, sD, kLd, sS, kLd, dv, 4);
-    // columns m0 + tx + 16 j go through shared memory to the NC layout of acc
-    __syncthreads();
+  double run = 0.0;                              // <S_out, X> plus the blocks after this one
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sS[(4 * ty + i) * kLd + col_of<true>(j)] = part[i][j] * sE[4 * ty + i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (m0 == 0) acc[i][j] = sS[(4 * ty + i) * kLd + 4 * (tid & 15) + j];
-        else acc[i][4 + j] = sS[(4 * ty + i) * kLd + 4 * (tid & 15) + j];
-  }
-  mm<8, true, false>(acc, sP, kLdP, sK, kLd, kC, 8);
-  row_dots(sR, sQ, acc, 1.f);
-  store_grad(p.dq, p.part_q, acc, u, p.Hq, p.H, h, dk);
-  // dk: X v_j likewise
-  zero(acc);
-  for (int m0 = 0; m0 < dk; m0 += 64) {
-    __syncthreads();
-    load_state(sS, X, m0, dk, dv);
-    __syncthreads();
-    float part[4][4];
-    zero(part);
-    mm<4, true, true>(part, sV, kLd, sS, kLd, dv, 4);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sS[(4 * ty + i) * kLd + col_of<true>(j)] = part[i][j] * sW[4 * ty + i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (m0 == 0) acc[i][j] = sS[(4 * ty + i) * kLd + 4 * (tid & 15) + j];
-        else acc[i][4 + j] = sS[(4 * ty + i) * kLd + 4 * (tid & 15) + j];
-  }
-  mm<8, false, false>(acc, sP, kLdP, sQ, kLd, kC, 8);
-  row_dots(sR, sK, acc, -1.f);
-  store_grad(p.dk, p.part_k, acc, u, p.Hk, p.H, h, dk);
-  __syncthreads();                            // the scores' gradients and sR are done
-  {
-    float sc[4][4];
-    zero(sc);
-    mm<4, true, true>(sc, sQ, kLd, sK, kLd, dk, 4);
-    store_scores(sP, sc, sG);
-  }
-  // dv: X^T k_j, state rows 64 at a time, then the chunk's own part
-  zero(acc);
-  for (int m0 = 0; m0 < dk; m0 += 64) {
-    __syncthreads();
-    load_state(sS, X, m0, dk, dv);
-    __syncthreads();
-    mm<8, true, false>(acc, sK + m0, kLd, sS, kLd, min(64, dk - m0), 8);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] *= sW[4 * ty + i];
-  mm<8, false, false>(acc, sP, kLdP, sD, kLd, kC, 8);
-  store_grad(p.dv, p.part_v, acc, u, p.Hv, p.H, h, dv);
-  // dg: suffix sums within the chunk (two rows per lane, from the end)
-  if (tid < 32) {
-    float all = 0.f;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) all += s_red[w];
-    const int i1 = kC - 1 - 2 * tid, i0 = i1 - 1;
-    const float r1 = sR[i1], r0 = sR[i0];
-    float sum = r0 + r1;
+  for (int w = 0; w < 8; ++w) run += s_sum[w];
+  const size_t row = (size_t)h * p.rows + u.row0, all_rows = (size_t)p.H * p.rows;
+  // 256 tokens at a time from the end; thread 0 takes the last of them
+  for (int top = u.len; top > 0; top -= 256) {
+    const int i = top - 1 - tid;
+    double x = 0.0;
+    for (int y = 0; i >= 0 && y < p.slices; ++y)
+      x += (double)p.rho[y * all_rows + row + i] - (double)p.kappa[y * all_rows + row + i];
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const float y = __shfl_up_sync(0xffffffffu, sum, off);
-      if (tid >= off) sum += y;
+      const double y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
     }
-    if (i0 < u.len) p.dg[(size_t)(u.row0 + i0) * p.H + h] = all + sum;
-    if (i1 < u.len) p.dg[(size_t)(u.row0 + i1) * p.H + h] = all + (sum - r0);
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    double before = 0.0, all = 0.0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) before += s_sum[w];
+      all += s_sum[w];
+    }
+    if (i >= 0) p.dg[(size_t)(u.row0 + i) * p.H + h] = (float)(run + before + x);
+    run += all;
   }
 }
 
@@ -494,23 +457,35 @@ __global__ void __launch_bounds__(256) lin_fixed_kernel(const float *__restrict_
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// Columns of an output that one block computes (16 NJ): 64, or 32 where that alone makes up for
+// few chunks (two blocks an SM at most).
+int slice_columns(long units, int d) { return d > 32 && units * (d / 64 + (d < 64)) >= 148 ? 64 : 32; }
+
 // Workspace past the header: the slot table, decays, the chunks' states, and backwards the state
-// gradients and what shared heads and fixed decays sum over.
+// gradients and what decay gradients, shared heads and fixed decays are summed from.
 struct SimtLayout {
   long slots;
-  size_t table, decay, S, X, pq, pk, pv, dg, total;
+  bool single;              // one chunk a sequence, forward: no states in between
+  int cols;                 // output columns of a block
+  size_t table, decay, S, X, rho, kappa, pq, pk, pv, dg, total;
 };
 SimtLayout layout(bool packed, int N, int T, int B, int H, int Hq, int Hk, int Hv, int dk, int dv,
                   bool g_fixed, bool back) {
   SimtLayout L;
   const size_t rows = (size_t)B * T;
   L.slots = slot_count(packed, N, T, kC, 1);
+  L.single = !packed && !back && T > 0 && T <= kC;
+  const int most = dk > dv ? dk : dv;
+  L.cols = slice_columns(((long)T / kC + 1) * (packed ? 1 : B) * H * (back ? 3 : 1), back ? most : dv);
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t r = at; at += round256(bytes); return r; };
+  const size_t states = L.single ? 0 : (size_t)L.slots * H * dk * dv * 4, slices = (dk + L.cols - 1) / L.cols;
   L.table = take(packed ? (size_t)L.slots * 4 : 0);
-  L.decay = take((size_t)L.slots * H * 4);
-  L.S = take((size_t)L.slots * H * dk * dv * 4);
-  L.X = take(back ? (size_t)L.slots * H * dk * dv * 4 : 0);
+  L.decay = take(L.single ? 0 : (size_t)L.slots * H * 4);
+  L.S = take(states);
+  L.X = take(back ? states : 0);
+  L.rho = take(back ? slices * rows * H * 4 : 0);
+  L.kappa = take(back ? slices * rows * H * 4 : 0);
   L.pq = take(back && Hq < H ? rows * H * dk * 4 : 0);
   L.pk = take(back && Hk < H ? rows * H * dk * 4 : 0);
   L.pv = take(back && Hv < H ? rows * H * dv * 4 : 0);
@@ -519,62 +494,76 @@ SimtLayout layout(bool packed, int N, int T, int B, int H, int Hq, int Hk, int H
   return L;
 }
 
-constexpr int kLocalSmem = (2 * kTile + 4 * kC) * 4;
-constexpr int kOutSmem = (3 * kTile + kTileP + 4 * kC) * 4;
-constexpr int kGradSmem = (5 * kTile + kTileP + 5 * kC) * 4;
-
-template <typename K>
-bool set_smem(K kern, int bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-}
-
-int run_simt(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
-  const SimtLayout L = layout(a.cu != nullptr, a.N, a.T, a.B, a.H, a.Hq, a.Hk, a.Hv, a.dk, a.dv,
-                              a.g_fixed, b != nullptr);
-  ChunkParams p = {};
-  p.q = a.q; p.k = a.k; p.v = a.v; p.g = a.g; p.o = a.o;
-  p.own_S = reinterpret_cast<float *>(a.ws + L.S);
-  p.own_X = reinterpret_cast<float *>(a.ws + L.X);
-  p.decay = reinterpret_cast<float *>(a.ws + L.decay);
-  p.H = a.H; p.Hq = a.Hq; p.Hk = a.Hk; p.Hv = a.Hv; p.ndk = a.dk; p.ndv = a.dv; p.g_fixed = a.g_fixed;
-  p.slots = Slots{a.cu, reinterpret_cast<const int *>(a.ws + L.table), a.status, a.N, a.T, kC, 1};
+template <int NJ>
+int run_cols(const LinArgs &a, const LinBwdArgs *b, const SimtLayout &L, cudaStream_t s) {
+  const int elems = a.dk * a.dv;
+  const unsigned slots = (unsigned)L.slots, H = (unsigned)a.H;
+  float *S = reinterpret_cast<float *>(a.ws + L.S), *X = reinterpret_cast<float *>(a.ws + L.X);
+  const Slots sl{a.cu, reinterpret_cast<const int *>(a.ws + L.table), a.status, a.N, a.T, kC, 1};
+  const long rows = (long)a.B * a.T;
+  auto f32 = [](const void *p) { return static_cast<const float *>(p); };
   if (a.cu) {
     const PlanTable t{reinterpret_cast<int *>(a.ws + L.table), kC, 1, L.slots};
     const int rc = launch_plan(a.cu, a.N, a.T, &t, 1, a.status, s);
     if (rc != CKDA_OK) return rc;
   }
-  if (b) {
-    p.dO = b->dO;
-    p.part_q = a.Hq < a.H; p.part_k = a.Hk < a.H; p.part_v = a.Hv < a.H;
-    p.dq = p.part_q ? reinterpret_cast<float *>(a.ws + L.pq) : static_cast<float *>(b->dq);
-    p.dk = p.part_k ? reinterpret_cast<float *>(a.ws + L.pk) : static_cast<float *>(b->dk);
-    p.dv = p.part_v ? reinterpret_cast<float *>(a.ws + L.pv) : static_cast<float *>(b->dv);
-    p.dg = a.g_fixed ? reinterpret_cast<float *>(a.ws + L.dg) : b->dg;
+  if (!L.single) {
+    LocalParams l = {};
+    l.y[0] = f32(a.k); l.z[0] = f32(a.v); l.hy[0] = a.Hk; l.hz[0] = a.Hv; l.own[0] = S;
+    if (b) {
+      l.y[1] = f32(a.q); l.z[1] = f32(b->dO); l.hy[1] = a.Hq; l.hz[1] = a.H; l.own[1] = X;
+    }
+    l.g = a.g; l.decay = reinterpret_cast<float *>(a.ws + L.decay); l.status = a.status;
+    l.H = a.H; l.ndk = a.dk; l.ndv = a.dv; l.g_fixed = a.g_fixed; l.cols = (a.dv + 16 * NJ - 1) / (16 * NJ); l.slots = sl;
+    const dim3 grid(slots, H, (unsigned)(l.cols * ((a.dk + 63) / 64) * (b ? 2 : 1)));
+    if (slots > 0) lin_local_kernel<NJ><<<grid, kThreads, 0, s>>>(l);
+    ScanParams c = {};
+    c.own[0] = S; c.own[1] = X;
+    c.init[0] = a.S0; c.init[1] = b ? b->dS_T : nullptr;
+    c.end[0] = a.S_T; c.end[1] = b ? b->dS0 : nullptr;
+    c.decay = l.decay; c.H = a.H; c.elems = elems; c.blocks = (elems / 4 + 127) / 128; c.keep = b != nullptr; c.slots = sl;
+    lin_scan_kernel<<<dim3((unsigned)a.N, H, (unsigned)(c.blocks * (b ? 2 : 1))), 128, 0, s>>>(c);
   }
-  const dim3 grid((unsigned)L.slots, (unsigned)a.H, b ? 2 : 1);
-  const int elems = a.dk * a.dv;
-  const dim3 scan((unsigned)a.N, (unsigned)a.H, (unsigned)((elems / 4 + 127) / 128));
-  if (!set_smem(lin_local_kernel, kLocalSmem) || !set_smem(lin_out_kernel, kOutSmem) ||
-      !set_smem(lin_grad_kernel, kGradSmem))
+  if (rows == 0 || (!b && !a.o && !L.single)) return cudaGetLastError() == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
+  const int smem = L.single ? kSingleSmem : kPassSmem;
+  if (cudaFuncSetAttribute(lin_pass_kernel<NJ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return CKDA_ERR_CUDA;
-  if (grid.x > 0) lin_local_kernel<<<grid, kThreads, kLocalSmem, s>>>(p);
-  ScanParams f{p.own_S, p.decay, a.S0, a.S_T, a.H, elems, 0, b != nullptr, p.slots};
-  lin_scan_kernel<<<scan, 128, 0, s>>>(f);
-  if (b) {
-    ScanParams r{p.own_X, p.decay, b->dS_T, b->dS0, a.H, elems, 1, 0, p.slots};
-    lin_scan_kernel<<<scan, 128, 0, s>>>(r);
+  PassParams p = {};
+  p.g = a.g; p.status = a.status; p.H = a.H; p.g_fixed = a.g_fixed; p.elems = elems; p.single = L.single; p.rows = rows;
+  p.slots = sl;
+  if (!b) {
+    p.pass[0] = SimtPass{f32(a.q), f32(a.k), f32(a.v), nullptr, a.Hq, a.Hk, a.Hv, 0, a.dk, a.dv, 0, 0,
+                         L.single ? a.S0 : S, static_cast<float *>(a.o), nullptr, L.single ? a.S_T : nullptr};
+    p.slices = (a.dv + 16 * NJ - 1) / (16 * NJ);
+    lin_pass_kernel<NJ><<<dim3(slots, H, (unsigned)p.slices), kThreads, smem, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
   }
-  const dim3 flat(grid.x, grid.y);
-  if (grid.x > 0 && !b && a.o) lin_out_kernel<<<flat, kThreads, kOutSmem, s>>>(p);
-  if (b) {
-    const long rows = (long)a.B * a.T;
-    if (grid.x > 0) lin_grad_kernel<<<flat, kThreads, kGradSmem, s>>>(p);
-    if (p.part_q) launch_share(p.dq, b->dq, rows, a.H, a.Hq, a.dk, false, a.status, s);
-    if (p.part_k) launch_share(p.dk, b->dk, rows, a.H, a.Hk, a.dk, false, a.status, s);
-    if (p.part_v) launch_share(p.dv, b->dv, rows, a.H, a.Hv, a.dv, false, a.status, s);
-    if (a.g_fixed) launch_fixed(p.dg, b->dg, rows, a.H, a.status, s);
-  }
+  const bool part_q = a.Hq < a.H, part_k = a.Hk < a.H, part_v = a.Hv < a.H;
+  float *rho = reinterpret_cast<float *>(a.ws + L.rho), *kappa = reinterpret_cast<float *>(a.ws + L.kappa);
+  float *pq = part_q ? reinterpret_cast<float *>(a.ws + L.pq) : static_cast<float *>(b->dq);
+  float *pk = part_k ? reinterpret_cast<float *>(a.ws + L.pk) : static_cast<float *>(b->dk);
+  float *pv = part_v ? reinterpret_cast<float *>(a.ws + L.pv) : static_cast<float *>(b->dv);
+  const float *q = f32(a.q), *k = f32(a.k), *v = f32(a.v), *dO = f32(b->dO);
+  p.pass[0] = SimtPass{dO, v, k, q, a.H, a.Hv, a.Hk, a.Hq, a.dv, a.dk, 0, 1, S, pq, rho, nullptr};
+  p.pass[1] = SimtPass{v, dO, q, k, a.Hv, a.H, a.Hq, a.Hk, a.dv, a.dk, 1, 1, X, pk, kappa, nullptr};
+  p.pass[2] = SimtPass{k, q, dO, nullptr, a.Hk, a.Hq, a.H, 0, a.dk, a.dv, 1, 0, X, pv, nullptr, nullptr};
+  const int most = a.dk > a.dv ? a.dk : a.dv;
+  p.slices = (most + 16 * NJ - 1) / (16 * NJ);
+  lin_pass_kernel<NJ><<<dim3(slots, H, (unsigned)(3 * p.slices)), kThreads, smem, s>>>(p);
+  DecayParams d = {};
+  d.S = S; d.X = X; d.rho = rho; d.kappa = kappa; d.slices = (a.dk + 16 * NJ - 1) / (16 * NJ);
+  d.dg = a.g_fixed ? reinterpret_cast<float *>(a.ws + L.dg) : b->dg;
+  d.H = a.H; d.elems = elems; d.rows = rows; d.slots = sl;
+  launch_decay(d, L.slots, s);
+  if (part_q) launch_share(pq, b->dq, rows, a.H, a.Hq, a.dk, false, a.status, s);
+  if (part_k) launch_share(pk, b->dk, rows, a.H, a.Hk, a.dk, false, a.status, s);
+  if (part_v) launch_share(pv, b->dv, rows, a.H, a.Hv, a.dv, false, a.status, s);
+  if (a.g_fixed) launch_fixed(d.dg, b->dg, rows, a.H, a.status, s);
   return cudaGetLastError() == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
+}
+int run_simt(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
+  const SimtLayout L = layout(a.cu != nullptr, a.N, a.T, a.B, a.H, a.Hq, a.Hk, a.Hv, a.dk, a.dv, a.g_fixed, b != nullptr);
+  return L.cols == 64 ? run_cols<4>(a, b, L, s) : run_cols<2>(a, b, L, s);
 }
 
 // ---------------------------------------------------------------- packed batches
@@ -585,10 +574,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t *cu, int N, in
     const int s = cu[n], e = cu[n + 1];
     bad |= s < 0 || e < s || e > T || (n == 0 && s != 0) || (n == N - 1 && e != T);
   }
-  if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) *status = CKDA_ERR_SEQLENS;
-    return;
-  }
+  const bool any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *status = any ? CKDA_ERR_SEQLENS : CKDA_OK;
+  if (any) return;
   for (int x = 0; x < 2; ++x) {
     const PlanTable t = x ? t1 : t0;
     if (!t.table) continue;
@@ -603,6 +591,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t *cu, int N, in
 
 }  // namespace
 
+void launch_decay(const DecayParams &p, long slots, cudaStream_t s) {
+  lin_decay_kernel<<<dim3((unsigned)slots, (unsigned)p.H), 256, 0, s>>>(p);
+}
 void launch_share(const void *part, void *out, long rows, int H, int Hx, int d, bool bf16,
                   const int *status, cudaStream_t s) {
   const long n = rows * Hx * d;

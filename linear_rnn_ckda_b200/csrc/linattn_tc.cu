@@ -943,61 +943,6 @@ __global__ void __launch_bounds__(128) lin_join_kernel(const JoinParams p) {
   if (m == 0 && p.end[back]) *reinterpret_cast<float4 *>(p.end[back] + own) = S;
 }
 
-// ------------------------------------------------------------------ decay gradients
-// dg_t = <S_out, X> + sum_{s >= t} (q_s . dq_s - k_s . dk_s) over a segment, S_out the state
-// after it and X its gradient.  One block per (segment, head).
-struct DecayParams {
-  const float *S, *X;       // [slots, H, elems]: incoming states (and the last's end), gradients
-  const float *rho, *kappa; // [H, rows]
-  float *dg;                // [rows, H]
-  int H, elems;
-  long rows;
-  Slots slots;
-};
-__global__ void __launch_bounds__(256) lin_decay_kernel(const DecayParams p) {
-  __shared__ double s_sum[8];
-  Piece u;
-  if (!find_piece(p.slots, blockIdx.x, u)) return;
-  const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const float4 *S = reinterpret_cast<const float4 *>(p.S + ((size_t)(blockIdx.x + 1) * p.H + h) * p.elems);
-  const float4 *X = reinterpret_cast<const float4 *>(p.X + ((size_t)blockIdx.x * p.H + h) * p.elems);
-  float part = 0.f;
-  for (int e = tid; e < p.elems / 4; e += 256) {
-    const float4 a = S[e], b = X[e];
-    part = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, part))));
-  }
-  double dot = part;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-  if (lane == 0) s_sum[warp] = dot;
-  __syncthreads();
-  double run = 0.0;                              // <S_out, X> plus the blocks after this one
-#pragma unroll
-  for (int w = 0; w < 8; ++w) run += s_sum[w];
-  const float *rho = p.rho + (size_t)h * p.rows + u.row0, *kap = p.kappa + (size_t)h * p.rows + u.row0;
-  // 256 tokens at a time from the end; thread 0 takes the last of them
-  for (int top = u.len; top > 0; top -= 256) {
-    const int i = top - 1 - tid;
-    double x = i >= 0 ? (double)rho[i] - (double)kap[i] : 0.0;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, x, off);
-      if (lane >= off) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_sum[warp] = x;
-    __syncthreads();
-    double before = 0.0, all = 0.0;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      if (w < warp) before += s_sum[w];
-      all += s_sum[w];
-    }
-    if (i >= 0) p.dg[(size_t)(u.row0 + i) * p.H + h] = (float)(run + before + x);
-    run += all;
-  }
-}
-
 // ------------------------------------------------------------------ host
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -1177,10 +1122,10 @@ int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
     if (!p.pass[i].part && !make_map(&p.outs[i], p.pass[i].out, a.H, rows, p.pass[i].dz, true)) return CKDA_ERR_CUDA;
   if (!launch<kGrad>(p, dim3(slots, H, 3), s)) return CKDA_ERR_CUDA;
   DecayParams d = {};
-  d.S = segS; d.X = segX; d.rho = rho; d.kappa = kappa;
+  d.S = segS; d.X = segX; d.rho = rho; d.kappa = kappa; d.slices = 1;
   d.dg = a.g_fixed ? reinterpret_cast<float *>(a.ws + l.dg) : b->dg;
   d.H = a.H; d.elems = p.elems; d.rows = rows; d.slots = p.slots;
-  lin_decay_kernel<<<dim3(slots, H), 256, 0, s>>>(d);
+  launch_decay(d, l.slots, s);
   if (part_q) launch_share(pq.out, b->dq, rows, a.H, a.Hq, a.dk, true, a.status, s);
   if (part_k) launch_share(pk.out, b->dk, rows, a.H, a.Hk, a.dk, true, a.status, s);
   if (part_v) launch_share(pv.out, b->dv, rows, a.H, a.Hv, a.dv, true, a.status, s);
