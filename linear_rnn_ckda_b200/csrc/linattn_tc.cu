@@ -71,16 +71,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// 16 lanes x 32 columns as 8 x 8 blocks: registers 4 k, 4 k + 1 hold lane t / 4, columns 8 k + 2 (t % 4)
+// 16 lanes x 16 columns as 8 x 8 blocks: registers 4 k, 4 k + 1 hold lane t / 4, columns 8 k + 2 (t % 4)
 // and the next; 4 k + 2, 4 k + 3 the same of lane t / 4 + 8
-__device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+__device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
 // four 8 x 8 blocks of 16-bit values, transposed: lane t's register i is column t / 4, rows 2 (t % 4)
 // and the next, of block i; lane 8 i + r gives the address of block i's row r
@@ -99,6 +95,11 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
@@ -347,25 +348,25 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     // M as the next chunk's operand
     auto put_state = [&]() {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (32 * b >= ps.dx) break;
-        uint32_t r[C::kTerms][16];
+      for (int b = 0; b < 8; ++b) {
+        if (16 * b >= ps.dx) break;
+        uint32_t r[C::kTerms][8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          r[0][i] = pack_bf16(M[16 * b + i]);
+        for (int i = 0; i < 8; ++i) {
+          r[0][i] = pack_bf16(M[8 * b + i]);
           if constexpr (KIND == kGrad) {
             if (!exact) continue;
-            uint64_t x = f2sub(M[16 * b + i], unpack_bf16(r[0][i]));
+            uint64_t x = f2sub(M[8 * b + i], unpack_bf16(r[0][i]));
             r[1][i] = pack_bf16(x);
             x = f2sub(x, unpack_bf16(r[1][i]));
             r[2][i] = pack_bf16(x);
           }
         }
-        tmem_st16(lanes + C::cM + 16 * b, r[0]);
+        tmem_st8(lanes + C::cM + 8 * b, r[0]);
         if constexpr (KIND == kGrad) {
           if (exact) {
-            tmem_st16(lanes + C::cM + 64 + 16 * b, r[1]);
-            tmem_st16(lanes + C::cM + 128 + 16 * b, r[2]);
+            tmem_st8(lanes + C::cM + 64 + 8 * b, r[1]);
+            tmem_st8(lanes + C::cM + 128 + 8 * b, r[2]);
           }
         }
       }
@@ -768,79 +769,104 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         const long row0 = u.row0 + ci * kC + 32 * g;
         if (!(ok = wait(b_gate + st, ph))) break;
         const bool apart = gt[449] != (float)kWhole;
-        uint64_t f[4], d[4];                                        // rowf of this lane's two tokens a block; dots
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 x = *reinterpret_cast<const float2 *>(gt + 32 * g + 8 * k + tk);
-          f[k] = f2pk(x.x, x.y);
-          d[k] = 0;
-        }
+        float *rd = red + ob * 256 + quad * 64;
         if (!(ok = wait(b_o + ob, c >> 1))) break;
         tc_fence_after();
-        uint32_t pk[2][8];                                          // [y][2 k + m]: block k, channel ch + 16 y + 8 m
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {                      // 16 tokens, two blocks
+          const int t0 = 16 * half + tk;
+          uint64_t f[2], d[2];                                      // rowf of this lane's two tokens a block; dots
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          uint32_t r[16];
-          tmem_ld_blocks(lanes + ((16u * y) << 16) + C::cO + 64 * ob, r);
-          tmem_wait_ld();
-          uint64_t v[8];
+          for (int k = 0; k < 2; ++k) {
+            const float2 x = *reinterpret_cast<const float2 *>(gt + 32 * g + t0 + 8 * k);
+            f[k] = f2pk(x.x, x.y);
+            d[k] = 0;
+          }
+          uint32_t pk[2][4];                                        // [y][2 k + m]: block k, channel ch + 16 y + 8 m
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = f2mul(f[i >> 1], f2bits(r[2 * i], r[2 * i + 1]));
-          if (apart) {
-            tmem_ld_blocks(lanes + ((16u * y) << 16) + C::cO + 64 * (ob ^ 1), r);
+          for (int y = 0; y < 2; ++y) {
+            uint32_t r[8];
+            tmem_ld_blocks(lanes + ((16u * y) << 16) + C::cO + 64 * ob + 16 * half, r);
             tmem_wait_ld();
+            uint64_t v[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = f2add(v[i], f2bits(r[2 * i], r[2 * i + 1]));
-          }
-          if (y == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_ofree + ob);
-          }
+            for (int i = 0; i < 4; ++i) v[i] = f2mul(f[i >> 1], f2bits(r[2 * i], r[2 * i + 1]));
+            if (apart) {
+              tmem_ld_blocks(lanes + ((16u * y) << 16) + C::cO + 64 * (ob ^ 1) + 16 * half, r);
+              tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) pk[y][i] = pack_bf16(v[i]);
-          if (!tma && any) {
+              for (int i = 0; i < 4; ++i) v[i] = f2add(v[i], f2bits(r[2 * i], r[2 * i + 1]));
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int t = 8 * (i >> 1) + tk, z = ch + 16 * y + 8 * (i & 1);
-              float a, b;
-              f2up(v[i], a, b);
-              const size_t step = (size_t)p.H * ps.dz, at = ((size_t)(row0 + t) * p.H + h) * ps.dz + z;
-              if (z >= ps.dz) continue;
-              if (KIND == kGrad && ps.part) {
-                if (t < len) static_cast<float *>(ps.out)[at] = a;
-                if (t + 1 < len) static_cast<float *>(ps.out)[at + step] = b;
-              } else {
-                if (t < len) static_cast<__nv_bfloat16 *>(ps.out)[at] = __float2bfloat16_rn(a);
-                if (t + 1 < len) static_cast<__nv_bfloat16 *>(ps.out)[at + step] = __float2bfloat16_rn(b);
+            for (int i = 0; i < 4; ++i) pk[y][i] = pack_bf16(v[i]);
+            if (!tma && any) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int t = t0 + 8 * (i >> 1), z = ch + 16 * y + 8 * (i & 1);
+                float a, b;
+                f2up(v[i], a, b);
+                const size_t step = (size_t)p.H * ps.dz, at = ((size_t)(row0 + t) * p.H + h) * ps.dz + z;
+                if (z >= ps.dz) continue;
+                if (KIND == kGrad && ps.part) {
+                  if (t < len) static_cast<float *>(ps.out)[at] = a;
+                  if (t + 1 < len) static_cast<float *>(ps.out)[at + step] = b;
+                } else {
+                  if (t < len) static_cast<__nv_bfloat16 *>(ps.out)[at] = __float2bfloat16_rn(a);
+                  if (t + 1 < len) static_cast<__nv_bfloat16 *>(ps.out)[at + step] = __float2bfloat16_rn(b);
+                }
               }
             }
-          }
-          if constexpr (KIND == kGrad) {
-            if (exact) {
-              // products with W, two 8 x 8 blocks of two channel groups at a time
-              const uint32_t wt = sb + st * C::kStage + C::oW + (quad >> 1) * kPanel;
-#pragma unroll
-              for (int k = 0; k < 4; k += 2) {
-                const int row = 32 * g + 8 * (k + (lane >> 4)) + (lane & 7);
+            if constexpr (KIND == kGrad) {
+              if (exact) {
+                // products with W, the two blocks of two channel groups
+                const uint32_t wt = sb + st * C::kStage + C::oW + (quad >> 1) * kPanel;
+                const int row = 32 * g + 16 * half + 8 * (lane >> 4) + (lane & 7);
                 uint32_t w[4];
                 ldmatrix4_t(wt + row * 128 + (((4 * (quad & 1) + 2 * y + (lane >> 3 & 1)) ^ (row & 7)) << 4), w);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if (32 * quad + 16 * y < ps.dz) d[k + (e >> 1)] = f2fma(v[2 * k + e], unpack_bf16(w[e]), d[k + (e >> 1)]);
+                  if (32 * quad + 16 * y < ps.dz) d[e >> 1] = f2fma(v[e], unpack_bf16(w[e]), d[e >> 1]);
               }
+            }
+          }
+          if (half == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_ofree + ob);
+          }
+          if (tma) {
+            if (half == 0) {
+              if (lane == 0) bulk_wait_read();                     // (the last store has been read)
+              __syncwarp();
+            }
+            // rows of 64 bytes, 16-byte pieces permuted by row / 2 % 4 (64-byte swizzle)
+            const int row = 16 * half + (lane & 7);
+            const uint32_t at = sb + mine + row * 64 + (((lane >> 3) ^ (row >> 1 & 3)) << 4);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) stmatrix4_t(at + 512 * k, pk[0][2 * k], pk[0][2 * k + 1], pk[1][2 * k], pk[1][2 * k + 1]);
+          }
+          if constexpr (KIND == kGrad) {
+            if (exact) {
+              // four tokens' sums over this lane's channels, then over the lanes that hold the same
+              // tokens (bits 2-4): two of them end up with one token
+              float s4[4];
+              f2up(d[0], s4[0], s4[1]);
+              f2up(d[1], s4[2], s4[3]);
+#pragma unroll
+              for (int step = 2; step >= 1; step >>= 1) {
+                const bool up = lane & (8 * step);
+#pragma unroll
+                for (int i = 0; i < step; ++i) {
+                  const float send = up ? s4[i] : s4[i + step], keep = up ? s4[i + step] : s4[i];
+                  s4[i] = keep + __shfl_xor_sync(0xffffffffu, send, 8 * step);
+                }
+              }
+              s4[0] += __shfl_xor_sync(0xffffffffu, s4[0], 4);
+              if (!(lane & 4)) rd[t0 + 8 * (lane >> 4) + (lane >> 3 & 1)] = s4[0];
             }
           }
         }
         if (tma) {
-          if (lane == 0) bulk_wait_read();                         // (the last store has been read)
-          __syncwarp();
-          // rows of 64 bytes, 16-byte pieces permuted by row / 2 % 4 (64-byte swizzle)
-          const int row = lane & 7;
-          const uint32_t at = sb + mine + row * 64 + (((lane >> 3) ^ (row >> 1)) << 4);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            stmatrix4_t(at + 512 * k, pk[0][2 * k], pk[0][2 * k + 1], pk[1][2 * k], pk[1][2 * k + 1]);
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) {
@@ -850,22 +876,6 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         }
         if constexpr (KIND == kGrad) {
           if (exact) {
-            // 8 tokens' sums over this lane's channels, then over the lanes that hold the same
-            // tokens (bits 2-4), each of which ends up with one token
-            float s8[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) f2up(d[k], s8[2 * k], s8[2 * k + 1]);
-#pragma unroll
-            for (int step = 4; step >= 1; step >>= 1) {
-              const bool up = lane & (4 * step);
-#pragma unroll
-              for (int i = 0; i < step; ++i) {
-                const float send = up ? s8[i] : s8[i + step], keep = up ? s8[i + step] : s8[i];
-                s8[i] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * step);
-              }
-            }
-            float *rd = red + ob * 256;
-            rd[quad * 64 + 8 * (lane >> 3) + tk + (lane >> 2 & 1)] = s8[0];
             __syncwarp();
             // (two barriers: a warp may be a chunk ahead of another that waits for its store)
             if (lane == 0) mbar_arrive(b_red + ob);
