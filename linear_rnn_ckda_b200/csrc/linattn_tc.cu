@@ -39,6 +39,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+
 #include "internal.h"
 #include "linattn_common.cuh"
 #include "sm100.cuh"
@@ -168,7 +170,7 @@ static_assert(Cfg<kOut>::kSmem <= 232448 && Cfg<kGrad>::kSmem <= 232448 && Cfg<k
               "shared memory");
 
 struct Pass {
-  int ix, iy, iz, iw;             // tensor maps (iw < 0: no row dots)
+  int ix, iy, iz, iw;             // tensor maps (iw: kGrad's row dots)
   int hx, hy, hz, hw;             // their heads
   int dx, dz;                     // channels of X and Y, of Z
   int rev;
@@ -181,7 +183,7 @@ struct Pass {
   float *decay;                   // kStates: [slots, H] the segment's whole decay
   void *out;                      // [rows, H, dz]
   int part;                       // out is fp32 per-head shares of a shared head's gradient
-  float *dots;                    // [H, rows] row dots, or NULL
+  float *dots;                    // kGrad: [H, rows] row dots
 };
 struct Params {
   CUtensorMap maps[4];            // q, k, v, dO
@@ -210,7 +212,7 @@ __device__ __forceinline__ void give_up(volatile int *abort, int *status) {
 }
 
 template <int KIND>
-__global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_constant__ Params p) {
+__device__ __forceinline__ void lin_tc(const Params &p) {
   using C = Cfg<KIND>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -298,7 +300,6 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
   //   kBlocks: rowb_i colb_j on the diagonal 32 x 32 blocks, cross_i cross_j (through token 31) off
   //            them (each half decays by at most 2^-100)
   //   kPairs : each pair's own weight on the diagonal blocks, cross_i cross_j off them
-  const bool exact = KIND == kGrad && ps.iw >= 0;   // row dots: M and P in three terms
   // a warp's wait (all lanes agree on the outcome) and a single thread's
   auto wait = [&](uint64_t *b, uint32_t ph) { return __all_sync(0xffffffffu, bar_wait(b, ph, s_abort)) != 0; };
   auto need = [&](uint64_t *b, uint32_t ph) { return bar_wait(b, ph, s_abort); };
@@ -355,7 +356,6 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         for (int i = 0; i < 8; ++i) {
           r[0][i] = pack_bf16(M[8 * b + i]);
           if constexpr (KIND == kGrad) {
-            if (!exact) continue;
             uint64_t x = f2sub(M[8 * b + i], unpack_bf16(r[0][i]));
             r[1][i] = pack_bf16(x);
             x = f2sub(x, unpack_bf16(r[1][i]));
@@ -364,10 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         }
         tmem_st8(lanes + C::cM + 8 * b, r[0]);
         if constexpr (KIND == kGrad) {
-          if (exact) {
-            tmem_st8(lanes + C::cM + 64 + 8 * b, r[1]);
-            tmem_st8(lanes + C::cM + 128 + 8 * b, r[2]);
-          }
+          tmem_st8(lanes + C::cM + 64 + 8 * b, r[1]);
+          tmem_st8(lanes + C::cM + 128 + 8 * b, r[2]);
         }
       }
       tmem_wait_st();
@@ -440,10 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       // (kStates, whose chunks are short: 14 and 22 take turns at the chunks' decays, which take a
       // warp some 2,000 cycles)
       const int px = (ps.dx + 63) / 64, pz = (ps.dz + 63) / 64;
-      const uint32_t bytes = kPanel * ((KIND != kStates ? px : 0) + px + pz + (exact ? pz : 0));
+      const uint32_t bytes = kPanel * ((KIND != kStates ? px : 0) + px + pz + (KIND == kGrad ? pz : 0));
       // lane 2 t + q loads panel q of tile t (Y Z, X Y Z, or X Y Z W)
       const int tile = (lane >> 1) + (KIND == kStates ? 1 : 0);
-      const bool load = lane < 2 * C::kTiles && (lane & 1) < (tile < 2 ? px : pz) && (tile < 3 || exact);
+      const bool load = lane < 2 * C::kTiles && (lane & 1) < (tile < 2 ? px : pz);
       const int map = tile == 0 ? ps.ix : tile == 1 ? ps.iy : tile == 2 ? ps.iz : ps.iw;
       const int head = h * (tile == 0 ? ps.hx : tile == 1 ? ps.hy : tile == 2 ? ps.hz : ps.hw) / p.H;
       for (; c < nc; ++c, next(st, ph)) {
@@ -541,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
           const uint64_t x = kmajor(st * C::kStage + C::oX);
           const uint32_t d = tmem + C::cO + 64 * ob;
           out1(d, tmem + C::cM, x, false);
-          if (exact) {
+          if (KIND == kGrad) {
             out1(d, tmem + C::cM + 64, x, true);
             out1(d, tmem + C::cM + 128, x, true);
           }
@@ -556,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
           mma_bf16_ss(d2, dz, dp, id2, !apart);
 #pragma unroll
           for (int k = 1; k < 4; ++k) mma_bf16_ss(d2, dz + 128 * k, dp + 2 * k, id2, true);
-          if (exact) {
+          if (KIND == kGrad) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               mma_bf16_ss(d2, dz + 128 * (k & 3), dp + (1 + (k >> 2)) * (kPanel >> 4) + 2 * (k & 3), id2, true);
@@ -724,7 +722,6 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
               uint64_t x = f2pk(m & (1u << (2 * j)) ? a : 0.f, m & (2u << (2 * j)) ? b : 0.f);
               r[0][j] = pack_bf16(x);
               if constexpr (KIND == kGrad) {
-                if (!exact) continue;
                 x = f2sub(x, unpack_bf16(r[0][j]));
                 r[1][j] = pack_bf16(x);
                 x = f2sub(x, unpack_bf16(r[1][j]));
@@ -734,10 +731,8 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             uint8_t *at = P + (((j0 / 8) ^ (row & 7)) << 4);
             *reinterpret_cast<uint4 *>(at) = make_uint4(r[0][0], r[0][1], r[0][2], r[0][3]);
             if constexpr (KIND == kGrad) {
-              if (exact) {
-                *reinterpret_cast<uint4 *>(at + kPanel) = make_uint4(r[1][0], r[1][1], r[1][2], r[1][3]);
-                *reinterpret_cast<uint4 *>(at + 2 * kPanel) = make_uint4(r[2][0], r[2][1], r[2][2], r[2][3]);
-              }
+              *reinterpret_cast<uint4 *>(at + kPanel) = make_uint4(r[1][0], r[1][1], r[1][2], r[1][3]);
+              *reinterpret_cast<uint4 *>(at + 2 * kPanel) = make_uint4(r[2][0], r[2][1], r[2][2], r[2][3]);
             }
           }
         }
@@ -765,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       for (; c < nc; ++c, next(st, ph)) {
         const int ci = chunk_at(c), len = rows_of(ci) - 32 * g, ob = c & 1;
         const float *gt = gates(st);
-        const bool tma = len >= 32 && any && !(KIND == kGrad && ps.part);
+        const bool tma = len >= 32 && any && !(ps.part);
         const long row0 = u.row0 + ci * kC + 32 * g;
         if (!(ok = wait(b_gate + st, ph))) break;
         const bool apart = gt[449] != (float)kWhole;
@@ -807,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 f2up(v[i], a, b);
                 const size_t step = (size_t)p.H * ps.dz, at = ((size_t)(row0 + t) * p.H + h) * ps.dz + z;
                 if (z >= ps.dz) continue;
-                if (KIND == kGrad && ps.part) {
+                if (ps.part) {
                   if (t < len) static_cast<float *>(ps.out)[at] = a;
                   if (t + 1 < len) static_cast<float *>(ps.out)[at + step] = b;
                 } else {
@@ -817,16 +812,14 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
               }
             }
             if constexpr (KIND == kGrad) {
-              if (exact) {
-                // products with W, the two blocks of two channel groups
-                const uint32_t wt = sb + st * C::kStage + C::oW + (quad >> 1) * kPanel;
-                const int row = 32 * g + 16 * half + 8 * (lane >> 4) + (lane & 7);
-                uint32_t w[4];
-                ldmatrix4_t(wt + row * 128 + (((4 * (quad & 1) + 2 * y + (lane >> 3 & 1)) ^ (row & 7)) << 4), w);
+              // products with W, the two blocks of two channel groups
+              const uint32_t wt = sb + st * C::kStage + C::oW + (quad >> 1) * kPanel;
+              const int row = 32 * g + 16 * half + 8 * (lane >> 4) + (lane & 7);
+              uint32_t w[4];
+              ldmatrix4_t(wt + row * 128 + (((4 * (quad & 1) + 2 * y + (lane >> 3 & 1)) ^ (row & 7)) << 4), w);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (32 * quad + 16 * y < ps.dz) d[e >> 1] = f2fma(v[e], unpack_bf16(w[e]), d[e >> 1]);
-              }
+              for (int e = 0; e < 4; ++e)
+                if (32 * quad + 16 * y < ps.dz) d[e >> 1] = f2fma(v[e], unpack_bf16(w[e]), d[e >> 1]);
             }
           }
           if (half == 1) {
@@ -846,24 +839,22 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             for (int k = 0; k < 2; ++k) stmatrix4_t(at + 512 * k, pk[0][2 * k], pk[0][2 * k + 1], pk[1][2 * k], pk[1][2 * k + 1]);
           }
           if constexpr (KIND == kGrad) {
-            if (exact) {
-              // four tokens' sums over this lane's channels, then over the lanes that hold the same
-              // tokens (bits 2-4): two of them end up with one token
-              float s4[4];
-              f2up(d[0], s4[0], s4[1]);
-              f2up(d[1], s4[2], s4[3]);
+            // four tokens' sums over this lane's channels, then over the lanes that hold the same
+            // tokens (bits 2-4): two of them end up with one token
+            float s4[4];
+            f2up(d[0], s4[0], s4[1]);
+            f2up(d[1], s4[2], s4[3]);
 #pragma unroll
-              for (int step = 2; step >= 1; step >>= 1) {
-                const bool up = lane & (8 * step);
+            for (int step = 2; step >= 1; step >>= 1) {
+              const bool up = lane & (8 * step);
 #pragma unroll
-                for (int i = 0; i < step; ++i) {
-                  const float send = up ? s4[i] : s4[i + step], keep = up ? s4[i + step] : s4[i];
-                  s4[i] = keep + __shfl_xor_sync(0xffffffffu, send, 8 * step);
-                }
+              for (int i = 0; i < step; ++i) {
+                const float send = up ? s4[i] : s4[i + step], keep = up ? s4[i + step] : s4[i];
+                s4[i] = keep + __shfl_xor_sync(0xffffffffu, send, 8 * step);
               }
-              s4[0] += __shfl_xor_sync(0xffffffffu, s4[0], 4);
-              if (!(lane & 4)) rd[t0 + 8 * (lane >> 4) + (lane >> 3 & 1)] = s4[0];
             }
+            s4[0] += __shfl_xor_sync(0xffffffffu, s4[0], 4);
+            if (!(lane & 4)) rd[t0 + 8 * (lane >> 4) + (lane >> 3 & 1)] = s4[0];
           }
         }
         if (tma) {
@@ -875,15 +866,13 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
           }
         }
         if constexpr (KIND == kGrad) {
-          if (exact) {
-            __syncwarp();
-            // (two barriers: a warp may be a chunk ahead of another that waits for its store)
-            if (lane == 0) mbar_arrive(b_red + ob);
-            if (quad == 0) {
-              if (!(ok = wait(b_red + ob, c >> 1))) break;
-              if (lane < len)
-                ps.dots[(size_t)h * p.rows + row0 + lane] = (rd[lane] + rd[64 + lane]) + (rd[128 + lane] + rd[192 + lane]);
-            }
+          __syncwarp();
+          // (two barriers: a warp may be a chunk ahead of another that waits for its store)
+          if (lane == 0) mbar_arrive(b_red + ob);
+          if (quad == 0) {
+            if (!(ok = wait(b_red + ob, c >> 1))) break;
+            if (lane < len)
+              ps.dots[(size_t)h * p.rows + row0 + lane] = (rd[lane] + rd[64 + lane]) + (rd[128 + lane] + rd[192 + lane]);
           }
         }
         __syncwarp();
@@ -905,6 +894,12 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     tc_fence_after();
     tmem_dealloc(*s_tmem, 512);
   }
+}
+template <int KIND>
+__global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_constant__ Params p) {
+  // (kGrad is dq and dk; dv, which has no row dots, is what kOut computes: 3.9 -> 2.2 us a chunk)
+  if (KIND == kGrad && blockIdx.z == 2) lin_tc<kOut>(p);
+  else lin_tc<KIND>(p);
 }
 
 // ------------------------------------------------------------------ walk over the segments
@@ -1040,9 +1035,9 @@ TcLayout tc_layout(bool packed, int N, int B, int T, int H, int Hq, int Hk, int 
 template <int KIND>
 bool launch(const Params &p, dim3 grid, cudaStream_t s) {
   auto kern = lin_tc_kernel<KIND>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<KIND>::kSmem) != cudaSuccess)
-    return false;
-  kern<<<grid, kThreads, Cfg<KIND>::kSmem, s>>>(p);
+  const uint32_t smem = KIND == kGrad ? std::max(Cfg<kGrad>::kSmem, Cfg<kOut>::kSmem) : Cfg<KIND>::kSmem;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
+  kern<<<grid, kThreads, smem, s>>>(p);
   return cudaGetLastError() == cudaSuccess;
 }
 
@@ -1100,7 +1095,7 @@ int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
   if (!b) {
     if (!a.o && !a.S_T) return cudaGetLastError() == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
     Pass &f = p.pass[0];
-    f.ix = 0; f.iy = 1; f.iz = 2; f.iw = -1;
+    f.ix = 0; f.iy = 1; f.iz = 2;
     f.hx = a.Hq; f.hy = a.Hk; f.hz = a.Hv; f.dx = a.dk; f.dz = a.dv; f.sz = 1; f.sx = a.dv;
     f.init = a.S0; f.seg_in = l.seg ? segS : nullptr; f.end = a.S_T; f.out = a.o;
     if (a.o && !make_map(&p.outs[0], a.o, a.H, rows, a.dv, true)) return CKDA_ERR_CUDA;
@@ -1123,7 +1118,7 @@ int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
   pk.dots = kappa;
   Pass &pv = p.pass[2];
   pv = pk;
-  pv.ix = 1; pv.iy = 0; pv.iz = 3; pv.iw = -1;
+  pv.ix = 1; pv.iy = 0; pv.iz = 3;
   pv.hx = a.Hk; pv.hy = a.Hq; pv.hz = a.H; pv.dx = a.dk; pv.dz = a.dv; pv.sz = 1; pv.sx = a.dv;
   pv.end = b->dS0;
   pv.part = part_v; pv.out = part_v ? a.ws + l.pv : static_cast<uint8_t *>(b->dv);
