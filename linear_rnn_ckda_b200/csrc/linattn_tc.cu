@@ -315,7 +315,97 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
   uint32_t ph = 0;
   bool ok = true;
 
-  if (warp < 4) {
+  if (KIND == kGrad && warp < 4) {
+    // ---------------------------------------------------------------- state (warps 0-3)
+    // M is its operand: three bf16 terms hold an fp32 value's 24 bits, and O1 wants them anyway.
+    // So M lives in tensor memory only, and a chunk's M <- e^{G_C} M + D is one short loop: held in
+    // registers as in the other kinds, the unrolled splitting alone was 11 KB of code a chunk, for
+    // which the warps waited more than they computed (put 5,300 cycles of 8,000 a chunk).
+    const int z = tid;                              // this thread's value channel (TMEM lane)
+    const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16) + C::cM;
+    auto put = [&](int b, uint64_t (&m)[8]) {       // x channels 16 b ..
+      uint32_t r[3][8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        r[0][i] = pack_bf16(m[i]);
+        uint64_t x = f2sub(m[i], unpack_bf16(r[0][i]));
+        r[1][i] = pack_bf16(x);
+        x = f2sub(x, unpack_bf16(r[1][i]));
+        r[2][i] = pack_bf16(x);
+      }
+#pragma unroll
+      for (int t = 0; t < 3; ++t) tmem_st8(lanes + 64 * t + 8 * b, r[t]);
+    };
+    auto get = [&](int b, uint64_t (&m)[8]) {
+      uint32_t r[3][8];
+#pragma unroll
+      for (int t = 0; t < 3; ++t) tmem_ld8(lanes + 64 * t + 8 * b, r[t]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[i] = f2add(f2add(unpack_bf16(r[0][i]), unpack_bf16(r[1][i])), unpack_bf16(r[2][i]));
+    };
+    auto ready = [&]() {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_s);
+    };
+    {
+      const bool live = z < ps.dz;
+      const float *src = ps.seg_in + ((size_t)blockIdx.x * p.H + h) * p.elems + (size_t)z * ps.sz;
+#pragma unroll 1
+      for (int b = 0; 16 * b < ps.dx; ++b) {
+        uint64_t m[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int x = 16 * b + 2 * i;
+          m[i] = f2pk(live ? src[(size_t)x * ps.sx] : 0.f, live ? src[(size_t)(x + 1) * ps.sx] : 0.f);
+        }
+        put(b, m);
+      }
+      ready();
+    }
+    for (; c < nc; ++c, next(st, ph)) {
+      if (!(ok = wait(b_gate + st, ph))) break;
+      const float a = gates(st)[448];
+      const uint64_t a2 = f2pk(a, a);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_empty + st);
+      // (D is there, and O1 of this chunk has read the operand)
+      if (!(ok = wait(b_o1, c) && wait(b_d, c))) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int b = 0; 16 * b < ps.dx; ++b) {
+        uint32_t r[16];
+        uint64_t m[8];
+        tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + C::cD + 16 * b, r);
+        get(b, m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = f2fma(a2, m[i], f2bits(r[2 * i], r[2 * i + 1]));
+        put(b, m);
+      }
+      ready();
+      if (lane == 0) mbar_arrive(b_dfree);
+    }
+    if (ok && last_seg) {
+#pragma unroll 1
+      for (int b = 0; 16 * b < ps.dx; ++b) {
+        uint64_t m[8];
+        get(b, m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float f[2];
+          f2up(m[i], f[0], f[1]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const size_t at = (size_t)z * ps.sz + (size_t)(16 * b + 2 * i + e) * ps.sx;
+            if (z < ps.dz && ps.end) ps.end[((size_t)u.n * p.H + h) * p.elems + at] = f[e];
+            if (z < ps.dz && ps.end_slot) ps.end_slot[((size_t)(blockIdx.x + 1) * p.H + h) * p.elems + at] = f[e];
+          }
+        }
+      }
+    }
+  } else if (KIND != kGrad && warp < 4) {
     // ---------------------------------------------------------------- state (warps 0-3)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsState));
     const int z = tid;                              // this thread's value channel (TMEM lane)
@@ -351,22 +441,10 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
         if (16 * b >= ps.dx) break;
-        uint32_t r[C::kTerms][8];
+        uint32_t r[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          r[0][i] = pack_bf16(M[8 * b + i]);
-          if constexpr (KIND == kGrad) {
-            uint64_t x = f2sub(M[8 * b + i], unpack_bf16(r[0][i]));
-            r[1][i] = pack_bf16(x);
-            x = f2sub(x, unpack_bf16(r[1][i]));
-            r[2][i] = pack_bf16(x);
-          }
-        }
-        tmem_st8(lanes + C::cM + 8 * b, r[0]);
-        if constexpr (KIND == kGrad) {
-          tmem_st8(lanes + C::cM + 64 + 8 * b, r[1]);
-          tmem_st8(lanes + C::cM + 128 + 8 * b, r[2]);
-        }
+        for (int i = 0; i < 8; ++i) r[i] = pack_bf16(M[8 * b + i]);
+        tmem_st8(lanes + C::cM + 8 * b, r);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -432,7 +510,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (KIND != kGrad) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 14 || (KIND == kStates && warp == 22)) {
       // -------------------------------------------------------------- loads (14) and decays
       // (kStates, whose chunks are short: 14 and 22 take turns at the chunks' decays, which take a
