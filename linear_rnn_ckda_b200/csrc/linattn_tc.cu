@@ -80,6 +80,17 @@ __device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, uint32_t (&r)[8])
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
+// 16 lanes x 16 columns of words: registers 2 k, 2 k + 1 are lane t / 4 and t / 4 + 8, column 4 k + t % 4
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 // four 8 x 8 blocks of 16-bit values, transposed: lane t's register i is column t / 4, rows 2 (t % 4)
 // and the next, of block i; lane 8 i + r gives the address of block i's row r
 __device__ __forceinline__ void stmatrix4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -174,7 +185,6 @@ struct Pass {
   int hx, hy, hz, hw;             // their heads
   int dx, dz;                     // channels of X and Y, of Z
   int rev;
-  int sz, sx;                     // strides of z and x channels in a stored state [dk][dv]
   const float *init;              // [N, H, dk, dv] or NULL (used without seg_in)
   const float *seg_in;            // [slots, H, dk, dv] incoming states, or NULL
   float *end;                     // [N, H, dk, dv]: the last segment's end state, or NULL
@@ -321,10 +331,8 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
     // So M lives in tensor memory only, and a chunk's M <- e^{G_C} M + D is one short loop: held in
     // registers as in the other kinds, the unrolled splitting alone was 11 KB of code a chunk, for
     // which the warps waited more than they computed (put 5,300 cycles of 8,000 a chunk).
-    const int z = tid;                              // this thread's value channel (TMEM lane)
-    const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16) + C::cM;
-    auto put = [&](int b, uint64_t (&m)[8]) {       // x channels 16 b ..
-      uint32_t r[3][8];
+    const uint32_t quarter = tmem + ((uint32_t)(32 * warp) << 16), lanes = quarter + C::cM;
+    auto split = [&](const uint64_t (&m)[8], uint32_t (&r)[3][8]) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         r[0][i] = pack_bf16(m[i]);
@@ -333,38 +341,42 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
         x = f2sub(x, unpack_bf16(r[1][i]));
         r[2][i] = pack_bf16(x);
       }
-#pragma unroll
-      for (int t = 0; t < 3; ++t) tmem_st8(lanes + 64 * t + 8 * b, r[t]);
     };
-    auto get = [&](int b, uint64_t (&m)[8]) {
-      uint32_t r[3][8];
-#pragma unroll
-      for (int t = 0; t < 3; ++t) tmem_ld8(lanes + 64 * t + 8 * b, r[t]);
-      tmem_wait_ld();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m[i] = f2add(f2add(unpack_bf16(r[0][i]), unpack_bf16(r[1][i])), unpack_bf16(r[2][i]));
+    auto whole = [&](const uint32_t (&r)[3][8], int i) {
+      return f2add(f2add(unpack_bf16(r[0][i]), unpack_bf16(r[1][i])), unpack_bf16(r[2][i]));
     };
+    // Stored states are rows of x channels: a warp reads and writes 8 of them (32-byte pieces) at a
+    // time, in the layout that puts a row into a lane (a lane's own row, 4 bytes or 16 at a time,
+    // took 20,000 cycles in and 34,000 out).
+    const size_t state = ((size_t)blockIdx.x * p.H + h) * p.elems;
+    const int z0 = 32 * warp + (lane >> 2), x0 = 2 * (lane & 3);
+    auto at = [&](int b, int y, int i) {             // where word i of 16 lanes and channels 32 b .. is stored
+      return (size_t)(z0 + 16 * y + 8 * (i & 1)) * ps.dx + 32 * b + 8 * (i >> 1) + x0;
+    };
+    auto have = [&](int b, int y, int i) { return z0 + 16 * y + 8 * (i & 1) < ps.dz && 32 * b + 8 * (i >> 1) < ps.dx; };
     auto ready = [&]() {
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_s);
     };
-    {
-      const bool live = z < ps.dz;
-      const float *src = ps.seg_in + ((size_t)blockIdx.x * p.H + h) * p.elems + (size_t)z * ps.sz;
 #pragma unroll 1
-      for (int b = 0; 16 * b < ps.dx; ++b) {
-        uint64_t m[8];
+    for (int b = 0; 32 * b < ps.dx; ++b) {
+      uint64_t m[2][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int x = 16 * b + 2 * i;
-          m[i] = f2pk(live ? src[(size_t)x * ps.sx] : 0.f, live ? src[(size_t)(x + 1) * ps.sx] : 0.f);
-        }
-        put(b, m);
+      for (int i = 0; i < 16; ++i) {
+        const int y = i >> 3, w = i & 7;
+        m[y][w] = have(b, y, w) ? *reinterpret_cast<const uint64_t *>(ps.seg_in + state + at(b, y, w)) : 0;
       }
-      ready();
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint32_t r[3][8];
+        split(m[y], r);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) tmem_st_rows(lanes + ((16u * y) << 16) + 64 * t + 16 * b, r[t]);
+      }
     }
+    ready();
     for (; c < nc; ++c, next(st, ph)) {
       if (!(ok = wait(b_gate + st, ph))) break;
       const float a = gates(st)[448];
@@ -376,32 +388,34 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
       tc_fence_after();
 #pragma unroll 1
       for (int b = 0; 16 * b < ps.dx; ++b) {
-        uint32_t r[16];
+        uint32_t d[16], r[3][8];
         uint64_t m[8];
-        tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + C::cD + 16 * b, r);
-        get(b, m);
+        tmem_ld16(quarter + C::cD + 16 * b, d);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m[i] = f2fma(a2, m[i], f2bits(r[2 * i], r[2 * i + 1]));
-        put(b, m);
+        for (int t = 0; t < 3; ++t) tmem_ld8(lanes + 64 * t + 8 * b, r[t]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = f2fma(a2, whole(r, i), f2bits(d[2 * i], d[2 * i + 1]));
+        split(m, r);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) tmem_st8(lanes + 64 * t + 8 * b, r[t]);
       }
       ready();
       if (lane == 0) mbar_arrive(b_dfree);
     }
-    if (ok && last_seg) {
+    if (ok && last_seg && ps.end_slot) {
+      float *dst = ps.end_slot + state + (size_t)p.H * p.elems;      // the next slot
 #pragma unroll 1
-      for (int b = 0; 16 * b < ps.dx; ++b) {
-        uint64_t m[8];
-        get(b, m);
+      for (int b = 0; 32 * b < ps.dx; ++b) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float f[2];
-          f2up(m[i], f[0], f[1]);
+        for (int y = 0; y < 2; ++y) {
+          uint32_t r[3][8];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const size_t at = (size_t)z * ps.sz + (size_t)(16 * b + 2 * i + e) * ps.sx;
-            if (z < ps.dz && ps.end) ps.end[((size_t)u.n * p.H + h) * p.elems + at] = f[e];
-            if (z < ps.dz && ps.end_slot) ps.end_slot[((size_t)(blockIdx.x + 1) * p.H + h) * p.elems + at] = f[e];
-          }
+          for (int t = 0; t < 3; ++t) tmem_ld_rows(lanes + ((16u * y) << 16) + 64 * t + 16 * b, r[t]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (have(b, y, i)) *reinterpret_cast<uint64_t *>(dst + at(b, y, i)) = whole(r, i);
         }
       }
     }
@@ -418,22 +432,10 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
         if (ps.seg_in) src = ps.seg_in + ((size_t)blockIdx.x * p.H + h) * p.elems;
         else if (ps.init) src = ps.init + ((size_t)u.n * p.H + h) * p.elems;
       }
-      const bool have = src && live;
-      if (src) src += (size_t)z * ps.sz;
-      if (ps.sx == 1) {
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (have && 2 * i < ps.dx) f = *reinterpret_cast<const float4 *>(src + 2 * i);
-          M[i] = f2pk(f.x, f.y);
-          M[i + 1] = f2pk(f.z, f.w);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          const bool in = have && 2 * i < ps.dx;
-          M[i] = f2pk(in ? src[(size_t)(2 * i) * ps.sx] : 0.f, in ? src[(size_t)(2 * i + 1) * ps.sx] : 0.f);
-        }
+      for (int i = 0; i < 64; ++i) {
+        const bool in = src && live && 2 * i < ps.dx;
+        M[i] = f2pk(in ? src[(2 * i) * ps.dz + z] : 0.f, in ? src[(2 * i + 1) * ps.dz + z] : 0.f);
       }
     }
     // M as the next chunk's operand
@@ -486,21 +488,13 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
       ps.decay[(size_t)blockIdx.x * p.H + h] = exp2_fixed(whole);
     if (ok && live) {
       auto store = [&](float *dst) {
-        dst += (size_t)z * ps.sz;
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          float4 f;
-          f2up(M[i], f.x, f.y);
-          f2up(M[i + 1], f.z, f.w);
+        for (int i = 0; i < 64; ++i) {
+          float a, b;
+          f2up(M[i], a, b);
           if (2 * i >= ps.dx) break;
-          if (ps.sx == 1) {
-            *reinterpret_cast<float4 *>(dst + 2 * i) = f;
-          } else {
-            dst[(size_t)(2 * i) * ps.sx] = f.x;
-            dst[(size_t)(2 * i + 1) * ps.sx] = f.y;
-            dst[(size_t)(2 * i + 2) * ps.sx] = f.z;
-            dst[(size_t)(2 * i + 3) * ps.sx] = f.w;
-          }
+          dst[(2 * i) * ps.dz + z] = a;
+          dst[(2 * i + 1) * ps.dz + z] = b;
         }
       };
       if (KIND == kStates) store(ps.end_slot + ((size_t)blockIdx.x * p.H + h) * p.elems);
@@ -1153,7 +1147,7 @@ int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
   if (l.seg && slots > 0) {
     Params w = p;
     Pass &f = w.pass[0];
-    f.iy = 1; f.iz = 2; f.hy = a.Hk; f.hz = a.Hv; f.dx = a.dk; f.dz = a.dv; f.sz = 1; f.sx = a.dv;
+    f.iy = 1; f.iz = 2; f.hy = a.Hk; f.hz = a.Hv; f.dx = a.dk; f.dz = a.dv;
     f.end_slot = segS; f.decay = decay;
     Pass &r = w.pass[1];
     r = f;
@@ -1174,7 +1168,7 @@ int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
     if (!a.o && !a.S_T) return cudaGetLastError() == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
     Pass &f = p.pass[0];
     f.ix = 0; f.iy = 1; f.iz = 2;
-    f.hx = a.Hq; f.hy = a.Hk; f.hz = a.Hv; f.dx = a.dk; f.dz = a.dv; f.sz = 1; f.sx = a.dv;
+    f.hx = a.Hq; f.hy = a.Hk; f.hz = a.Hv; f.dx = a.dk; f.dz = a.dv;
     f.init = a.S0; f.seg_in = l.seg ? segS : nullptr; f.end = a.S_T; f.out = a.o;
     if (a.o && !make_map(&p.outs[0], a.o, a.H, rows, a.dv, true)) return CKDA_ERR_CUDA;
     return launch<kOut>(p, dim3(slots, H, 1), s) ? CKDA_OK : CKDA_ERR_CUDA;
@@ -1184,7 +1178,7 @@ int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
   Pass &pq = p.pass[0];
   pq.ix = 3; pq.iy = 2; pq.iz = 1; pq.iw = 0;
   pq.hx = a.H; pq.hy = a.Hv; pq.hz = a.Hk; pq.hw = a.Hq; pq.dx = a.dv; pq.dz = a.dk;
-  pq.sz = a.dv; pq.sx = 1; pq.seg_in = segS; pq.end_slot = segS;
+  pq.seg_in = segS; pq.end_slot = segS;
   pq.part = part_q; pq.out = part_q ? a.ws + l.pq : static_cast<uint8_t *>(b->dq);
   pq.dots = rho;
   Pass &pk = p.pass[1];
@@ -1197,7 +1191,7 @@ int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
   Pass &pv = p.pass[2];
   pv = pk;
   pv.ix = 1; pv.iy = 0; pv.iz = 3;
-  pv.hx = a.Hk; pv.hy = a.Hq; pv.hz = a.H; pv.dx = a.dk; pv.dz = a.dv; pv.sz = 1; pv.sx = a.dv;
+  pv.hx = a.Hk; pv.hy = a.Hq; pv.hz = a.H; pv.dx = a.dk; pv.dz = a.dv;
   pv.end = b->dS0;
   pv.part = part_v; pv.out = part_v ? a.ws + l.pv : static_cast<uint8_t *>(b->dv);
   pv.dots = nullptr;
