@@ -170,7 +170,7 @@ struct Cfg {
   static constexpr uint32_t kGate = 7 * 64 * 4 + 16;                          // one stage's decays
   static constexpr uint32_t offDot = offGate + kStages * kGate;               // kGrad: 2 x 4 x 64 floats
   static constexpr uint32_t offBar = offDot + (KIND == kGrad ? 512 * 4 : 0);
-  static constexpr int kBars = 3 * kStages + 2 * kTokBufs + 21;
+  static constexpr int kBars = 3 * kStages + 2 * kTokBufs + (KIND == kGrad ? 25 : 21);
   static constexpr uint32_t kSmem = offBar + kBars * 8 + 64 + 1024;           // + slack to align
   // TMEM columns: scores, M, O twice, D (twice where there is room)
   static constexpr int kDBufs = KIND == kGrad ? 1 : 2;
@@ -249,7 +249,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
   uint64_t *b_full = bars, *b_empty = bars + C::kStages, *b_gate = bars + 2 * C::kStages;
   uint64_t *b_w = bars + 3 * C::kStages, *b_wfree = b_w + C::kTokBufs;
   uint64_t *bx = b_wfree + C::kTokBufs;
-  uint64_t *b_zeroed = bx, *b_sc = bx + 1, *b_p = bx + 2, *b_s = bx + 3, *b_o = bx + 4 /* 2 */,
+  uint64_t *b_zeroed = bx, *b_sc = bx + 1, *b_p = bx + 2, *b_s = bx + (KIND == kGrad ? 21 : 3) /* 4 in kGrad */, *b_o = bx + 4 /* 2 */,
            *b_ofree = bx + 6 /* 2 */, *b_d = bx + 8 /* 2 */, *b_dfree = bx + 16 /* 2 */, *b_drain = bx + 10 /* 2 */,
            *b_red = bx + 12 /* 2 */, *b_o1 = bx + 14;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bx + 18);
@@ -270,7 +270,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
     mbar_init(b_zeroed, tok_warps);
     mbar_init(b_sc, 1);
     mbar_init(b_p, 3);
-    mbar_init(b_s, 4);
+    for (int s = 0; s < (KIND == kGrad ? 4 : 1); ++s) mbar_init(b_s + s, 4);
     mbar_init(b_o1, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(b_o + s, 1);
@@ -354,11 +354,11 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
       return (size_t)(z0 + 16 * y + 8 * (i & 1)) * ps.dx + 32 * b + 8 * (i >> 1) + x0;
     };
     auto have = [&](int b, int y, int i) { return z0 + 16 * y + 8 * (i & 1) < ps.dz && 32 * b + 8 * (i >> 1) < ps.dx; };
-    auto ready = [&]() {
+    auto ready = [&](int b) {                        // 32 x channels of the operand (O1 need not wait for all)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(b_s);
+      if (lane == 0) mbar_arrive(b_s + b);
     };
 #pragma unroll 1
     for (int b = 0; 32 * b < ps.dx; ++b) {
@@ -375,8 +375,8 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
 #pragma unroll
         for (int t = 0; t < 3; ++t) tmem_st_rows(lanes + ((16u * y) << 16) + 64 * t + 16 * b, r[t]);
       }
+      ready(b);
     }
-    ready();
     for (; c < nc; ++c, next(st, ph)) {
       if (!(ok = wait(b_gate + st, ph))) break;
       const float a = gates(st)[448];
@@ -399,8 +399,8 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
         split(m, r);
 #pragma unroll
         for (int t = 0; t < 3; ++t) tmem_st8(lanes + 64 * t + 8 * b, r[t]);
+        if ((b & 1) || ps.dx == 16) ready(b >> 1);
       }
-      ready();
       if (lane == 0) mbar_arrive(b_dfree);
     }
     if (ok && last_seg && ps.end_slot) {
@@ -605,15 +605,27 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
         for (; ok && c < nc; ++c, next(st, ph)) {
           // (the outputs that were in this buffer have been read; X is there, for the scores read it)
           const int ob = c & 1;
-          if (!(ok = need(b_s, c) && (c < 2 || need(b_ofree + ob, (c >> 1) - 1)))) break;
+          if (!(ok = (KIND == kGrad || need(b_s, c)) && (c < 2 || need(b_ofree + ob, (c >> 1) - 1)))) break;
           if (!(ok = need(b_full + st, ph) && need(b_gate + st, ph) && (!both || need(b_ofree + (ob ^ 1), (c - 1) >> 1)))) break;
           tc_fence_after();
           const uint64_t x = kmajor(st * C::kStage + C::oX);
           const uint32_t d = tmem + C::cO + 64 * ob;
-          out1(d, tmem + C::cM, x, false);
-          if (KIND == kGrad) {
-            out1(d, tmem + C::cM + 64, x, true);
-            out1(d, tmem + C::cM + 128, x, true);
+          if constexpr (KIND == kGrad) {
+            // 32 channels of M at a time, as they are updated
+#pragma unroll 1
+            for (int b = 0; 32 * b < ps.dx; ++b) {
+              if (!(ok = need(b_s + b, c))) break;
+              tc_fence_after();
+              const uint64_t xb = x + (b >> 1) * (kPanel >> 4) + 4 * (b & 1);
+#pragma unroll
+              for (int t = 0; t < 3; ++t) {
+                mma_bf16_ts(d, tmem + C::cM + 64 * t + 16 * b, xb, id1, b > 0 || t > 0);
+                if (ps.dx > 16) mma_bf16_ts(d, tmem + C::cM + 64 * t + 16 * b + 8, xb + 2, id1, true);
+              }
+            }
+            if (!ok) break;
+          } else {
+            out1(d, tmem + C::cM, x, false);
           }
           mma_commit(b_o1);
           // the second part on top, or (weights not over the whole chunk) in the other buffer
