@@ -1061,24 +1061,32 @@ bool make_map(CUtensorMap *map, const void *base, int heads, long rows, int d, b
 
 constexpr int kSMs = 148;
 
-// Tokens per segment.  Unpacked: the cut into m segments that the model below finds shortest, in
-// chunk times: main launch = waves x (segment + 3 chunks' worth of start), first launch half a
-// chunk time per chunk, 8 for the extra launches.  Packed: lengths are on the device, so a
-// segment is a quarter of an SM's share of all chunks, between 8 and 64 chunks.
-int segment_tokens(bool packed, int N, int B, int T, int H, int passes) {
+// Tokens per segment.  Unpacked: the cut into m segments that a model in chunk times finds
+// shortest.  Forwards: main launch = waves x (segment + 3 chunks' worth of start), first launch
+// half a chunk time per chunk, 8 for the extra launches (B1 T4096 H32: 16 chunks 94 us, 64 150;
+// B4 T4096 H16: 32 or 64 chunks 155, 22 185).  Backwards, where two units on the SMs of a pair run
+// at two thirds of one's speed: all units' chunks over all SMs, 1.2 times a unit's own for the last
+// ones, 0.6 a chunk for the first launch (B1 T4096 H32: 16 chunks 311 us, 64 463; B2 T2048 H16:
+// 8 chunks 190, 32 253).  Packed: lengths are on the device, so a segment is half an SM's share of
+// all chunks (backwards a quarter), between 8 and 64 chunks, a multiple of 4 so that even lengths
+// are cut evenly (13 sequences, 40,000 tokens, H16 forward: 32 chunks 416 us, 16 433, 34 436, 64
+// 445; 10 sequences, 9,000 tokens, H16 backward: 12 chunks 390 us, 24 422).
+int segment_tokens(bool packed, int B, int T, int H, bool back) {
   const long nch = ((long)T + kC - 1) / kC;
+  const long units1 = (long)B * H * (back ? 3 : 1), local1 = (long)B * H * (back ? 2 : 1);
   if (nch <= 1) return kC;
-  if (packed) {
-    long c = nch * H * passes / kSMs / 4;
-    c = c < 8 ? 8 : c > 64 ? 64 : c;
-    return (int)c * kC;
-  }
+  if (packed) return (int)(std::min(std::max(nch * units1 / kSMs / (back ? 4 : 2), 8L), 64L) & ~3L) * kC;
   long best = -1, best_c = nch;
   for (long m = 1; m <= nch && m <= 64; ++m) {
     const long c = (nch + m - 1) / m, mm = (nch + c - 1) / c;
-    const long units = (long)B * H * passes * mm;
-    long cost = 2 * ((units + kSMs - 1) / kSMs) * (c + 3);
-    if (mm > 1) cost += (((long)B * H * (passes > 1 ? 2 : 1) * (mm - 1) + kSMs - 1) / kSMs) * (c + 3) + 16;
+    long cost;
+    if (back) {
+      cost = units1 * mm * (c + 3) * 10 / kSMs + 12 * (c + 3);
+      if (mm > 1) cost += local1 * (mm - 1) * (c + 3) * 6 / kSMs + 30;
+    } else {
+      cost = 2 * ((units1 * mm + kSMs - 1) / kSMs) * (c + 3);
+      if (mm > 1) cost += ((local1 * (mm - 1) + kSMs - 1) / kSMs) * (c + 3) + 16;
+    }
     if (best < 0 || cost < best) { best = cost; best_c = c; }
   }
   return (int)best_c * kC;
@@ -1096,7 +1104,7 @@ struct TcLayout {
 TcLayout tc_layout(bool packed, int N, int B, int T, int H, int Hq, int Hk, int Hv, int dk, int dv,
                    bool g_fixed, bool back) {
   TcLayout l = {};
-  l.L = segment_tokens(packed, N, B, T, H, back ? 3 : 1);
+  l.L = segment_tokens(packed, B, T, H, back);
   l.seg = packed || T > l.L;
   l.slots = slot_count(packed, N, T, l.L, back ? 1 : 0);
   const size_t rows = (size_t)B * T, state = (size_t)l.slots * H * dk * dv * 4;
