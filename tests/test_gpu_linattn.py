@@ -164,6 +164,40 @@ def test_extreme_decays(cuda_lib, dtype):
     check_bwd(cuda_lib, t, dO, dS)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("gap", [0, 40])
+def test_chunks_that_decay_fast_but_not_at_once(cuda_lib, gap, dtype):
+    """64 tokens lose 2^-138, 32 of them 2^-69: a chunk's weights leave fp32's range, a half's do
+    not.  (`gap` tokens without decay first, so that such chunks stand beside ordinary ones.)"""
+    t, (dO, dS) = make(2, 150 + gap, 2, 1, 2, 2, 64, 128, dtype, seed=gap)
+    t["g"] = torch.full_like(t["g"], -1.5)
+    t["g"][:, :gap] = 0.0
+    check_fwd(cuda_lib, t)
+    check_bwd(cuda_lib, t, dO, dS)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_two_calls_at_once(cuda_lib, dtype):
+    """Forward and backward calls in flight on two streams give the bits that they give alone."""
+    sets, alone = [], []
+    for seed in (1, 2):
+        t, (dO, dS) = make(1, 700, 8, 8, 4, 8, 128, 128, dtype, seed=seed)
+        sets.append((cuda(t), dO.cuda(), dS.cuda()))
+    run = lambda x: (*cuda_lib.linattn_fwd(**x[0]), *cuda_lib.linattn_bwd(**x[0], dO=x[1], dS_T=x[2]))  # noqa: E731
+    for x in sets:
+        alone.append(run(x))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        got = []
+        for s, x in zip(streams, sets):
+            with torch.cuda.stream(s):
+                got.append(run(x))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_large_sums_of_decays(cuda_lib):
     """A chunk that starts with a thousandfold underflow and then decays slowly: the weights among
     the later tokens keep fp32 accuracy although their summed decays are large."""
