@@ -188,9 +188,6 @@ struct DecodeArgs {
   int B, H, dk, dv, signed_gate, io_dtype, o_dtype;
 };
 
-// CKDA_OK when the current device is sm_100, else the CKDA_ERR_* code a call returns.
-int check_device();
-
 // Argument checks of ckda_chunk_fwd that need no device (everything but the workspace):
 // CKDA_OK or the CKDA_ERR_* code the call returns.
 int check_chunk_args(const void *q, const void *k, const void *v, const void *a, const float *b,

@@ -15,6 +15,8 @@
 #include <stdint.h>
 
 namespace ckda {
+// CKDA_OK when the current device is sm_100, else the CKDA_ERR_* code a call returns.
+int check_device();
 
 struct LinArgs {
   const void *q, *k, *v;      // [rows, Hq, dk], [rows, Hk, dk], [rows, Hv, dv]
