@@ -177,6 +177,24 @@ def test_chunks_that_decay_fast_but_not_at_once(cuda_lib, gap, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("lens", [[40], [700], [3, 0, 640, 64]])
+def test_states_in_place(cuda_lib, lens, dtype):
+    """S_T over S0 and dS0 over dS_T give the bits that separate buffers give."""
+    T, N = sum(lens), len(lens)
+    t, (dO, dS) = make(1, T, 4, 2, 4, 4, 64, 128, dtype, N=N, seed=T)
+    d, cu = cuda(t), offsets(lens).cuda()
+    dO, dS = dO.cuda(), dS.cuda()
+    o, S_T = cuda_lib.linattn_fwd(**d, cu_seqlens=cu)
+    grads = cuda_lib.linattn_bwd(**d, cu_seqlens=cu, dO=dO, dS_T=dS)
+    over = d["S0"].clone()
+    o2, S2 = cuda_lib.linattn_fwd(**{**d, "S0": over}, cu_seqlens=cu, S_T=over)
+    assert S2 is over and torch.equal(S2, S_T) and torch.equal(o2, o)
+    room = [torch.empty_like(d[n]) for n in ("q", "k", "v", "g")] + [dS.clone()]
+    again = cuda_lib.linattn_bwd(**d, cu_seqlens=cu, dO=dO, dS_T=room[4], grads=room)
+    assert all(torch.equal(x, y) for x, y in zip(again, grads))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
 def test_two_calls_at_once(cuda_lib, dtype):
     """Forward and backward calls in flight on two streams give the bits that they give alone."""
     sets, alone = [], []
