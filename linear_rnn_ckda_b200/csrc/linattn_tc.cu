@@ -26,6 +26,11 @@
 // term in the mean, the size of the output's own rounding); tokf Z is split into three terms
 // (24 bits), so M itself carries fp32 accuracy over any length.  Where row dots are wanted
 // (decay gradients, which cancel) M and P go into O in three terms too (two leave dg 2.7e-5 off).
+// The tensor cores truncate the accumulator at every addition (dq came out 4.4e-7 too small), so
+// terms are added from the lowest up, and the many additions of lower terms truncate a small sum
+// only: dg 1.8e-6 -> 1.0e-6 off, final states 2.3e-7 -> 1.1e-7 (B4 T4096 H16), for 4 % of the
+// gradients' time.  (D's lower terms of both halves of a chunk first, as the gradients take them, cost
+// the forward 10 %: there each half is added by itself.)
 //
 // One CTA per (segment, head), 24 warps: 0-3 state (200 registers a thread where they hold M), 4-11
 // outputs, 12, 13 and one of 16, 17 scores (a 32 x 32 block each), 14 TMA loads and decays, 15
@@ -620,19 +625,20 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
           const uint64_t x = kmajor(st * C::kStage + C::oX);
           const uint32_t d = tmem + C::cO + 64 * ob;
           if constexpr (KIND == kGrad) {
-            // 32 channels of M at a time, as they are updated
+            // the lower terms of 32 channels of M at a time, as they are updated, then all first terms
 #pragma unroll 1
             for (int b = 0; 32 * b < ps.dx; ++b) {
               if (!(ok = need(b_s + b, c))) break;
               tc_fence_after();
               const uint64_t xb = x + (b >> 1) * (kPanel >> 4) + 4 * (b & 1);
 #pragma unroll
-              for (int t = 0; t < 3; ++t) {
-                mma_bf16_ts(d, tmem + C::cM + 64 * t + 16 * b, xb, id1, b > 0 || t > 0);
+              for (int t = 2; t >= 1; --t) {
+                mma_bf16_ts(d, tmem + C::cM + 64 * t + 16 * b, xb, id1, b > 0 || t < 2);
                 if (ps.dx > 16) mma_bf16_ts(d, tmem + C::cM + 64 * t + 16 * b + 8, xb + 2, id1, true);
               }
             }
             if (!ok) break;
+            out1(d, tmem + C::cM, x, true);
           } else {
             out1(d, tmem + C::cM, x, false);
           }
@@ -644,14 +650,10 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
           const uint64_t dz = mnmajor(st * C::kStage + C::oZ, kPanel), dp = kmajor(C::offP);
           const uint32_t d2 = apart ? tmem + C::cO + 64 * (ob ^ 1) : d;
           both = apart;
-          mma_bf16_ss(d2, dz, dp, id2, !apart);
+          // (P's terms, the last first)
 #pragma unroll
-          for (int k = 1; k < 4; ++k) mma_bf16_ss(d2, dz + 128 * k, dp + 2 * k, id2, true);
-          if (KIND == kGrad) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_bf16_ss(d2, dz + 128 * (k & 3), dp + (1 + (k >> 2)) * (kPanel >> 4) + 2 * (k & 3), id2, true);
-          }
+          for (int k = 0; k < 4 * C::kTerms; ++k)
+            mma_bf16_ss(d2, dz + 128 * (k & 3), dp + (C::kTerms - 1 - (k >> 2)) * (kPanel >> 4) + 2 * (k & 3), id2, k > 0 || !apart);
           mma_commit(b_o + ob);
           mma_commit(b_empty + st);
         }
@@ -686,20 +688,28 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
             }
             mma_commit(b_sc);
           }
+          // tokf Z's terms from the lowest up: in the gradients the lower ones of both halves of the
+          // chunk first, else of each half, whose room is free the sooner
           const int db = c & (C::kDBufs - 1);
+          const uint32_t d = tmem + C::cD + 128 * db;
+          constexpr bool kBoth = KIND == kGrad;
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            const int hh = 2 * c + half, slot = hh % C::kTokBufs;
-            if (!(ok = need(b_w + slot, hh / C::kTokBufs) && (half || c < C::kDBufs || need(b_dfree + db, c / C::kDBufs - 1)))) break;
-            tc_fence_after();
+          for (int step = 0; step < (kBoth ? 4 : 2); ++step) {
+            const int half = step & 1, hh = 2 * c + half, slot = hh % C::kTokBufs;
             const uint64_t dy = mnmajor(st * C::kStage + C::oY, kPanel) + 256 * half;
             const uint64_t dw = mnmajor(C::offTok + slot * kTokB, kPanel / 2);
-            const uint32_t d = tmem + C::cD + 128 * db;
-            mma_bf16_ss(d, dw, dy, id_d, half > 0);
+            if (step < 2) {
+              if (!(ok = need(b_w + slot, hh / C::kTokBufs) && (half || c < C::kDBufs || need(b_dfree + db, c / C::kDBufs - 1)))) break;
+              tc_fence_after();
 #pragma unroll
-            for (int m = 1; m < 6; ++m)              // (m >> 1)-th term, 16 tokens
-              mma_bf16_ss(d, dw + (m >> 1) * (kPanel >> 4) + 128 * (m & 1), dy + 128 * (m & 1), id_d, true);
-            mma_commit(b_wfree + slot);
+              for (int m = 5; m >= 2; --m)           // (m >> 1)-th term, 16 tokens
+                mma_bf16_ss(d, dw + (m >> 1) * (kPanel >> 4) + 128 * (m & 1), dy + 128 * (m & 1), id_d, step > 0 || m < 5);
+            }
+            if (step >= 2 || !kBoth) {
+              mma_bf16_ss(d, dw, dy, id_d, true);
+              mma_bf16_ss(d, dw + 128, dy + 128, id_d, true);
+              mma_commit(b_wfree + slot);
+            }
           }
           if (!ok) break;
           mma_commit(b_d + db);

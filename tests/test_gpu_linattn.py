@@ -395,3 +395,35 @@ def test_rotary_then_attention(cuda_lib, dtype):
     o1 = cuda_lib.linattn_decode_step(q1, k1, d["v"][:, T].contiguous(), d["g"][:, T].contiguous(), S)
     r1, _ = ref.fwd(q1[:, None], k1[:, None], t["v"][:, T:], t["g"][:, T:], rS)
     assert_close(f64(o1), r1[:, 0].numpy(), TOL[dtype], "o of the next token", bf16_out=b)
+
+
+def decay_gradient(q, k, v, g, dO):
+    """dg of sum(dO o) in float64 on the GPU, token by token: g's share of S_t = e^g S_{t-1} + k v^T is
+    e^{g_t} <S_{t-1}, R_t>, R_t the gradient of S_t; <S_T, 0> plus the suffix sums of q.dq - k.dk."""
+    q, k, v, g, dO = (x.double() for x in (q, k, v, g, dO))
+    B, T, H, dk = q.shape
+    S = torch.zeros(B, H, dk, v.shape[-1], dtype=torch.float64, device=q.device)
+    R, dots = S.clone(), torch.zeros(B, T, H, dtype=torch.float64, device=q.device)
+    a = g.exp()[..., None, None]
+    for t in range(T):
+        S.mul_(a[:, t]).add_(k[:, t, :, :, None] * v[:, t, :, None, :])
+        dots[:, t] += ((S * dO[:, t, :, None, :]).sum(-1) * q[:, t]).sum(-1)
+    for t in range(T - 1, -1, -1):
+        R.add_(q[:, t, :, :, None] * dO[:, t, :, None, :])
+        dots[:, t] -= ((R * v[:, t, :, None, :]).sum(-1) * k[:, t]).sum(-1)
+        R.mul_(a[:, t])
+    return dots.flip(1).cumsum(1).flip(1)
+
+
+def test_decay_gradients_of_long_sequences(cuda_lib):
+    """bf16 inputs, a training batch whose sequences stay in few segments.  dg is a sum of q.dq - k.dk
+    over up to a segment's tokens.  The tensor cores truncate an accumulator at each addition, by
+    2^-24 of its value in the mean over all mantissas (half a step of 2^-23, times ln 2 and more): with
+    one addition per 16 of 128 channels and 64 tokens at full size, 12 x 2^-24 x ln 2 = 5e-7 of dq and
+    of dk, and so of dg, at most the sum of both: 1e-6.  (An addition for each of three terms would
+    be three times as many.)"""
+    t, (dO, _) = make(2, 3000, 26, 26, 26, 26, 128, 128, BF, state=False, seed=21)
+    d, dO = cuda(t), dO.cuda()
+    got = cuda_lib.linattn_bwd(**d, dO=dO, want_dS0=False)[3].double()
+    want = decay_gradient(d["q"], d["k"], d["v"], d["g"], dO)
+    assert float((got - want).norm() / want.norm()) <= 1e-6
