@@ -14,7 +14,7 @@
 // or a column of a product, so it is applied in fp32 to scores, to outputs as they leave, and
 // for the state to Z alone.  Per chunk of 64 tokens (all M = 128, fp32 accumulation in TMEM):
 //   scores  X Y^T            [64 x 64]   A, B from shared memory
-//   O       M X^T + Z^T P^T  [z x 64]    M as bf16 from TMEM, P as bf16 through shared memory
+//   O       M X^T + Z^T P^T  [z x 64]    M in bf16 terms from TMEM, P in bf16 terms through shared memory
 //   D       (tokf Z)^T Y     [z x x]     tokf Z in three bf16 terms
 // A row's factor rowf is common to both parts of O as long as P_ij / rowf_i stays in range (the
 // chunk decays by no more than 2^-100): P is formed as colb_j (x_i . y_j) and O is scaled once
@@ -22,21 +22,22 @@
 // decays faster still pair by pair; then the second part has its own accumulator.
 //
 // M is held in fp32: in registers, or (dq and dk, whose operand M is wanted in three terms, which
-// are an fp32 value's 24 bits) as those terms in tensor memory.  Roundings to bf16: P, M as an operand of O (each 2^-9 of a
-// term in the mean, the size of the output's own rounding); tokf Z is split into three terms
-// (24 bits), so M itself carries fp32 accuracy over any length.  Where row dots are wanted
-// (decay gradients, which cancel) M and P go into O in three terms too (two leave dg 2.7e-5 off).
+// are an fp32 value's 24 bits) as those terms in tensor memory.  tokf Z is split into three terms, so
+// M carries fp32 accuracy over any length.  M and P go into o and dv in two terms, 2^-18 of a value
+// off: what is left is the rounding of the output (1.66e-3; in one term each 2.35e-3), for 9 to 17 % of
+// the forward's time.  Where row dots are wanted (decay gradients, which cancel) M and P go into O in
+// three terms (two leave dg 2.7e-5 off).
 // The tensor cores truncate the accumulator at every addition (dq came out 4.4e-7 too small), so
 // terms are added from the lowest up, and the many additions of lower terms truncate a small sum
 // only: dg 1.8e-6 -> 1.0e-6 off, final states 2.3e-7 -> 1.1e-7 (B4 T4096 H16), for 4 % of the
 // gradients' time.  (D's lower terms of both halves of a chunk first, as the gradients take them, cost
 // the forward 10 %: there each half is added by itself.)
 //
-// One CTA per (segment, head), 24 warps: 0-3 state (200 registers a thread where they hold M), 4-11
+// One CTA per (segment, head), 28 warps: 0-3 and 24-27 state (112 registers a thread where they hold M), 4-11
 // outputs, 12, 13 and one of 16, 17 scores (a 32 x 32 block each), 14 TMA loads and decays, 15
 // issue of O, 23 issue of scores and D (two issuers: one thread's products take 50 cycles or
 // more each to issue), the rest tokf Z.  The roles run the chunks at their own pace through
-// mbarriers.  Spills and unrolled loops cost more than they save: 24 warps share 28 KB of L1, and
+// mbarriers.  Spills and unrolled loops cost more than they save: 28 warps share 28 KB of L1, and
 // waiting for code was 42 % of all stalls when the roles were fully unrolled.
 //
 // Measured (B200): B4 T4096 H16 128 x 128 forward 157 us, B8 T8192 H16 285 us (1090 MB, 3.8 TB/s,
@@ -157,19 +158,22 @@ __device__ __forceinline__ uint64_t f2bits(uint32_t a, uint32_t b) {
 // ------------------------------------------------------------------ shapes
 enum : int { kStates = 0, kOut = 1, kGrad = 2 };   // what a launch computes
 enum : int { kWhole = 0, kBlocks = 1, kPairs = 2 };   // how a chunk's weights are formed
-constexpr int kThreads = 768;
+constexpr int kThreads = 896;
 constexpr uint32_t kPanel = 8192;                  // 64 tokens x 64 channels of bf16, 128-byte swizzle
 constexpr uint32_t kTileB = 2 * kPanel;            // 64 tokens x 128 channels
+// The causal side of P in 32 x 32 blocks of 64-byte rows (64-byte swizzle): the two blocks that share
+// their columns (keys), one above the other, and the other diagonal block behind them
+constexpr uint32_t kPBig = 4096, kPTerm = 6144;
 constexpr uint32_t kTokB = 3 * kPanel;             // tokf Z of 32 tokens: three terms x two panels of 4 KB
-// Registers a thread by role where the state role holds M: 128 x 200 + 640 x 56 = 61,440, the
-// launch's 768 x 80.
-constexpr int kRegsState = 200, kRegsOther = 56;
+// Registers a thread by role where the state role holds M: 256 x 112 + 640 x 56 = 64,512, the
+// launch's 896 x 72.
+constexpr int kRegsState = 112, kRegsOther = 56;
 
 template <int KIND>
 struct Cfg {
   static constexpr int kTiles = KIND == kStates ? 2 : KIND == kOut ? 3 : 4;   // Y Z | X Y Z | X Y Z W
   static constexpr int kStages = KIND == kGrad ? 2 : 3;
-  static constexpr int kTerms = KIND == kGrad ? 3 : 1;                        // of M and P
+  static constexpr int kTerms = KIND == kGrad ? 3 : 2;                        // of M and P
   static constexpr int kTokBufs = KIND == kStates ? 4 : 2;                    // half chunks of tokf Z
   static constexpr uint32_t kStage = kTiles * kTileB;
   static constexpr uint32_t oX = 0;
@@ -178,16 +182,16 @@ struct Cfg {
   [[maybe_unused]] static constexpr uint32_t oW = oZ + kTileB;                // kGrad
   static constexpr uint32_t offTok = kStages * kStage;
   static constexpr uint32_t offP = offTok + kTokBufs * kTokB;
-  static constexpr uint32_t kP = KIND == kStates ? 0 : kTerms * kPanel;
+  static constexpr uint32_t kP = KIND == kStates ? 0 : kTerms * kPTerm;
   static constexpr uint32_t offOut = offP + kP;
   static constexpr uint32_t offGate = offOut + (KIND == kStates ? 0 : 8 * 2048);
   static constexpr uint32_t kGate = 7 * 64 * 4 + 16;                          // one stage's decays
   static constexpr uint32_t offDot = offGate + kStages * kGate;               // kGrad: 2 x 4 x 64 floats
   static constexpr uint32_t offBar = offDot + (KIND == kGrad ? 512 * 4 : 0);
-  static constexpr int kBars = 3 * kStages + 2 * kTokBufs + (KIND == kGrad ? 25 : 21);
+  static constexpr int kBars = 3 * kStages + 2 * kTokBufs + (KIND == kStates ? 21 : 25);
   static constexpr uint32_t kSmem = offBar + kBars * 8 + 64 + 1024;           // + slack to align
   // TMEM columns: scores, M, O twice, D (twice where there is room)
-  static constexpr int kDBufs = KIND == kGrad ? 1 : 2;
+  static constexpr int kDBufs = KIND == kStates ? 2 : 1;
   static constexpr uint32_t cSc = 0, cM = 64, cO = cM + 64 * kTerms, cD = 512 - 128 * kDBufs;
 };
 static_assert(Cfg<kGrad>::cO + 128 <= Cfg<kGrad>::cD && Cfg<kOut>::cO + 128 <= Cfg<kOut>::cD, "tensor memory");
@@ -263,7 +267,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
   uint64_t *b_full = bars, *b_empty = bars + C::kStages, *b_gate = bars + 2 * C::kStages;
   uint64_t *b_w = bars + 3 * C::kStages, *b_wfree = b_w + C::kTokBufs;
   uint64_t *bx = b_wfree + C::kTokBufs;
-  uint64_t *b_zeroed = bx, *b_sc = bx + 1, *b_p = bx + 2, *b_s = bx + (KIND == kGrad ? 21 : 3) /* 4 in kGrad */, *b_o = bx + 4 /* 2 */,
+  uint64_t *b_zeroed = bx, *b_sc = bx + 1, *b_p = bx + 2, *b_s = bx + 21 /* 4, kOut and kGrad */, *b_o = bx + 4 /* 2 */,
            *b_ofree = bx + 6 /* 2 */, *b_d = bx + 8 /* 2 */, *b_dfree = bx + 16 /* 2 */, *b_drain = bx + 10 /* 2 */,
            *b_red = bx + 12 /* 2 */, *b_o1 = bx + 14;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bx + 18);
@@ -273,8 +277,8 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(b_full + s, 1);
-      // state 4, tokf Z, a commit; beside outputs 8, scores 3 and a second commit
-      mbar_init(b_empty + s, 4 + tok_warps + 1 + (KIND == kStates ? 0 : 12));
+      // state 8, tokf Z, a commit; beside outputs 8, scores 3 and a second commit
+      mbar_init(b_empty + s, 8 + tok_warps + 1 + (KIND == kStates ? 0 : 12));
       mbar_init(b_gate + s, 1);
     }
     for (int s = 0; s < C::kTokBufs; ++s) {
@@ -284,12 +288,12 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
     mbar_init(b_zeroed, tok_warps);
     mbar_init(b_sc, 1);
     mbar_init(b_p, 3);
-    for (int s = 0; s < (KIND == kGrad ? 4 : 1); ++s) mbar_init(b_s + s, 4);
+    for (int s = 0; s < (KIND == kStates ? 0 : 4); ++s) mbar_init(b_s + s, 4);
     mbar_init(b_o1, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(b_o + s, 1);
       mbar_init(b_d + s, 1);
-      mbar_init(b_dfree + s, 4);
+      mbar_init(b_dfree + s, 8);
       mbar_init(b_ofree + s, 8);
       mbar_init(b_red + s, 8);
       mbar_init(b_drain + s, 1);
@@ -299,10 +303,6 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
     mbar_fence_init();
   }
   if (warp == 15) tmem_alloc(s_tmem, 512);
-  // (scores on the acausal side are never written: they stay 0)
-  for (int i = tid; i < (int)(C::kP / 16); i += kThreads)
-    reinterpret_cast<uint4 *>(sm + C::offP)[i] = make_uint4(0, 0, 0, 0);
-  fence_proxy_async();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -316,6 +316,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
   const uint32_t sb = smem_u32(sm);
   constexpr uint64_t kHi = (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32;
   auto kmajor = [&](uint32_t at) { return kHi | (((sb + at) >> 4) | (1u << 16)); };
+  constexpr uint64_t kHi64 = (uint64_t)((512u >> 4) | (1u << 14) | (4u << 29)) << 32;   // 64-byte swizzle: P
   auto mnmajor = [&](uint32_t at, uint32_t panel) { return kHi | (((sb + at) >> 4) | ((panel >> 4) << 16)); };
   auto gates = [&](int st) { return reinterpret_cast<float *>(sm + C::offGate + st * C::kGate); };
   // gates (floats): [0] rowf, [64] tokf, [128] colb, [192] rowb, [256] cross, [320] G (64-bit
@@ -339,13 +340,16 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
   uint32_t ph = 0;
   bool ok = true;
 
-  if (KIND == kGrad && warp < 4) {
-    // ---------------------------------------------------------------- state (warps 0-3)
+  // State: the warps of group 0 (0-3) and 1 (24-27) take turns at blocks of 32 x channels
+  const bool is_state = warp < 4 || warp >= 24;
+  const int quad_warp = warp & 3, group = warp >= 24;
+  if (KIND == kGrad && is_state) {
+    // ---------------------------------------------------------------- state (warps 0-3, 24-27)
     // M is its operand: three bf16 terms hold an fp32 value's 24 bits, and O1 wants them anyway.
     // So M lives in tensor memory only, and a chunk's M <- e^{G_C} M + D is one short loop: held in
     // registers as in the other kinds, the unrolled splitting alone was 11 KB of code a chunk, for
     // which the warps waited more than they computed (put 5,300 cycles of 8,000 a chunk).
-    const uint32_t quarter = tmem + ((uint32_t)(32 * warp) << 16), lanes = quarter + C::cM;
+    const uint32_t quarter = tmem + ((uint32_t)(32 * quad_warp) << 16), lanes = quarter + C::cM;
     auto split = [&](const uint64_t (&m)[8], uint32_t (&r)[3][8]) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -363,7 +367,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
     // time, in the layout that puts a row into a lane (a lane's own row, 4 bytes or 16 at a time,
     // took 20,000 cycles in and 34,000 out).
     const size_t state = ((size_t)blockIdx.x * p.H + h) * p.elems;
-    const int z0 = 32 * warp + (lane >> 2), x0 = 2 * (lane & 3);
+    const int z0 = 32 * quad_warp + (lane >> 2), x0 = 2 * (lane & 3);
     auto at = [&](int b, int y, int i) {             // where word i of 16 lanes and channels 32 b .. is stored
       return (size_t)(z0 + 16 * y + 8 * (i & 1)) * ps.dx + 32 * b + 8 * (i >> 1) + x0;
     };
@@ -375,7 +379,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
       if (lane == 0) mbar_arrive(b_s + b);
     };
 #pragma unroll 1
-    for (int b = 0; 32 * b < ps.dx; ++b) {
+    for (int b = group; 32 * b < ps.dx; b += 2) {
       uint64_t m[2][8];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -401,7 +405,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
       if (!(ok = wait(b_o1, c) && wait(b_d, c))) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int b = 0; 16 * b < ps.dx; ++b) {
+      for (int b = 2 * group; 16 * b < ps.dx; b += b & 1 ? 3 : 1) {
         uint32_t d[16], r[3][8];
         uint64_t m[8];
         tmem_ld16(quarter + C::cD + 16 * b, d);
@@ -415,12 +419,13 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
         for (int t = 0; t < 3; ++t) tmem_st8(lanes + 64 * t + 8 * b, r[t]);
         if ((b & 1) || ps.dx == 16) ready(b >> 1);
       }
+      __syncwarp();
       if (lane == 0) mbar_arrive(b_dfree);
     }
     if (ok && last_seg && ps.end_slot) {
       float *dst = ps.end_slot + state + (size_t)p.H * p.elems;      // the next slot
 #pragma unroll 1
-      for (int b = 0; 32 * b < ps.dx; ++b) {
+      for (int b = group; 32 * b < ps.dx; b += 2) {
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           uint32_t r[3][8];
@@ -433,13 +438,15 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
         }
       }
     }
-  } else if (KIND != kGrad && warp < 4) {
-    // ---------------------------------------------------------------- state (warps 0-3)
+  } else if (KIND != kGrad && is_state) {
+    // ---------------------------------------------------------------- state (warps 0-3, 24-27)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsState));
-    const int z = tid;                              // this thread's value channel (TMEM lane)
-    const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+    const int z = 32 * quad_warp + lane;            // this thread's value channel (TMEM lane)
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad_warp) << 16);
     const bool live = z < ps.dz;
-    uint64_t M[64];                                 // x channels 2 i, 2 i + 1
+    uint64_t M[32];                                 // x channels x_of(i) and the next
+    auto block = [&](int j) { return 2 * j + group; };              // the j-th of this group's blocks
+    auto x_of = [&](int i) { return 32 * block(i >> 4) + 2 * (i & 15); };
     {
       const float *src = nullptr;
       if (KIND != kStates) {
@@ -447,27 +454,36 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
         else if (ps.init) src = ps.init + ((size_t)u.n * p.H + h) * p.elems;
       }
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        const bool in = src && live && 2 * i < ps.dx;
-        M[i] = f2pk(in ? src[(2 * i) * ps.dz + z] : 0.f, in ? src[(2 * i + 1) * ps.dz + z] : 0.f);
+      for (int i = 0; i < 32; ++i) {
+        const bool in = src && live && x_of(i) < ps.dx;
+        M[i] = f2pk(in ? src[x_of(i) * ps.dz + z] : 0.f, in ? src[(x_of(i) + 1) * ps.dz + z] : 0.f);
       }
     }
-    // M as the next chunk's operand
-    auto put_state = [&]() {
+    // a block of M as the next chunk's operand
+    auto put_state = [&](int j) {
+      const uint32_t at = lanes + C::cM + 16 * block(j);
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        if (16 * b >= ps.dx) break;
-        uint32_t r[8];
+      for (int t = 0; t < 2; ++t) {
+        uint32_t r[2][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = pack_bf16(M[8 * b + i]);
-        tmem_st8(lanes + C::cM + 8 * b, r);
+        for (int i = 0; i < 8; ++i) {
+          const uint64_t m = M[16 * j + 8 * t + i];
+          r[0][i] = pack_bf16(m);
+          r[1][i] = pack_bf16(f2sub(m, unpack_bf16(r[0][i])));
+        }
+        tmem_st8(at + 8 * t, r[0]);
+        tmem_st8(at + 64 + 8 * t, r[1]);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(b_s);
+      if (lane == 0) mbar_arrive(b_s + block(j));
     };
-    if (KIND != kStates) put_state();
+    if (KIND != kStates) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (32 * block(j) < ps.dx) put_state(j);
+    }
     long long whole = 0;                            // kStates: the segment's decay
     for (; c < nc; ++c, next(st, ph)) {
       if (!(ok = wait(b_gate + st, ph))) break;
@@ -477,25 +493,23 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
       __syncwarp();
       if (lane == 0) mbar_arrive(b_empty + st);
       const int db = c & (C::kDBufs - 1);
-      if (!(ok = wait(b_d + db, c / C::kDBufs))) break;
+      // (O1 of this chunk has read the operand)
+      const bool put = KIND != kStates && c + 1 < nc;
+      if (!(ok = wait(b_d + db, c / C::kDBufs) && (!put || wait(b_o1, c)))) break;
       tc_fence_after();
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (32 * b >= ps.dx) break;
+      for (int j = 0; j < 2; ++j) {
+        if (32 * block(j) >= ps.dx) break;
         uint32_t r[32];
-        tmem_ld32(lanes + C::cD + 128 * (c & (C::kDBufs - 1)) + 32 * b, r);
+        tmem_ld32(lanes + C::cD + 128 * (c & (C::kDBufs - 1)) + 32 * block(j), r);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) M[16 * b + i] = f2fma(a2, M[16 * b + i], f2bits(r[2 * i], r[2 * i + 1]));
+        for (int i = 0; i < 16; ++i) M[16 * j + i] = f2fma(a2, M[16 * j + i], f2bits(r[2 * i], r[2 * i + 1]));
+        if (put) put_state(j);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_dfree + db);
-      if (KIND != kStates && c + 1 < nc) {
-        if (!(ok = wait(b_o1, c))) break;           // (O1 of this chunk has read the operand)
-        tc_fence_after();
-        put_state();
-      }
     }
     // (a backward walk's segments but the last belong to the forward walk too, which writes theirs)
     if (KIND == kStates && ok && tid == 0 && (!rev || u.piece == u.pieces - 1))
@@ -503,12 +517,12 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
     if (ok && live) {
       auto store = [&](float *dst) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
+        for (int i = 0; i < 32; ++i) {
           float a, b;
           f2up(M[i], a, b);
-          if (2 * i >= ps.dx) break;
-          dst[(2 * i) * ps.dz + z] = a;
-          dst[(2 * i + 1) * ps.dz + z] = b;
+          if (x_of(i) >= ps.dx) break;
+          dst[x_of(i) * ps.dz + z] = a;
+          dst[(x_of(i) + 1) * ps.dz + z] = b;
         }
       };
       if (KIND == kStates) store(ps.end_slot + ((size_t)blockIdx.x * p.H + h) * p.elems);
@@ -600,7 +614,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
     } else if (warp == 15) {
       // -------------------------------------------------------------- issue of O
       if (KIND != kStates && lane == 0) {
-        const uint32_t id1 = idesc_bf16(128, 64, false, false), id2 = idesc_bf16(128, 64, true, false);
+        const uint32_t id1 = idesc_bf16(128, 64, false, false), id2 = idesc_bf16(128, 64, true, false), id3 = idesc_bf16(128, 32, true, false);
         // M's columns times X^T, 16 channels at a time
         auto out1 = [&](uint32_t d, uint32_t m, uint64_t b, bool more) {
           mma_bf16_ts(d, m, b, id1, more);
@@ -619,41 +633,44 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
         for (; ok && c < nc; ++c, next(st, ph)) {
           // (the outputs that were in this buffer have been read; X is there, for the scores read it)
           const int ob = c & 1;
-          if (!(ok = (KIND == kGrad || need(b_s, c)) && (c < 2 || need(b_ofree + ob, (c >> 1) - 1)))) break;
+          if (!(ok = (c < 2 || need(b_ofree + ob, (c >> 1) - 1)))) break;
           if (!(ok = need(b_full + st, ph) && need(b_gate + st, ph) && (!both || need(b_ofree + (ob ^ 1), (c - 1) >> 1)))) break;
           tc_fence_after();
           const uint64_t x = kmajor(st * C::kStage + C::oX);
           const uint32_t d = tmem + C::cO + 64 * ob;
-          if constexpr (KIND == kGrad) {
-            // the lower terms of 32 channels of M at a time, as they are updated, then all first terms
+          // 32 channels of M at a time, as they are updated: of the gradients' the lower terms, and
+          // all first terms at the end
 #pragma unroll 1
-            for (int b = 0; 32 * b < ps.dx; ++b) {
-              if (!(ok = need(b_s + b, c))) break;
-              tc_fence_after();
-              const uint64_t xb = x + (b >> 1) * (kPanel >> 4) + 4 * (b & 1);
+          for (int b = 0; 32 * b < ps.dx; ++b) {
+            if (!(ok = need(b_s + b, c))) break;
+            tc_fence_after();
+            const uint64_t xb = x + (b >> 1) * (kPanel >> 4) + 4 * (b & 1);
 #pragma unroll
-              for (int t = 2; t >= 1; --t) {
-                mma_bf16_ts(d, tmem + C::cM + 64 * t + 16 * b, xb, id1, b > 0 || t < 2);
-                if (ps.dx > 16) mma_bf16_ts(d, tmem + C::cM + 64 * t + 16 * b + 8, xb + 2, id1, true);
-              }
+            for (int t = C::kTerms - 1; t >= C::kTerms - 2; --t) {
+              mma_bf16_ts(d, tmem + C::cM + 64 * t + 16 * b, xb, id1, b > 0 || t < C::kTerms - 1);
+              if (ps.dx > 16) mma_bf16_ts(d, tmem + C::cM + 64 * t + 16 * b + 8, xb + 2, id1, true);
             }
-            if (!ok) break;
-            out1(d, tmem + C::cM, x, true);
-          } else {
-            out1(d, tmem + C::cM, x, false);
           }
+          if (!ok) break;
+          if (KIND == kGrad) out1(d, tmem + C::cM, x, true);
           mma_commit(b_o1);
           // the second part on top, or (weights not over the whole chunk) in the other buffer
           const bool apart = gates(st)[449] != (float)kWhole;
           if (!(ok = need(b_p, c) && (!apart || c == 0 || need(b_ofree + (ob ^ 1), (c - 1) >> 1)))) break;
           tc_fence_after();
-          const uint64_t dz = mnmajor(st * C::kStage + C::oZ, kPanel), dp = kmajor(C::offP);
+          // (P's terms, the last first: its two blocks of common keys for all tokens, then the other)
+          const uint64_t dz = mnmajor(st * C::kStage + C::oZ, kPanel) + (rev ? 256 : 0), dp = kHi64 | ((sb + C::offP) >> 4) | (1u << 16);
+          const uint64_t dz2 = mnmajor(st * C::kStage + C::oZ, kPanel) + (rev ? 0 : 256);
           const uint32_t d2 = apart ? tmem + C::cO + 64 * (ob ^ 1) : d;
           both = apart;
-          // (P's terms, the last first)
 #pragma unroll
-          for (int k = 0; k < 4 * C::kTerms; ++k)
-            mma_bf16_ss(d2, dz + 128 * (k & 3), dp + (C::kTerms - 1 - (k >> 2)) * (kPanel >> 4) + 2 * (k & 3), id2, k > 0 || !apart);
+          for (int t = C::kTerms - 1; t >= 0; --t) {
+            const uint64_t dt = dp + t * (kPTerm >> 4);
+            mma_bf16_ss(d2, dz, dt, id2, t < C::kTerms - 1 || !apart);
+            mma_bf16_ss(d2, dz + 128, dt + 2, id2, true);
+            mma_bf16_ss(d2 + (rev ? 0 : 32), dz2, dt + (kPBig >> 4), id3, true);
+            mma_bf16_ss(d2 + (rev ? 0 : 32), dz2 + 128, dt + (kPBig >> 4) + 2, id3, true);
+          }
           mma_commit(b_o + ob);
           mma_commit(b_empty + st);
         }
@@ -776,7 +793,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
       const int rb = warp & 3, row = 32 * rb + lane;               // rows (TMEM lanes) of the block
       const int cb = warp < 16 ? rb : 1 - rb;                      // its columns: the diagonal, or the causal other
       const uint32_t lanes = tmem + ((uint32_t)(32 * rb) << 16);
-      uint8_t *P = sm + C::offP + row * 128;
+      uint8_t *P = sm + C::offP + (cb == (rev ? 1 : 0) ? row * 64 : kPBig + lane * 64);
       const uint32_t mask = cb != rb ? ~0u : rev ? ~0u << lane : ~0u >> (31 - lane);   // the causal columns
       for (; c < nc; ++c, next(st, ph)) {
         if (!(ok = wait(b_gate + st, ph))) break;
@@ -798,7 +815,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
 #pragma unroll
             for (int t = 0; t < C::kTerms; ++t) {
               const __nv_bfloat16 v = __float2bfloat16_rn(x);
-              *reinterpret_cast<__nv_bfloat16 *>(P + t * kPanel + (((4 * cb + j / 8) ^ (row & 7)) << 4) + 2 * (j & 7)) = v;
+              *reinterpret_cast<__nv_bfloat16 *>(P + t * kPTerm + ((j / 8 ^ (lane >> 1 & 3)) << 4) + 2 * (j & 7)) = v;
               x -= __bfloat162float(v);
             }
           }
@@ -823,20 +840,16 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
               float a, b;
               f2up(f2mul(f2bits(s[2 * j], s[2 * j + 1]), f2mul(f[j], mine)), a, b);
               uint64_t x = f2pk(m & (1u << (2 * j)) ? a : 0.f, m & (2u << (2 * j)) ? b : 0.f);
-              r[0][j] = pack_bf16(x);
-              if constexpr (KIND == kGrad) {
-                x = f2sub(x, unpack_bf16(r[0][j]));
-                r[1][j] = pack_bf16(x);
-                x = f2sub(x, unpack_bf16(r[1][j]));
-                r[2][j] = pack_bf16(x);
+#pragma unroll
+              for (int t = 0; t < C::kTerms; ++t) {
+                r[t][j] = pack_bf16(x);
+                x = f2sub(x, unpack_bf16(r[t][j]));
               }
             }
-            uint8_t *at = P + (((j0 / 8) ^ (row & 7)) << 4);
-            *reinterpret_cast<uint4 *>(at) = make_uint4(r[0][0], r[0][1], r[0][2], r[0][3]);
-            if constexpr (KIND == kGrad) {
-              *reinterpret_cast<uint4 *>(at + kPanel) = make_uint4(r[1][0], r[1][1], r[1][2], r[1][3]);
-              *reinterpret_cast<uint4 *>(at + 2 * kPanel) = make_uint4(r[2][0], r[2][1], r[2][2], r[2][3]);
-            }
+            uint8_t *at = P + ((q ^ (lane >> 1 & 3)) << 4);
+#pragma unroll
+            for (int t = 0; t < C::kTerms; ++t)
+              *reinterpret_cast<uint4 *>(at + t * kPTerm) = make_uint4(r[t][0], r[t][1], r[t][2], r[t][3]);
           }
         }
         fence_proxy_async();

@@ -427,3 +427,22 @@ def test_decay_gradients_of_long_sequences(cuda_lib):
     got = cuda_lib.linattn_bwd(**d, dO=dO, want_dS0=False)[3].double()
     want = decay_gradient(d["q"], d["k"], d["v"], d["g"], dO)
     assert float((got - want).norm() / want.norm()) <= 1e-6
+
+
+@pytest.mark.parametrize("decay", [None, -1.5, -6.0])
+def test_bf16_results_are_rounded_once(cuda_lib, decay):
+    """bf16 outputs and gradients against the float64 ones rounded to bf16.  The kernel's operands (state
+    and scores) keep 17 bits and more: each at most 2^-18 off, so a result is at most about 2^-17 off
+    before it is rounded, and only values that lie that near a border between two bf16 values (steps of at
+    least 2^-8 of the value), 2 x 2^-17 / 2^-8 = 2^-8 of them, may fall on its other side, by a step of
+    at most 2^-7: sqrt(2^-8) x 2^-7 = 2^-11 in the mean square.  (Operands of 8 bits: 2.6e-3.)"""
+    t, (dO, dS) = make(2, 300, 4, 4, 2, 4, 128, 64, BF, seed=31)
+    if decay is not None:
+        t["g"] = torch.full_like(t["g"], decay)
+    d = cuda(t)
+    o, _ = cuda_lib.linattn_fwd(**d)
+    grads = cuda_lib.linattn_bwd(**d, dO=dO.cuda(), dS_T=dS.cuda())[:3]
+    want = [ref.fwd(**t)[0]] + [x.detach() for x in ref.bwd(**t, dO=dO, dS_T=dS)[:3]]
+    for x, y, name in zip((o, *grads), want, ("o", "dq", "dk", "dv")):
+        once = y.to(BF).double()
+        assert float((x.double().cpu() - once).norm() / once.norm()) <= 2.0 ** -11, name
