@@ -30,9 +30,9 @@ __global__ void __launch_bounds__(256, 2) linattn_decode_kernel(const LinDecodeA
     st[m] = __ldcs(reinterpret_cast<const float4 *>(S + (r0 + 8 * m) * DV));
   const uint32_t b = head / (uint32_t)p.H;
   const int h = (int)(head - b * p.H);
-  const T *q = static_cast<const T *>(p.q) + ((size_t)b * p.Hq + h * p.Hq / p.H) * DK;
-  const T *k = static_cast<const T *>(p.k) + ((size_t)b * p.Hk + h * p.Hk / p.H) * DK;
-  const T *v = static_cast<const T *>(p.v) + ((size_t)b * p.Hv + h * p.Hv / p.H) * DV + col;
+  const T *q = static_cast<const T *>(p.q) + ((size_t)b * p.Hq + head_of(h, p.H, p.Hq)) * DK;
+  const T *k = static_cast<const T *>(p.k) + ((size_t)b * p.Hk + head_of(h, p.H, p.Hk)) * DK;
+  const T *v = static_cast<const T *>(p.v) + ((size_t)b * p.Hv + head_of(h, p.H, p.Hv)) * DV + col;
   for (int i = lane; i < DK; i += 32) s_kq[warp][i] = make_float2(to_f32(k[i]), to_f32(q[i]));
   const float al = expf(p.g[p.g_fixed ? (uint32_t)h : head]);
   const float v0 = to_f32(v[0]), v1 = to_f32(v[1]), v2 = to_f32(v[2]), v3 = to_f32(v[3]);

@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(kThreads) lin_local_kernel(const LocalParams p
   const int slice = blockIdx.z % p.cols, m0 = 64 * (blockIdx.z / p.cols % blocks), back = blockIdx.z / (p.cols * blocks);
   const int c0 = 16 * NJ * slice, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   chunk_gates(sG, sE, sW, p.g, u.row0, u.len, p.H, h, p.g_fixed);
-  load_tile(sY, kLdP, p.y[back], u.row0, u.len, p.hy[back], h * p.hy[back] / p.H, p.ndk, m0, 64);
-  load_tile(sZ, kLdP, p.z[back], u.row0, u.len, p.hz[back], h * p.hz[back] / p.H, p.ndv, c0, 16 * NJ);
+  load_tile(sY, kLdP, p.y[back], u.row0, u.len, p.hy[back], head_of(h, p.H, p.hy[back]), p.ndk, m0, 64);
+  load_tile(sZ, kLdP, p.z[back], u.row0, u.len, p.hz[back], head_of(h, p.H, p.hz[back]), p.ndv, c0, 16 * NJ);
   __syncthreads();
   const float *w = back ? sE : sW;
   for (int i = threadIdx.x; i < kC * 4 * NJ; i += kThreads) {
@@ -283,9 +283,9 @@ __global__ void __launch_bounds__(kThreads) lin_pass_kernel(const PassParams p) 
   const int h = blockIdx.y, c0 = 16 * NJ * (blockIdx.z - pi * p.slices), tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   if (c0 >= ps.dz) return;
   chunk_gates(sG, sE, sW, p.g, u.row0, u.len, p.H, h, p.g_fixed);
-  load_tile(sX, kLd, ps.x, u.row0, u.len, ps.hx, h * ps.hx / p.H, ps.dx, 0, ps.dx);
-  load_tile(sY, kLd, ps.y, u.row0, u.len, ps.hy, h * ps.hy / p.H, ps.dx, 0, ps.dx);
-  load_tile(sZ, kLd, ps.z, u.row0, u.len, ps.hz, h * ps.hz / p.H, ps.dz, c0, 16 * NJ);
+  load_tile(sX, kLd, ps.x, u.row0, u.len, ps.hx, head_of(h, p.H, ps.hx), ps.dx, 0, ps.dx);
+  load_tile(sY, kLd, ps.y, u.row0, u.len, ps.hy, head_of(h, p.H, ps.hy), ps.dx, 0, ps.dx);
+  load_tile(sZ, kLd, ps.z, u.row0, u.len, ps.hz, head_of(h, p.H, ps.hz), ps.dz, c0, 16 * NJ);
   __syncthreads();
   {
     float acc[4][4];
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads) lin_pass_kernel(const PassParams p) 
     if (ps.dots) {                                 // over the 16 threads of a row, then the slices
       float d = 0.f;
       if (r < u.len && col < ps.dz) {
-        const float *w = ps.w + ((size_t)(u.row0 + r) * ps.hw + h * ps.hw / p.H) * ps.dz + col;
+        const float *w = ps.w + ((size_t)(u.row0 + r) * ps.hw + head_of(h, p.H, ps.hw)) * ps.dz + col;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) d = fmaf(w[j], acc[i][j], d);
       }

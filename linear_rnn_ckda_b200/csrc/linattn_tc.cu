@@ -543,7 +543,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
       const int tile = (lane >> 1) + (KIND == kStates ? 1 : 0);
       const bool load = lane < 2 * C::kTiles && (lane & 1) < (tile < 2 ? px : pz);
       const int map = tile == 0 ? ps.ix : tile == 1 ? ps.iy : tile == 2 ? ps.iz : ps.iw;
-      const int head = h * (tile == 0 ? ps.hx : tile == 1 ? ps.hy : tile == 2 ? ps.hz : ps.hw) / p.H;
+      const int head = load ? head_of(h, p.H, tile == 0 ? ps.hx : tile == 1 ? ps.hy : tile == 2 ? ps.hz : ps.hw) : 0;
       for (; c < nc; ++c, next(st, ph)) {
         const int ci = chunk_at(c), len = rows_of(ci);
         const bool turn = KIND != kStates || (c & 1) == (warp == 14 ? 0 : 1);

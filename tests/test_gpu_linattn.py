@@ -446,3 +446,19 @@ def test_bf16_results_are_rounded_once(cuda_lib, decay):
     for x, y, name in zip((o, *grads), want, ("o", "dq", "dk", "dv")):
         once = y.to(BF).double()
         assert float((x.double().cpu() - once).norm() / once.norm()) <= 2.0 ** -11, name
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_many_heads(cuda_lib, dtype):
+    """50,000 heads (their product with a tensor's heads passes 32 bits), own and shared ones: one
+    token, a prompt and its gradients."""
+    H = 50_000
+    t, (dO, dS) = make(1, 3, H, H, H // 2, H, 16, 16, dtype, seed=41)
+    check_fwd(cuda_lib, t)
+    check_bwd(cuda_lib, t, dO, dS)
+    d = cuda(t)
+    S = d["S0"].clone()
+    o = cuda_lib.linattn_decode_step(*(d[n][:, 0].contiguous() for n in ("q", "k", "v", "g")), S)
+    ro, rS = ref.fwd(**{n: x if n == "S0" else x[:, :1] for n, x in t.items()})
+    assert_close(f64(o), ro[:, 0].numpy(), TOL[dtype], "o", bf16_out=dtype == BF)
+    assert_close(f64(S), rS.numpy(), TOL[F32], "S")

@@ -256,3 +256,27 @@ def test_empty_calls_need_no_pointers(lib):
     assert lib.ckda_linattn_decode_step(None, None, None, None, None, 0, 4, 4, 4, 4, 65, 64, 0, 0, None,
                                         None) == -2
     assert ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+def test_shared_heads_up_to_the_most(tmp_path):
+    """head_of(h, H, Hx), the head of a shared tensor that a kernel reads, is h * Hx // H for every size
+    that the calls accept: from H = 46,342 on that product no longer fits 32 bits."""
+    import os
+    import subprocess
+
+    src = os.path.join(lib_build.CSRC, "linattn.h")
+    (tmp_path / "h.cc").write_text(f'''#include "{src}"
+#include <cstdio>
+int main() {{
+  for (int H : {{1, 6, 46341, 46342, 50000, 65520, 65535}})
+    for (int Hx = 1; Hx <= H; ++Hx) {{
+      if (H % Hx) continue;
+      for (int h = 0; h < H; ++h)
+        if (ckda::head_of(h, H, Hx) != (long long)h * Hx / H) return std::printf("%d %d %d", h, H, Hx), 1;
+    }}
+  return 0;
+}}''')
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(lib_build.nvcc()))), "include")
+    subprocess.run(["g++", "-std=c++17", "-I", cuda, str(tmp_path / "h.cc"), "-o", str(tmp_path / "h")], check=True)
+    r = subprocess.run([str(tmp_path / "h")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
