@@ -227,7 +227,8 @@ int ckda_decode_step(const void *q, const void *k, const void *v, const void *a,
  *   workspace : device scratch of ckda_linattn_fwd_workspace_size() bytes, 256-byte aligned,
  *            never shared by two calls in flight at once; its status word is read with
  *            ckda_workspace_status.
- * fp32 inputs are computed in exact fp32.  Returns CKDA_OK or a negative CKDA_ERR_* code.
+ * fp32 inputs are computed in exact fp32.  bf16 outputs are rounded once; states and the products
+ * q . k are held to 24 and 17 bits, and to about 2^-54 absolutely.  Returns CKDA_OK or a negative CKDA_ERR_* code.
  */
 int ckda_linattn_fwd(const void *q, const void *k, const void *v, const float *g, const float *S0,
                      const int32_t *cu_seqlens, int n_seqs, int B, int T, int H, int Hq, int Hk,

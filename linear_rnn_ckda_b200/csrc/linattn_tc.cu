@@ -16,11 +16,14 @@
 //   scores  X Y^T            [64 x 64]   A, B from shared memory
 //   O       M X^T + Z^T P^T  [z x 64]    M in bf16 terms from TMEM, P in bf16 terms through shared memory
 //   D       (tokf Z)^T Y     [z x x]     tokf Z in three bf16 terms
-// A row's factor rowf is common to both parts of O as long as P_ij / rowf_i stays in range (the
-// chunk decays by no more than 2^-100): P is formed as colb_j (x_i . y_j) and O is scaled once
-// as it leaves.  A chunk that decays faster takes its weights block by block, and one that
-// decays faster still pair by pair; then the second part has its own accumulator.
-//
+// While a chunk decays by no more than 2^-72, a row's factor is common to both parts of O: P is
+// formed as colb_j (x_i . y_j) and O is scaled once as it leaves.  So that no value can leave fp32's
+// range on the way, M is held times 2^-72 and so is colb, whose 1 / rowf_i <= 2^72 it makes up for:
+// nothing is larger than what it stands for.  Small values pay: states and x . y are held to about
+// 2^-126 2^72 = 2^-54 absolutely.  (With 2^-64 decays of 2^(-1/2) a token, a usual slope, already take
+// the form by blocks: B8 T8192 H16 with one such head 444 us, with 72 411.)  A chunk that decays faster
+// takes its weights block by block, and one that decays faster still pair by pair; then the second
+// part has its own accumulator.
 // M is held in fp32: in registers, or (dq and dk, whose operand M is wanted in three terms, which
 // are an fp32 value's 24 bits) as those terms in tensor memory.  tokf Z is split into three terms, so
 // M carries fp32 accuracy over any length.  M and P go into o and dv in two terms, 2^-18 of a value
@@ -159,6 +162,9 @@ __device__ __forceinline__ uint64_t f2bits(uint32_t a, uint32_t b) {
 enum : int { kStates = 0, kOut = 1, kGrad = 2 };   // what a launch computes
 enum : int { kWhole = 0, kBlocks = 1, kPairs = 2 };   // how a chunk's weights are formed
 constexpr int kThreads = 896;
+// M is held times 2^-kShift; a chunk's weights have one reference while it decays by 2^-kShift at most
+constexpr int kShift = 72;
+constexpr float kUp = 4722366482869645213696.f, kDown = 1.f / kUp;
 constexpr uint32_t kPanel = 8192;                  // 64 tokens x 64 channels of bf16, 128-byte swizzle
 constexpr uint32_t kTileB = 2 * kPanel;            // 64 tokens x 128 channels
 // The causal side of P in 32 x 32 blocks of 64-byte rows (64-byte swizzle): the two blocks that share
@@ -319,9 +325,9 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
   constexpr uint64_t kHi64 = (uint64_t)((512u >> 4) | (1u << 14) | (4u << 29)) << 32;   // 64-byte swizzle: P
   auto mnmajor = [&](uint32_t at, uint32_t panel) { return kHi | (((sb + at) >> 4) | ((panel >> 4) << 16)); };
   auto gates = [&](int st) { return reinterpret_cast<float *>(sm + C::offGate + st * C::kGate); };
-  // gates (floats): [0] rowf, [64] tokf, [128] colb, [192] rowb, [256] cross, [320] G (64-bit
+  // gates (floats): [0] rowf 2^72, [64] tokf 2^-72, [128] colb, [192] rowb, [256] cross, [320] G (64-bit
   // fixed point), [448] e^{G_C}, [449] mode, [450] G_C.  P_ij is (x_i . y_j) times
-  //   kWhole : colb_j, its row's factor left to rowf (the chunk decays by at most 2^-100)
+  //   kWhole : colb_j 2^-72, its row's factor left to rowf (the chunk decays by at most 2^-72)
   //   kBlocks: rowb_i colb_j on the diagonal 32 x 32 blocks, cross_i cross_j (through token 31) off
   //            them (each half decays by at most 2^-100)
   //   kPairs : each pair's own weight on the diagonal blocks, cross_i cross_j off them
@@ -386,9 +392,12 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
         const int y = i >> 3, w = i & 7;
         m[y][w] = have(b, y, w) ? *reinterpret_cast<const uint64_t *>(ps.seg_in + state + at(b, y, w)) : 0;
       }
+      __syncwarp();                                  // (all loads are in flight)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         uint32_t r[3][8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) m[y][w] = f2mul(f2pk(kDown, kDown), m[y][w]);
         split(m[y], r);
 #pragma unroll
         for (int t = 0; t < 3; ++t) tmem_st_rows(lanes + ((16u * y) << 16) + 64 * t + 16 * b, r[t]);
@@ -434,7 +443,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (have(b, y, i)) *reinterpret_cast<uint64_t *>(dst + at(b, y, i)) = whole(r, i);
+            if (have(b, y, i)) *reinterpret_cast<uint64_t *>(dst + at(b, y, i)) = f2mul(f2pk(kUp, kUp), whole(r, i));
         }
       }
     }
@@ -444,7 +453,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
     const int z = 32 * quad_warp + lane;            // this thread's value channel (TMEM lane)
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad_warp) << 16);
     const bool live = z < ps.dz;
-    uint64_t M[32];                                 // x channels x_of(i) and the next
+    uint64_t M[32];                                 // times 2^-72: x channels x_of(i) and the next
     auto block = [&](int j) { return 2 * j + group; };              // the j-th of this group's blocks
     auto x_of = [&](int i) { return 32 * block(i >> 4) + 2 * (i & 15); };
     {
@@ -458,6 +467,9 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
         const bool in = src && live && x_of(i) < ps.dx;
         M[i] = f2pk(in ? src[x_of(i) * ps.dz + z] : 0.f, in ? src[(x_of(i) + 1) * ps.dz + z] : 0.f);
       }
+      __syncwarp();                                 // (all loads are in flight)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) M[i] = f2mul(f2pk(kDown, kDown), M[i]);
     }
     // a block of M as the next chunk's operand
     auto put_state = [&](int j) {
@@ -519,7 +531,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           float a, b;
-          f2up(M[i], a, b);
+          f2up(f2mul(f2pk(kUp, kUp), M[i]), a, b);
           if (x_of(i) >= ps.dx) break;
           dst[x_of(i) * ps.dz + z] = a;
           dst[(x_of(i) + 1) * ps.dz + z] = b;
@@ -574,16 +586,16 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
           const long long sum = scan_pairs(x0, x1);
           const long long all = __shfl_sync(0xffffffffu, sum, 31);
           const long long mid = __shfl_sync(0xffffffffu, sum, 15);      // up to token 31
-          const long long lim = 100ll << 32;
-          const int mode = all >= -lim ? kWhole : mid >= -lim && all - mid >= -lim ? kBlocks : kPairs;
+          const long long lim = 100ll << 32, shift = (long long)kShift << 32;
+          const int mode = all >= -shift ? kWhole : mid >= -lim && all - mid >= -lim ? kBlocks : kPairs;
           // where a block's factors start from: forwards its first token's past, backwards its end
-          const long long ref = mode == kWhole ? (rev ? all : 0) : (lane < 16) == rev ? mid : rev ? all : 0;
+          const long long ref = mode == kWhole ? (rev ? all + shift : -shift) : (lane < 16) == rev ? mid : rev ? all : 0;
           float *gt = gates(st);
           float2 rf, tf, cb, rb, cr;
           auto one = [&](long long G, int i, float &r, float &t, float &c, float &b, float &x) {
-            const float since = exp2_fixed(G), until = exp2_fixed(all - G);
-            r = rev ? until : since;
-            t = i < len ? (rev ? since : until) : 0.f;
+            const long long row = rev ? all - G : G, tok = rev ? G : all - G;
+            r = exp2_fixed(row + shift);
+            t = i < len ? exp2_fixed(tok - shift) : 0.f;
             if (KIND == kStates) return;
             c = exp2_fixed(rev ? G - ref : ref - G);
             if (mode == kWhole) return;

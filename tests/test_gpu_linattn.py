@@ -462,3 +462,19 @@ def test_many_heads(cuda_lib, dtype):
     ro, rS = ref.fwd(**{n: x if n == "S0" else x[:, :1] for n, x in t.items()})
     assert_close(f64(o), ro[:, 0].numpy(), TOL[dtype], "o", bf16_out=dtype == BF)
     assert_close(f64(S), rS.numpy(), TOL[F32], "S")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("decay", [-0.85, -1.05, -1.5, -3.0])
+@pytest.mark.parametrize("log2", [20, -12])
+def test_large_and_small_values_with_fast_decays(cuda_lib, log2, decay, dtype):
+    """Values of a million and of a four-thousandth where a chunk of 64 tokens loses 2^-78 to 2^-277: no
+    factor on the way may leave fp32's range while the results (2^60 and 2^-36) are far inside it."""
+    t, (dO, dS) = make(2, 150, 2, 2, 1, 2, 64, 128, dtype, seed=log2 + 50)
+    f = 2.0 ** log2
+    for n in ("q", "k", "v"):
+        t[n] = t[n] * f
+    t["S0"] = t["S0"] * f * f
+    t["g"] = torch.full_like(t["g"], decay)
+    check_fwd(cuda_lib, t)
+    check_bwd(cuda_lib, t, dO * f, dS * f * f)
