@@ -215,8 +215,9 @@ int ckda_decode_step(const void *q, const void *k, const void *v, const void *a,
  *
  *   q : [B, T, Hq, dk]   k : [B, T, Hk, dk]   v : [B, T, Hv, dv]   io_dtype
  *            Hq, Hk, Hv divide H: head h reads head h * Hx / H of a tensor with Hx heads.
- *   g : log decays, float32, g <= 0 (-inf forgets everything before; a value above 0 or a NaN
- *            gives undefined values in its own sequence and head, but no fault):
+ *   g : log decays, float32, g <= 0 (-inf forgets everything before; a value above 0 gives
+ *            undefined values in its own sequence and head, but no fault; a NaN makes all NaN that
+ *            it reaches in its sequence and head, and the rest of its chunk of 64 tokens):
  *            [B, T, H] with decay = CKDA_DECAY_PER_TOKEN, [H] with CKDA_DECAY_PER_HEAD
  *   o : [B, T, H, dv] io_dtype (NULL: not written)
  *   S0, S_T : [N, H, dk, dv] float32, as in ckda_chunk_fwd (S_T may alias S0; an empty

@@ -91,6 +91,7 @@ void launch_fixed(const float *part, float *dg, long rows, int H, const int *sta
 // fp32 sum of a few thousand would lose 2^-12 of it), and 2^x splits into its integer word and
 // its fraction word for nothing.  2^x below -200 is 0 in fp32, so clamping there changes no
 // result, keeps -inf (a reset) finite and bounds a chunk's sum by 12,800.
+// (A NaN has no fixed-point form: its chunk's factors are set to NaN, chunk_is_nan.)
 __device__ __forceinline__ long long fixed_log2(float g) {
   return __double2ll_rn((double)fmaxf(g, -140.f) * 6196328018.8645515);   // log2(e) 2^32
 }
@@ -101,6 +102,10 @@ __device__ __forceinline__ float exp2_fixed(long long x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__uint2float_rn((uint32_t)x) * 2.3283064365386963e-10f));
   return n < -126 ? 0.f : r * __int_as_float((min(n, 126) + 127) << 23);
+}
+// Whether a log decay of the warp's tokens, two per lane, is NaN
+__device__ __forceinline__ bool chunk_is_nan(float g0, float g1) {
+  return __any_sync(0xffffffffu, isnan(g0) || isnan(g1)) != 0;
 }
 // Sums over the warp's tokens, two per lane (x0, x1): returns the sum up to and with the second.
 __device__ __forceinline__ long long scan_pairs(long long x0, long long x1) {

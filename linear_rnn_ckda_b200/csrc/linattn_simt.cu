@@ -60,20 +60,23 @@ __device__ void chunk_gates(float2 *sG, float *sE, float *sW, const float *g, lo
   const int lane = threadIdx.x;
   if (lane >= 32) return;
   long long x[2];
+  float gl[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int i = 2 * lane + u;
-    x[u] = i < len ? fixed_log2(g[g_fixed ? (size_t)h : (size_t)(row0 + i) * H + h]) : 0;
+    gl[u] = i < len ? g[g_fixed ? (size_t)h : (size_t)(row0 + i) * H + h] : 0.f;
+    x[u] = fixed_log2(gl[u]);
   }
+  const bool bad = chunk_is_nan(gl[0], gl[1]);
   const long long sum = scan_pairs(x[0], x[1]);
   const long long all = __shfl_sync(0xffffffffu, sum, 31);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int i = 2 * lane + u;
     const long long G = u ? sum : sum - x[1];
-    sG[i] = split_sum(G);
-    sE[i] = exp2_fixed(G);
-    sW[i] = i < len ? exp2_fixed(all - G) : 0.f;
+    sG[i] = bad ? make_float2(nanf(""), 0.f) : split_sum(G);
+    sE[i] = bad ? nanf("") : exp2_fixed(G);
+    sW[i] = i >= len ? 0.f : bad ? nanf("") : exp2_fixed(all - G);
   }
 }
 

@@ -604,6 +604,8 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
           };
           one(sum - x1, 2 * lane, rf.x, tf.x, cb.x, rb.x, cr.x);
           one(sum, 2 * lane + 1, rf.y, tf.y, cb.y, rb.y, cr.y);
+          const bool bad = chunk_is_nan(g0, g1);
+          if (bad) rf.x = rf.y = tf.x = tf.y = cb.x = cb.y = rb.x = rb.y = cr.x = cr.y = nanf("");
           reinterpret_cast<float2 *>(gt + 64)[lane] = tf;
           if (KIND != kStates) {
             reinterpret_cast<float2 *>(gt)[lane] = rf;
@@ -615,7 +617,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
             }
           }
           if (lane == 0) {
-            gt[448] = exp2_fixed(all);
+            gt[448] = bad ? nanf("") : exp2_fixed(all);
             gt[449] = (float)mode;
             *reinterpret_cast<long long *>(gt + 450) = all;
           }

@@ -478,3 +478,36 @@ def test_large_and_small_values_with_fast_decays(cuda_lib, log2, decay, dtype):
     t["g"] = torch.full_like(t["g"], decay)
     check_fwd(cuda_lib, t)
     check_bwd(cuda_lib, t, dO * f, dS * f * f)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("fixed", [False, True])
+@pytest.mark.parametrize("T", [60, 200, 1500])
+def test_nan_decay_shows(cuda_lib, T, fixed, dtype):
+    """A NaN log decay makes NaN of everything it reaches (as in a decode step), in its own head and
+    sequence only; chunks of 64 tokens before it (after it for dk and dv) keep their bits."""
+    t, (dO, dS) = make(2, T, 3, 3, 3, 3, 64, 64, dtype, fixed=fixed, seed=T)
+    at = T // 2
+    d, dO, dS = cuda(t), dO.cuda(), dS.cuda()
+    run = lambda: (*cuda_lib.linattn_fwd(**d), *cuda_lib.linattn_bwd(**d, dO=dO, dS_T=dS))  # noqa: E731
+    clean = run()
+    d["g"] = d["g"].clone()
+    d["g"][(1,) if fixed else (0, at, 1)] = math.nan
+    got = run()
+    lo, hi = (0, T) if fixed else (at // 64 * 64, min(T, at // 64 * 64 + 64))
+    for n, x, y in zip(("o", "S_T", "dq", "dk", "dv", "dg", "dS0"), got, clean):
+        if n == "dg" and fixed:
+            assert bool(torch.isnan(x[1])) and torch.equal(x[[0, 2]], y[[0, 2]])
+            continue
+        heads = (lambda z: z) if n in ("S_T", "dS0") else (lambda z: z.transpose(1, 2))  # noqa: E731
+        x, y = heads(x), heads(y)                    # [B, H, ..]
+        assert torch.equal(x[:, [0, 2]], y[:, [0, 2]]), n
+        bad, ok = x[0, 1], y[0, 1]
+        if not fixed:
+            assert torch.equal(x[1, 1], y[1, 1]), n
+        if n in ("S_T", "dS0", "dg"):
+            assert bool(torch.isnan(bad).all()), n
+        elif n in ("o", "dq"):
+            assert bool(torch.isnan(bad[0 if fixed else at:]).all()) and torch.equal(bad[:lo], ok[:lo]), n
+        else:
+            assert bool(torch.isnan(bad[:T if fixed else at]).all()) and torch.equal(bad[hi:], ok[hi:]), n
