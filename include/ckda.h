@@ -245,7 +245,9 @@ size_t ckda_linattn_fwd_workspace_size(int B, int T, int H, int dk, int dv, int 
  *   dq, dk_out, dv_out : shaped and typed as q, k, v (all required); a shared head's gradient
  *            is the sum over the heads that read it, summed in fp32 and rounded once
  *   dg : shaped as g, float32 (required); with CKDA_DECAY_PER_HEAD the sum over all tokens.
- *            A decay of -inf has gradient 0.
+ *            A decay that leaves nothing of the state (e^g below 2^-126, as -inf) has gradient 0.
+ *            The accuracy of dg is absolute, of the size of the q . dq that are summed into it: a
+ *            strongly decaying token's small gradient is not resolved next to its neighbours'.
  *   dS0 : [N, H, dk, dv] float32, NULL = not written; may alias dS_T
  * Sums are taken in a fixed order: the same inputs give the same bits.
  * Returns CKDA_OK or a negative CKDA_ERR_* code.

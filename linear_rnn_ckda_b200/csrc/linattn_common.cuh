@@ -70,10 +70,12 @@ size_t tc_workspace(bool packed, int N, int B, int T, int H, int Hq, int Hk, int
                     bool g_fixed, bool back);
 int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s);
 // dg from the row dots rho = q . dq and kappa = k . dk, each [slices, H, rows] (slices summed in
-// order), and the states after every piece and their gradients (linattn_simt.cu).
+// order), and the states around every piece and their gradients (linattn_simt.cu).
 struct DecayParams {
-  const float *S, *X;       // [slots, H, elems]: incoming states (and each sequence's end), gradients
-  const float *rho, *kappa;
+  const float *S, *X;       // [slots, H, elems]: incoming states and each sequence's end; the gradients
+                            // of the states after the pieces and (with S0) of each sequence's S0
+  const float *rho, *kappa, *g;
+  int g_fixed, has_S0;
   float *dg;                // [rows, H]
   int H, elems, slices;
   long rows;

@@ -202,8 +202,7 @@ __global__ void __launch_bounds__(kThreads) lin_local_kernel(const LocalParams p
 
 // ---------------------------------------------------------------- walk over the chunks
 // blockIdx: (sequence, head, direction x block of 4 x 128 entries); replaces each chunk's own state
-// by the state before it (direction 1: after it).  keep: the forward end state also goes to the
-// spare slot.
+// by the state before it (direction 1: after it).  keep: the end states also go to the spare slots.
 struct ScanParams {
   float *own[2];
   const float *init[2];
@@ -245,7 +244,7 @@ __global__ void __launch_bounds__(128) lin_scan_kernel(const ScanParams p) {
       S.z = fmaf(a[u], S.z, d[u].z); S.w = fmaf(a[u], S.w, d[u].w);
     }
   }
-  if (!back && p.keep) *reinterpret_cast<float4 *>(own + ((size_t)(base + nc) * p.H + h) * p.elems + e) = S;
+  if (p.keep) *reinterpret_cast<float4 *>(own + ((size_t)(base + nc) * p.H + h) * p.elems + e) = S;
   if (end) *reinterpret_cast<float4 *>(end + ((size_t)n * p.H + h) * p.elems + e) = S;
 }
 
@@ -380,51 +379,102 @@ __global__ void __launch_bounds__(kThreads) lin_pass_kernel(const PassParams p) 
 }
 
 // ---------------------------------------------------------------- decay gradients
-// dg_t = <S_out, X> + sum_{s >= t} (q_s . dq_s - k_s . dk_s) over a segment, S_out the state
-// after it and X its gradient.  One block per (segment or chunk, head).
+// dg_t = e^{g_t} <S_{t-1}, R_t> = <S_out, X> + sum_{s >= t} (q_s . dq_s - k_s . dk_s) over a piece (a
+// segment or chunk), S_out the state after it and X its gradient.  At the piece's first token that is
+// <S_in, gradient of S_in>, which is known by itself: 0 for a sequence without S0, else the value that
+// ends the piece before.  The sums of a long piece miss it by their rounding errors, and the difference
+// is spread over the tokens by the size of what was summed (tied at both ends, a random walk keeps
+// 1 / sqrt 3 of its error, and a common factor on all terms goes).  A token that keeps nothing of
+// the state (e^{g_t} = 0) has no gradient.  One block per (piece, head).
 __global__ void __launch_bounds__(256) lin_decay_kernel(const DecayParams p) {
-  __shared__ double s_sum[8];
+  __shared__ double s_all[4][8], s_sum[8], s_abs[8];
   Piece u;
   if (!find_piece(p.slots, blockIdx.x, u)) return;
   const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const float4 *S = reinterpret_cast<const float4 *>(p.S + ((size_t)(blockIdx.x + 1) * p.H + h) * p.elems);
-  const float4 *X = reinterpret_cast<const float4 *>(p.X + ((size_t)blockIdx.x * p.H + h) * p.elems);
-  float part = 0.f;
-  for (int e = tid; e < p.elems / 4; e += 256) {
-    const float4 a = S[e], b = X[e];
-    part = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, part))));
-  }
-  double dot = part;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-  if (lane == 0) s_sum[warp] = dot;
-  __syncthreads();
-  double run = 0.0;                              // <S_out, X> plus the blocks after this one
-#pragma unroll
-  for (int w = 0; w < 8; ++w) run += s_sum[w];
   const size_t row = (size_t)h * p.rows + u.row0, all_rows = (size_t)p.H * p.rows;
+  auto term = [&](int i, double &x, double &size) {
+    x = size = 0.0;
+    for (int y = 0; i >= 0 && y < p.slices; ++y) {
+      const float a = p.rho[y * all_rows + row + i], b = p.kappa[y * all_rows + row + i];
+      x += (double)a - (double)b;
+      size += (double)(fabsf(a) + fabsf(b));
+    }
+  };
+  double t[4] = {0.0, 0.0, 0.0, 0.0};            // <S_out, X>, the same before the piece; sum, sum of sizes
+  {
+    const long slot = blockIdx.x;
+    const bool first = u.piece == 0, tie = !first || p.has_S0;
+    auto state = [&](const float *x, long s) { return reinterpret_cast<const float4 *>(x + ((size_t)s * p.H + h) * p.elems); };
+    const float4 *S1 = state(p.S, slot + 1), *X1 = state(p.X, slot);
+    const float4 *S0 = state(p.S, slot), *X0 = tie ? state(p.X, first ? slot + u.pieces : slot - 1) : X1;
+#pragma unroll 4
+    for (int e = tid; e < p.elems / 4; e += 256) {
+      const float4 a = S1[e], b = X1[e], c = S0[e], d = X0[e];
+      t[0] += (double)fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, a.w * b.w)));
+      t[1] += (double)fmaf(c.x, d.x, fmaf(c.y, d.y, fmaf(c.z, d.z, c.w * d.w)));
+    }
+    if (!tie) t[1] = 0.0;
+  }
+  for (int i = tid; i < u.len; i += 256) {
+    double x, size;
+    term(i, x, size);
+    t[2] += x;
+    t[3] += size;
+  }
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) t[y] += __shfl_xor_sync(0xffffffffu, t[y], off);
+    if (lane == 0) s_all[y][warp] = t[y];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    t[y] = 0.0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t[y] += s_all[y][w];
+  }
+  double run = t[0], runs = 0.0;                 // <S_out, X>; with what has been summed, and its size
+  const double start = t[1], share = (start - (run + t[2])) / t[3];
+  const bool tied = isfinite(share);             // (not where there is nothing to spread over, or no number)
   // 256 tokens at a time from the end; thread 0 takes the last of them
   for (int top = u.len; top > 0; top -= 256) {
     const int i = top - 1 - tid;
-    double x = 0.0;
-    for (int y = 0; i >= 0 && y < p.slices; ++y)
-      x += (double)p.rho[y * all_rows + row + i] - (double)p.kappa[y * all_rows + row + i];
+    double x, size;
+    term(i, x, size);
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, x, off);
-      if (lane >= off) x += y;
+      const double y = __shfl_up_sync(0xffffffffu, x, off), z = __shfl_up_sync(0xffffffffu, size, off);
+      if (lane >= off) {
+        x += y;
+        size += z;
+      }
     }
     __syncthreads();
-    if (lane == 31) s_sum[warp] = x;
+    if (lane == 31) {
+      s_sum[warp] = x;
+      s_abs[warp] = size;
+    }
     __syncthreads();
-    double before = 0.0, all = 0.0;
+    double before = 0.0, befores = 0.0, all = 0.0, alls = 0.0;
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
-      if (w < warp) before += s_sum[w];
+      if (w < warp) {
+        before += s_sum[w];
+        befores += s_abs[w];
+      }
       all += s_sum[w];
+      alls += s_abs[w];
     }
-    if (i >= 0) p.dg[(size_t)(u.row0 + i) * p.H + h] = (float)(run + before + x);
+    if (i >= 0) {
+      const size_t at = (size_t)(u.row0 + i) * p.H + h;
+      double d = run + before + x;
+      if (tied) d = i == 0 ? start : d + share * (runs + befores + size);
+      const float g = p.g[p.g_fixed ? (size_t)h : at];
+      p.dg[at] = !isnan(g) && exp2_fixed(fixed_log2(g)) == 0.f ? 0.f : (float)d;
+    }
     run += all;
+    runs += alls;
   }
 }
 
@@ -555,7 +605,7 @@ int run_cols(const LinArgs &a, const LinBwdArgs *b, const SimtLayout &L, cudaStr
   p.slices = (most + 16 * NJ - 1) / (16 * NJ);
   lin_pass_kernel<NJ><<<dim3(slots, H, (unsigned)(3 * p.slices)), kThreads, smem, s>>>(p);
   DecayParams d = {};
-  d.S = S; d.X = X; d.rho = rho; d.kappa = kappa; d.slices = (a.dk + 16 * NJ - 1) / (16 * NJ);
+  d.S = S; d.X = X; d.rho = rho; d.kappa = kappa; d.g = a.g; d.g_fixed = a.g_fixed; d.has_S0 = a.S0 != nullptr; d.slices = (a.dk + 16 * NJ - 1) / (16 * NJ);
   d.dg = a.g_fixed ? reinterpret_cast<float *>(a.ws + L.dg) : b->dg;
   d.H = a.H; d.elems = elems; d.rows = rows; d.slots = sl;
   launch_decay(d, L.slots, s);

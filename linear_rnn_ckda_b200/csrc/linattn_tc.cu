@@ -213,7 +213,7 @@ struct Pass {
   const float *seg_in;            // [slots, H, dk, dv] incoming states, or NULL
   float *end;                     // [N, H, dk, dv]: the last segment's end state, or NULL
   float *end_slot;                // [slots, H, ..]: end state of every segment (kStates), or of the
-                                  // last to the slot after it (kGrad), or NULL
+                                  // last to the sequence's spare slot (kGrad; kOut for dv), or NULL
   float *decay;                   // kStates: [slots, H] the segment's whole decay
   void *out;                      // [rows, H, dz]
   int part;                       // out is fp32 per-head shares of a shared head's gradient
@@ -540,7 +540,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
       if (KIND == kStates) store(ps.end_slot + ((size_t)blockIdx.x * p.H + h) * p.elems);
       else if (last_seg) {
         if (ps.end) store(ps.end + ((size_t)u.n * p.H + h) * p.elems);
-        if (ps.end_slot) store(ps.end_slot + ((size_t)(blockIdx.x + 1) * p.H + h) * p.elems);
+        if (ps.end_slot) store(ps.end_slot + ((size_t)(blockIdx.x - u.piece + u.pieces) * p.H + h) * p.elems);
       }
     }
   } else {
@@ -1258,14 +1258,14 @@ int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
   pv = pk;
   pv.ix = 1; pv.iy = 0; pv.iz = 3;
   pv.hx = a.Hk; pv.hy = a.Hq; pv.hz = a.H; pv.dx = a.dk; pv.dz = a.dv;
-  pv.end = b->dS0;
+  pv.end = b->dS0; pv.end_slot = a.S0 ? segX : nullptr;
   pv.part = part_v; pv.out = part_v ? a.ws + l.pv : static_cast<uint8_t *>(b->dv);
   pv.dots = nullptr;
   for (int i = 0; i < 3; ++i)      // (a shared head's gradient goes through fp32 sums instead)
     if (!p.pass[i].part && !make_map(&p.outs[i], p.pass[i].out, a.H, rows, p.pass[i].dz, true)) return CKDA_ERR_CUDA;
   if (!launch<kGrad>(p, dim3(slots, H, 3), s)) return CKDA_ERR_CUDA;
   DecayParams d = {};
-  d.S = segS; d.X = segX; d.rho = rho; d.kappa = kappa; d.slices = 1;
+  d.S = segS; d.X = segX; d.rho = rho; d.kappa = kappa; d.g = a.g; d.g_fixed = a.g_fixed; d.has_S0 = a.S0 != nullptr; d.slices = 1;
   d.dg = a.g_fixed ? reinterpret_cast<float *>(a.ws + l.dg) : b->dg;
   d.H = a.H; d.elems = p.elems; d.rows = rows; d.slots = p.slots;
   launch_decay(d, l.slots, s);

@@ -511,3 +511,35 @@ def test_nan_decay_shows(cuda_lib, T, fixed, dtype):
             assert bool(torch.isnan(bad[0 if fixed else at:]).all()) and torch.equal(bad[:lo], ok[:lo]), n
         else:
             assert bool(torch.isnan(bad[:T if fixed else at]).all()) and torch.equal(bad[hi:], ok[hi:]), n
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_decay_gradients_where_nothing_is_left(cuda_lib, dtype):
+    """A token whose decay leaves nothing of the state has gradient 0 itself, and so has a sequence's
+    first token without S0; the others of each head keep their accuracy on the head's own scale."""
+    t, (dO, _) = make(2, 700, 3, 3, 3, 3, 64, 64, dtype, state=False, seed=61)
+    g = t["g"]
+    g[0, 10::37, 1] = -math.inf
+    g[0, 100:110, 2] = -1e30
+    g[1, 20::50, 0] = -88.0
+    got = cuda_lib.linattn_bwd(**cuda(t), dO=dO.cuda())[3].double().cpu()
+    want = ref.bwd(**t, dO=dO)[3].detach()
+    assert bool((got[g < -87.4] == 0).all()) and bool((got[:, 0] == 0).all())
+    for h in range(3):
+        assert float((got[:, :, h] - want[:, :, h]).norm() / want[:, :, h].norm()) <= TOL_DG, h
+
+
+def test_decay_gradients_of_one_long_segment(cuda_lib):
+    """bf16, so many sequences that each stays whole.  Each of the 12 additions at full size that make
+    up an element of dq truncates by up to 2^-23, 2^-23 / sqrt 12 in the mean square, and q . dq sums
+    independent elements: 2^-23 of q . dq, sqrt 2 of that with k . dk.  A sum of n such errors, tied at both
+    ends, is sqrt(n / 6) of one in the mean square over its tokens (tied at one end sqrt(n / 2))."""
+    n = 6000
+    t, (dO, _) = make(4, n, 40, 40, 40, 40, 128, 128, BF, state=False, seed=71)
+    d, dO = cuda(t), dO.cuda()
+    got = cuda_lib.linattn_bwd(**d, dO=dO, want_dS0=False)
+    want = decay_gradient(d["q"], d["k"], d["v"], d["g"], dO)
+    rho = float((got[0].float() * d["q"].float()).sum(-1).pow(2).mean().sqrt())
+    size = float(want.pow(2).mean().sqrt())
+    tol = math.sqrt(2 * n / 6) * 2.0 ** -23 * rho / size + 5e-7
+    assert float((got[3].double() - want).pow(2).mean().sqrt()) / size <= tol
