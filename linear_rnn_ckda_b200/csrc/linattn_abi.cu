@@ -31,8 +31,8 @@ int check_sizes(long long B, long long T, int H, int Hq, int Hk, int Hv, int dk,
     return CKDA_ERR_DIM;
   if (!valid_io(io_dtype) || (decay != CKDA_DECAY_PER_TOKEN && decay != CKDA_DECAY_PER_HEAD))
     return CKDA_ERR_DTYPE;
-  // token rows are 32-bit coordinates; row x head counts stay far below 2^63
-  if (B * T > INT32_MAX || B * T * H > (1LL << 41)) return CKDA_ERR_DIM;
+  // token rows are 32-bit coordinates, whole chunks of 64 too; row x head counts stay far below 2^63
+  if (B * T > INT32_MAX - 63 || B * T * H > (1LL << 41)) return CKDA_ERR_DIM;
   return CKDA_OK;
 }
 int check_seqs(const void *cu, int n_seqs, int B, int T) {

@@ -10,6 +10,9 @@ namespace lin {
 
 constexpr int kC = 64;    // tokens per chunk
 
+// Pieces of L tokens that len tokens take (their sum may pass 32 bits)
+__host__ __device__ __forceinline__ int pieces_of(int len, int L) { return (int)(((long)len + L - 1) / L); }
+
 // Pieces of `L` tokens of every sequence (chunks, or segments of several chunks) are numbered in
 // one array, `spare` further slots after each sequence's.  Packed: sequence n starts at
 // cu[n] / L + n (1 + spare), which leaves room for its ceil(len / L) pieces before the next;
@@ -20,11 +23,11 @@ struct Slots {
   const int *status;      // non-zero: bad offsets, nothing runs
   int N, T, L, spare;
   __host__ __device__ __forceinline__ long base(int n) const {
-    return cu ? (long)cu[n] / L + (long)n * (1 + spare) : (long)n * ((T + L - 1) / L + spare);
+    return cu ? (long)cu[n] / L + (long)n * (1 + spare) : (long)n * (pieces_of(T, L) + spare);
   }
 };
 inline long slot_count(bool packed, int N, int T, int L, int spare) {
-  return packed ? (long)T / L + (long)N * (1 + spare) + 1 : (long)N * ((T + L - 1) / L + spare);
+  return packed ? (long)T / L + (long)N * (1 + spare) + 1 : (long)N * (pieces_of(T, L) + spare);
 }
 
 // One slot's tokens: rows [row0, row0 + len) of the token axis, piece `piece` of `pieces`.
@@ -43,12 +46,12 @@ __device__ __forceinline__ bool find_piece(const Slots &s, long slot, Piece &p) 
     first = s.cu[p.n];
     total = s.cu[p.n + 1] - (int)first;
   } else {
-    p.n = (int)(slot / ((s.T + s.L - 1) / s.L + s.spare));
+    p.n = (int)(slot / (pieces_of(s.T, s.L) + s.spare));
     first = (long)p.n * s.T;
     total = s.T;
   }
   p.piece = (int)(slot - s.base(p.n));
-  p.pieces = (total + s.L - 1) / s.L;
+  p.pieces = pieces_of(total, s.L);
   if (p.piece >= p.pieces) return false;
   p.row0 = first + (long)p.piece * s.L;
   p.len = min(s.L, total - p.piece * s.L);

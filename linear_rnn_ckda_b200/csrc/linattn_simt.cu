@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(128) lin_scan_kernel(const ScanParams p) {
   const float *const init = back ? p.init[1] : p.init[0];
   float *const end = back ? p.end[1] : p.end[0];
   const int len = p.slots.cu ? p.slots.cu[n + 1] - p.slots.cu[n] : p.slots.T;
-  const int nc = (len + kC - 1) / kC;
+  const int nc = pieces_of(len, kC);
   const long base = p.slots.base(n);
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
   if (init) S = *reinterpret_cast<const float4 *>(init + ((size_t)n * p.H + h) * p.elems + e);
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t *cu, int N, in
     const Slots s{cu, nullptr, nullptr, N, T, t.L, t.spare};
     for (int n = threadIdx.x; n < N; n += 1024) {
       const long b = s.base(n), next = n + 1 < N ? s.base(n + 1) : t.count;
-      const int pieces = (cu[n + 1] - cu[n] + t.L - 1) / t.L;
+      const int pieces = pieces_of(cu[n + 1] - cu[n], t.L);
       for (long i = b; i < next; ++i) t.table[i] = i - b < pieces ? n : -1;
     }
   }

@@ -259,7 +259,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
   // a segment whose own state nothing reads: the last in the direction of the walk
   const bool last_seg = rev ? u.piece == 0 : u.piece == u.pieces - 1;
   if (KIND == kStates && last_seg) return;
-  const int nc = (u.len + kC - 1) / kC;
+  const int nc = pieces_of(u.len, kC);
 
   // Warps by role (the scores' off-diagonal block lies in the TMEM lanes of a quarter that goes
   // with the direction: 17 forwards, 16 backwards; the other of the two takes part in tokf Z)
@@ -1049,7 +1049,7 @@ __global__ void __launch_bounds__(128) lin_join_kernel(const JoinParams p) {
   const int e = ((blockIdx.z % p.blocks) * 128 + threadIdx.x) * 4;
   if (e >= p.elems) return;
   const int len = p.slots.cu ? p.slots.cu[n + 1] - p.slots.cu[n] : p.slots.T;
-  const int m = (len + p.slots.L - 1) / p.slots.L;
+  const int m = pieces_of(len, p.slots.L);
   const long base = p.slots.base(n);
   const size_t own = ((size_t)n * p.H + h) * p.elems + e;
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);

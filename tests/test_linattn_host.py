@@ -280,3 +280,15 @@ int main() {{
     subprocess.run(["g++", "-std=c++17", "-I", cuda, str(tmp_path / "h.cc"), "-o", str(tmp_path / "h")], check=True)
     r = subprocess.run([str(tmp_path / "h")], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+def test_longest_sequences(lib):
+    """Up to 2^31 - 64 tokens: their segments are counted in 64 bits (the sum of a length and a segment's
+    passes 32), so the workspace grows with the call; one token more is refused."""
+    w, most = lib.ckda_linattn_fwd_workspace_size, 2**31 - 64
+    for io in (0, 1):
+        for n_seqs in (0, 1):
+            half, full = w(1, 2**30, 1, 16, 16, io, n_seqs), w(1, most, 1, 16, 16, io, n_seqs)
+            assert half <= full <= 2 * half + (1 << 20), (io, n_seqs, half, full)
+    assert w(1, most, 1, 16, 16, 0, 0) >= (2**31 // 64) * 16 * 16 * 4
+    assert fwd_call(lib, T=most + 1) == -2 and fwd_call(lib, T=most, nbytes=255) == -7
