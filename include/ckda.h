@@ -278,8 +278,9 @@ int ckda_linattn_decode_step(const void *q, const void *k, const void *v, const 
  *   scale * (x_a cos t - x_b sin t,  x_b cos t + x_a sin t)       (inverse: t -> -t)
  * for the 2 * n_freqs first channels (CKDA_ROTARY_HALF: a = i, b = i + n_freqs;
  * CKDA_ROTARY_INTERLEAVED: a = 2 i, b = 2 i + 1); the other channels are copied.  The inverse
- * with the same scale is the gradient.  The angle is formed exactly modulo one turn, at any
- * position.
+ * with the same scale is the gradient.  The angle is formed modulo one turn in 64-bit fixed point: it is
+ * off by at most 2^-63 of a turn per position (frequencies below 2^90), and by fp32's rounding of the
+ * fraction of a turn.
  *   q, q_out : [n_tokens, Hq, d]   k, k_out : [n_tokens, Hk, d] io_dtype (Hk = 0: q alone);
  *            an output may be its input, else no two of them overlap; element-aligned
  *            (16-byte aligned tensors with n_freqs and d in whole 16-byte vectors run faster)

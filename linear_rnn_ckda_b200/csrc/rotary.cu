@@ -7,10 +7,10 @@
 // the gradient.
 //
 // The angle is needed modulo one turn.  Each frequency is held as a 64-bit fixed-point
-// fraction of a turn, F = f / (2 pi) * 2^64 modulo 2^64, and pos * F in wrapping 64-bit integer
-// arithmetic is the angle's fraction of a turn: nothing is lost to the size of the position
-// (an fp32 product is a tenth of a radian off at a million tokens), and no range reduction
-// follows.  One fp32 rounding of the fraction costs 2^-25 of half a turn.
+// fraction of a turn, F = f / (2 pi) * 2^64 modulo 2^64, to two units (the product is taken in four
+// fp64 parts), and pos * F in wrapping 64-bit integer arithmetic is the angle's fraction of a turn, off
+// by at most 2^-63 of a turn per position (an fp32 product is a tenth of a radian off at a million
+// tokens); no range reduction follows.  One fp32 rounding of the fraction costs 2^-25 of half a turn.
 //
 // Bound: HBM, q and k read and written once.  A warp takes a token (or some of its heads, when
 // tokens are few): its first loads are in flight while it fills a table of the token's cos and
@@ -96,10 +96,12 @@ __global__ void __launch_bounds__(kRotThreads, kRotBlocks<T>) rotary_kernel(cons
   constexpr bool kTwo = !INTER || V == 1;                        // an item has a second vector
   constexpr int kE = INTER && V > 1 ? V / 2 : V;                 // table entries of an item
   for (int i = threadIdx.x; i < p.nf; i += kRotThreads) {
-    const double turns = p.freqs[i] * 0.15915494309189533577;   // 1 / (2 pi)
-    const double frac = (turns - floor(turns)) * 4294967296.0;
-    const double hi = floor(frac);
-    freq[i] = ((uint64_t)hi << 32) + (uint64_t)((frac - hi) * 4294967296.0);
+    // f / (2 pi) with 1 / (2 pi) as a sum of three doubles: products and their rounding errors, whose
+    // fractions of a turn, [-1/2, 1/2], become integers (their sum wraps as turns do)
+    constexpr double kInv0 = 0x1.45f306dc9c883p-3, kInv1 = -0x1.6b01ec5417056p-57, kInv2 = -0x1.6447e493ad4cep-111;
+    const double f = p.freqs[i], x = f * kInv0, y = f * kInv1;
+    auto units = [](double t) { return (uint64_t)__double2ll_rn((t - rint(t)) * 18446744073709551616.0); };
+    freq[i] = units(x) + units(fma(f, kInv0, -x)) + units(y) + units(fma(f, kInv1, -y) + f * kInv2);
   }
   __syncthreads();
   const int rows = p.iph <= 32 ? 32 / p.iph : 1;                 // heads a warp takes at once

@@ -99,3 +99,27 @@ def test_many_tokens(cuda_lib, dtype):
             close(y[lo:lo + 200], ref.rotary(x[lo:lo + 200], pos[lo:lo + 200], f.cpu(), "interleaved"), dtype)
     back, _ = cuda_lib.rotary(a.float(), None, pos, f, layout="interleaved", inverse=True)
     assert float((back - q.float()).abs().max()) < (1e-5 if dtype == F32 else 2.0 ** -7 * float(q.float().abs().max()) * 1.5)
+
+
+def test_angles_at_any_position(cuda_lib):
+    """fp32, positions up to 2^44 and frequencies of many turns, none and negative ones: the angle is off
+    by 2^-63 of a turn per position, 2 pi 2^-63 |pos| radians, and by fp32's rounding of its fraction of a
+    turn and of the results (the 1e-6 of the other tests, of values up to 4)."""
+    from fractions import Fraction
+    import math
+
+    f = torch.tensor([1.0, 0.37, 1e-3, 2.5, -0.7, 1e-9, 1000.1, 3e15], dtype=torch.float64)
+    pos = torch.tensor([1, 999_999, -2**31, 2**33 + 7, -2**40 - 1, 2**42 + 3, 2**44 - 5], dtype=torch.int64)
+    q = rnd(len(pos), 1, 16, seed=13, dtype=F32).clamp(-4, 4)
+    got, _ = cuda_lib.rotary(q.cuda(), None, pos.cuda(), f.cuda())
+    # 2 pi to 60 digits
+    turn = Fraction(6283185307179586476925286766559005768394338798750211641949889, 10**60)
+    for t, p in enumerate(pos.tolist()):
+        for i, fi in enumerate(f.tolist()):
+            x = Fraction(fi) * p
+            a = float(x - turn * (x // turn))
+            c, s = math.cos(a), math.sin(a)
+            u, w = q[t, 0, i].double(), q[t, 0, i + 8].double()
+            tol = 4.0 * (1e-6 + abs(p) * 2.0 * math.pi * 2.0 ** -63)
+            assert abs(float(got[t, 0, i]) - float(u * c - w * s)) <= tol, (p, fi)
+            assert abs(float(got[t, 0, i + 8]) - float(w * c + u * s)) <= tol, (p, fi)
