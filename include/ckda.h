@@ -348,7 +348,9 @@ int ckda_workspace_status(const void *workspace, int *status, void *stream);
  * by `wait_ns` nanoseconds (0 = the normal 2 s bound).  The wait runs out, the
  * unit abandons its work (outputs of that unit are left unwritten or partial),
  * lets every copy and product it started finish, releases its tensor memory
- * and records CKDA_ERR_TIMEOUT in the status word.  chunk_index < 0 switches
+ * and records CKDA_ERR_TIMEOUT in the status word.  The bf16 kernels of
+ * linear attention do the same at chunk `chunk_index` of each segment of a
+ * sequence, whose results are then undefined.  chunk_index < 0 switches
  * the hook off (the default).  Process-wide; takes effect at the next launch.
  */
 void ckda_debug_wait_injection(int chunk_index, unsigned long long wait_ns);

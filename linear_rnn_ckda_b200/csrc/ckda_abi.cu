@@ -12,6 +12,7 @@
 
 #include "../../include/ckda.h"
 #include "internal.h"
+#include "linattn.h"
 
 namespace {
 
@@ -55,6 +56,11 @@ ckda::SegChoice seg_choice_for_lengths(const int32_t *lengths, int n, int H, int
 }  // namespace
 
 namespace ckda {
+
+int wait_injection(uint64_t *wait_ns) {
+  *wait_ns = g_inject_wait_ns.load(std::memory_order_relaxed);
+  return g_inject_chunk.load(std::memory_order_relaxed);
+}
 
 // sm_100 check for the current device, cached per device (atomics: host threads may call the
 // library concurrently; the cached value is the same whoever writes it).

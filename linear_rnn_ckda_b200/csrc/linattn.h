@@ -21,6 +21,8 @@ __host__ __device__ inline int head_of(int h, int H, int Hx) { return h / (H / H
 
 // CKDA_OK when the current device is sm_100, else the CKDA_ERR_* code a call returns.
 int check_device();
+// ckda_debug_wait_injection's settings: the chunk (-1: off) and the bound of its wait (0: the usual one).
+int wait_injection(uint64_t *wait_ns);
 
 struct LinArgs {
   const void *q, *k, *v;      // [rows, Hq, dk], [rows, Hk, dk], [rows, Hv, dv]

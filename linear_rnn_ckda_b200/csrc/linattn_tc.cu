@@ -194,7 +194,7 @@ struct Cfg {
   static constexpr uint32_t kGate = 7 * 64 * 4 + 16;                          // one stage's decays
   static constexpr uint32_t offDot = offGate + kStages * kGate;               // kGrad: 2 x 4 x 64 floats
   static constexpr uint32_t offBar = offDot + (KIND == kGrad ? 512 * 4 : 0);
-  static constexpr int kBars = 3 * kStages + 2 * kTokBufs + (KIND == kStates ? 21 : 25);
+  static constexpr int kBars = 3 * kStages + 2 * kTokBufs + (KIND == kStates ? 22 : 26);
   static constexpr uint32_t kSmem = offBar + kBars * 8 + 64 + 1024;           // + slack to align
   // TMEM columns: scores, M, O twice, D (twice where there is room)
   static constexpr int kDBufs = KIND == kStates ? 2 : 1;
@@ -228,11 +228,14 @@ struct Params {
   long rows;
   Slots slots;
   int *status;
+  int inject_chunk;               // test hook: chunk of a segment whose loads wait for nothing (-1: off)
+  uint64_t inject_wait_ns;        // that wait's bound
 };
 
-// Waits are bounded by a count of tries, each of which the hardware lets sleep for a while: some
-// seconds, after which every role ends and the status word says so.
-constexpr uint32_t kTries = 2000000;
+// Waits are bounded by a count of tries, 110 ns each as measured, so 2 s in all, after which every role
+// ends and the status word says so.  (Reading the clock in every wait instead is so much more code that
+// calls take 5 to 8 % longer.)
+constexpr uint32_t kTries = 20000000;
 constexpr uint64_t kDrainNs = 2000000000ull;
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
   uint32_t n = 0;
@@ -275,7 +278,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
   uint64_t *bx = b_wfree + C::kTokBufs;
   uint64_t *b_zeroed = bx, *b_sc = bx + 1, *b_p = bx + 2, *b_s = bx + 21 /* 4, kOut and kGrad */, *b_o = bx + 4 /* 2 */,
            *b_ofree = bx + 6 /* 2 */, *b_d = bx + 8 /* 2 */, *b_dfree = bx + 16 /* 2 */, *b_drain = bx + 10 /* 2 */,
-           *b_red = bx + 12 /* 2 */, *b_o1 = bx + 14;
+           *b_red = bx + 12 /* 2 */, *b_o1 = bx + 14, *b_never = bx + (KIND == kStates ? 21 : 25);
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bx + 18);
   volatile int *s_abort = reinterpret_cast<volatile int *>(bx + 19);
   volatile int *s_issued = reinterpret_cast<volatile int *>(bx + 20);
@@ -296,6 +299,7 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
     mbar_init(b_p, 3);
     for (int s = 0; s < (KIND == kStates ? 0 : 4); ++s) mbar_init(b_s + s, 4);
     mbar_init(b_o1, 1);
+    mbar_init(b_never, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(b_o + s, 1);
       mbar_init(b_d + s, 1);
@@ -567,6 +571,8 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
         }
         if (c >= C::kStages && (turn || warp == 14) && !(ok = wait(b_empty + st, ph ^ 1u))) break;
         if (warp == 14) {
+          // test hook: a wait that runs out (ckda_debug_wait_injection)
+          if (c == p.inject_chunk && !(ok = mbar_wait(b_never, 0, p.inject_wait_ns))) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(b_full + st, bytes);
             *s_issued = c + 1;
@@ -1200,6 +1206,8 @@ int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
   }
   p.g = a.g; p.H = a.H; p.g_fixed = a.g_fixed; p.elems = a.dk * a.dv; p.rows = rows;
   p.status = a.status;
+  p.inject_chunk = wait_injection(&p.inject_wait_ns);
+  if (p.inject_wait_ns == 0) p.inject_wait_ns = kDrainNs;
   p.slots = Slots{a.cu, reinterpret_cast<const int *>(a.ws + l.table), a.status, a.N, a.T, l.L, b ? 1 : 0};
   if (a.cu) {
     const PlanTable t{reinterpret_cast<int *>(a.ws + l.table), l.L, b ? 1 : 0, l.slots};

@@ -543,3 +543,38 @@ def test_decay_gradients_of_one_long_segment(cuda_lib):
     size = float(want.pow(2).mean().sqrt())
     tol = math.sqrt(2 * n / 6) * 2.0 ** -23 * rho / size + 5e-7
     assert float((got[3].double() - want).pow(2).mean().sqrt()) / size <= tol
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("chunk", [0, 2])
+def test_a_wait_that_runs_out(cuda_lib, chunk, packed):
+    """A role that waits for nothing (test hook, 0.2 ms): every unit that reaches that chunk ends, the
+    status word says so, and the next calls in the same workspace give the bits they gave before."""
+    # (forty heads and more than that in sequences of 500 tokens: their segments have three chunks and more)
+    B, T, lens = (1, 2000, [700, 0, 30, 1270]) if packed else (4, 500, None)
+    N = len(lens) if packed else B
+    t, (dO, dS) = make(B, T, 40, 40, 20, 40, 64, 128, BF, N=N, seed=81)
+    d, dO, dS = cuda(t), dO.cuda(), dS.cuda()
+    cu = offsets(lens).cuda() if packed else None
+    n = max(cuda_lib.linattn_bwd_workspace_size(B, T, 40, 40, 20, 40, 64, 128, 0, BF, N if packed else 0),
+            cuda_lib.linattn_fwd_workspace_size(B, T, 40, 64, 128, BF, N if packed else 0))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def fwd():
+        return cuda_lib.linattn_fwd(**d, cu_seqlens=cu, workspace=ws)
+
+    def bwd():
+        return cuda_lib.linattn_bwd(**d, cu_seqlens=cu, dO=dO, dS_T=dS, workspace=ws)
+
+    for call in (fwd, bwd):
+        want = call()
+        assert cuda_lib.workspace_status(ws) == 0
+        try:
+            cuda_lib.debug_wait_injection(chunk, 200_000)
+            call()
+            assert cuda_lib.workspace_status(ws) == -8      # CKDA_ERR_TIMEOUT
+        finally:
+            cuda_lib.debug_wait_injection(-1, 0)
+        again = call()
+        assert cuda_lib.workspace_status(ws) == 0
+        assert all(torch.equal(x, y) for x, y in zip(want, again))
