@@ -559,7 +559,7 @@ def rotary_freqs(dim: int, base: float = 10000.0, scaling: Optional[str] = None,
         keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
         f = f / factor * (1.0 - keep) + f * keep
         scale = 0.1 * math.log(factor) + 1.0
-    return f.to(device or "cuda"), scale
+    return f.to("cuda" if device is None else device), scale
 
 
 def rotary(q, k, pos, freqs, layout: str = "half", inverse: bool = False, scale: float = 1.0,

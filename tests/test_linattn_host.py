@@ -292,3 +292,12 @@ def test_longest_sequences(lib):
             assert half <= full <= 2 * half + (1 << 20), (io, n_seqs, half, full)
     assert w(1, most, 1, 16, 16, 0, 0) >= (2**31 // 64) * 16 * 16 * 4
     assert fwd_call(lib, T=most + 1) == -2 and fwd_call(lib, T=most, nbytes=255) == -7
+
+
+def test_rotary_freqs_on_the_first_device(monkeypatch):
+    """device=0 is a device (and not the current one, whichever that is)."""
+    asked = []
+    monkeypatch.setattr(torch.Tensor, "to", lambda self, dev: asked.append(dev) or self)
+    for dev in (0, 1, "cpu", None):
+        ops.rotary_freqs(8, device=dev)
+    assert asked == [0, 1, "cpu", "cuda"]
