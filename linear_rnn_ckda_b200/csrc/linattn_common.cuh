@@ -58,15 +58,14 @@ __device__ __forceinline__ bool find_piece(const Slots &s, long slot, Piece &p) 
   return true;
 }
 
-// Checks a packed batch's offsets (status word) and writes the slot tables of the one or two
-// slot numberings a call uses.  Host side in linattn_abi.cu.
+// Checks a packed batch's offsets (status word) and writes the table, of `count` slots, of the slot
+// numbering that a call uses (linattn_simt.cu).
 struct PlanTable {
   int *table;
   int L, spare;
   long count;
 };
-int launch_plan(const int32_t *cu, int N, int T, const PlanTable *tables, int n_tables, int *status,
-                cudaStream_t s);
+int launch_plan(const int32_t *cu, int N, int T, const PlanTable &t, int *status, cudaStream_t s);
 
 // The tensor-core path (linattn_tc.cu): bf16 inputs.
 size_t tc_workspace(bool packed, int N, int B, int T, int H, int Hq, int Hk, int Hv, int dk, int dv,
@@ -91,11 +90,11 @@ void launch_share(const void *part, void *out, long rows, int H, int Hx, int d, 
                   const int *status, cudaStream_t s);
 void launch_fixed(const float *part, float *dg, long rows, int H, const int *status, cudaStream_t s);
 
-// Log decays in base 2 as 64-bit fixed point, 32 bits of fraction: sums and differences are exact,
-// so the weight between two tokens keeps fp32 accuracy however large the sums before them are (an
+// Log decays in base 2 as 64-bit fixed point, 32 bits of fraction: each is rounded by 2^-33 at most,
+// sums and differences of them are exact, so the weight between two tokens keeps fp32 accuracy however large the sums before them are (an
 // fp32 sum of a few thousand would lose 2^-12 of it), and 2^x splits into its integer word and
 // its fraction word for nothing.  2^x below -200 is 0 in fp32, so clamping there changes no
-// result, keeps -inf (a reset) finite and bounds a chunk's sum by 12,800.
+// result, keeps -inf (a reset) finite and bounds a chunk's sum by 12,927 (64 x 140 log2 e).
 // (A NaN has no fixed-point form: its chunk's factors are set to NaN, chunk_is_nan.)
 __device__ __forceinline__ long long fixed_log2(float g) {
   return __double2ll_rn((double)fmaxf(g, -140.f) * 6196328018.8645515);   // log2(e) 2^32

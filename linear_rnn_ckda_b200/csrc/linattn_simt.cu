@@ -558,7 +558,7 @@ int run_cols(const LinArgs &a, const LinBwdArgs *b, const SimtLayout &L, cudaStr
   auto f32 = [](const void *p) { return static_cast<const float *>(p); };
   if (a.cu) {
     const PlanTable t{reinterpret_cast<int *>(a.ws + L.table), kC, 1, L.slots};
-    const int rc = launch_plan(a.cu, a.N, a.T, &t, 1, a.status, s);
+    const int rc = launch_plan(a.cu, a.N, a.T, t, a.status, s);
     if (rc != CKDA_OK) return rc;
   }
   if (!L.single) {
@@ -621,8 +621,7 @@ int run_simt(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------- packed batches
-__global__ void __launch_bounds__(1024) plan_kernel(const int32_t *cu, int N, int T, PlanTable t0,
-                                                    PlanTable t1, int *status) {
+__global__ void __launch_bounds__(1024) plan_kernel(const int32_t *cu, int N, int T, PlanTable t, int *status) {
   bool bad = false;
   for (int n = threadIdx.x; n < N; n += 1024) {
     const int s = cu[n], e = cu[n + 1];
@@ -631,15 +630,11 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t *cu, int N, in
   const bool any = __syncthreads_or(bad);
   if (threadIdx.x == 0) *status = any ? CKDA_ERR_SEQLENS : CKDA_OK;
   if (any) return;
-  for (int x = 0; x < 2; ++x) {
-    const PlanTable t = x ? t1 : t0;
-    if (!t.table) continue;
-    const Slots s{cu, nullptr, nullptr, N, T, t.L, t.spare};
-    for (int n = threadIdx.x; n < N; n += 1024) {
-      const long b = s.base(n), next = n + 1 < N ? s.base(n + 1) : t.count;
-      const int pieces = pieces_of(cu[n + 1] - cu[n], t.L);
-      for (long i = b; i < next; ++i) t.table[i] = i - b < pieces ? n : -1;
-    }
+  const Slots s{cu, nullptr, nullptr, N, T, t.L, t.spare};
+  for (int n = threadIdx.x; n < N; n += 1024) {
+    const long b = s.base(n), next = n + 1 < N ? s.base(n + 1) : t.count;
+    const int pieces = pieces_of(cu[n + 1] - cu[n], t.L);
+    for (long i = b; i < next; ++i) t.table[i] = i - b < pieces ? n : -1;
   }
 }
 
@@ -663,11 +658,8 @@ void launch_fixed(const float *part, float *dg, long rows, int H, const int *sta
   lin_fixed_kernel<<<H, 256, 0, s>>>(part, dg, rows, H, status);
 }
 
-int launch_plan(const int32_t *cu, int N, int T, const PlanTable *tables, int n_tables, int *status,
-                cudaStream_t s) {
-  PlanTable none{nullptr, 1, 0, 0};
-  plan_kernel<<<1, 1024, 0, s>>>(cu, N, T, n_tables > 0 ? tables[0] : none,
-                                 n_tables > 1 ? tables[1] : none, status);
+int launch_plan(const int32_t *cu, int N, int T, const PlanTable &t, int *status, cudaStream_t s) {
+  plan_kernel<<<1, 1024, 0, s>>>(cu, N, T, t, status);
   return cudaGetLastError() == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
 }
 

@@ -165,6 +165,8 @@ constexpr int kThreads = 896;
 // M is held times 2^-kShift; a chunk's weights have one reference while it decays by 2^-kShift at most
 constexpr int kShift = 72;
 constexpr float kUp = 4722366482869645213696.f, kDown = 1.f / kUp;
+// (a reset is held as 2^-201.9, and its row factor, times 2^kShift, has to be 0: below 2^-126)
+static_assert(kShift <= 75, "resets");
 constexpr uint32_t kPanel = 8192;                  // 64 tokens x 64 channels of bf16, 128-byte swizzle
 constexpr uint32_t kTileB = 2 * kPanel;            // 64 tokens x 128 channels
 // The causal side of P in 32 x 32 blocks of 64-byte rows (64-byte swizzle): the two blocks that share
@@ -1211,7 +1213,7 @@ int launch_tc(const LinArgs &a, const LinBwdArgs *b, cudaStream_t s) {
   p.slots = Slots{a.cu, reinterpret_cast<const int *>(a.ws + l.table), a.status, a.N, a.T, l.L, b ? 1 : 0};
   if (a.cu) {
     const PlanTable t{reinterpret_cast<int *>(a.ws + l.table), l.L, b ? 1 : 0, l.slots};
-    const int rc = launch_plan(a.cu, a.N, a.T, &t, 1, a.status, s);
+    const int rc = launch_plan(a.cu, a.N, a.T, t, a.status, s);
     if (rc != CKDA_OK) return rc;
   }
   float *segS = reinterpret_cast<float *>(a.ws + l.S), *segX = reinterpret_cast<float *>(a.ws + l.X);
