@@ -6,7 +6,7 @@
 // l / 4 + 8 m, so a load covers 8 rows x 64 contiguous bytes and o's sum over rows is in-thread
 // sums and three shuffles.  Warps share nothing, so the block's warp count is free: few heads
 // are spread one warp per block over the SMs, many take eight.  Measured: B256 H32 128 x 128, 1,082
-// MB, 177 to 185 us (89 to 94 % of the copy rate); B1 H16 13 us, of which the host's call is most.
+// MB, 177 to 188 us (88 to 93 % of the copy rate); B1 H16 13 us, of which the host's call is most.
 #include "common.cuh"
 #include "linattn.h"
 

@@ -17,7 +17,7 @@
 //
 // Bound: fp32 FMA and shared-memory loads; few chunks are split over columns of the output, which
 // repeats the scores, so that a small call occupies more SMs.  Measured: B2 T37 H3 64 x 64 forward
-// 22 us (one launch), B2 T515 H4 32 x 64 gradients 51 us (five).
+// 22 us (one launch), B2 T515 H4 32 x 64 gradients 52 us (five).
 #include "linattn_common.cuh"
 
 namespace ckda {

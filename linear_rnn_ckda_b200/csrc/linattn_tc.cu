@@ -24,11 +24,12 @@
 // the form by blocks: B8 T8192 H16 with one such head 444 us, with 72 411.)  A chunk that decays faster
 // takes its weights block by block, and one that decays faster still pair by pair; then the second
 // part has its own accumulator.
+//
 // M is held in fp32: in registers, or (dq and dk, whose operand M is wanted in three terms, which
 // are an fp32 value's 24 bits) as those terms in tensor memory.  tokf Z is split into three terms, so
 // M carries fp32 accuracy over any length.  M and P go into o and dv in two terms, 2^-18 of a value
-// off: what is left is the rounding of the output (1.66e-3; in one term each 2.35e-3), for 9 to 17 % of
-// the forward's time.  Where row dots are wanted (decay gradients, which cancel) M and P go into O in
+// off: what is left is the rounding of the output (1.66e-3; in one term each 2.35e-3, and 172 us were
+// 156, 395 us 336).  Where row dots are wanted (decay gradients, which cancel) M and P go into O in
 // three terms (two leave dg 2.7e-5 off).
 // The tensor cores truncate the accumulator at every addition (dq came out 4.4e-7 too small), so
 // terms are added from the lowest up, and the many additions of lower terms truncate a small sum
@@ -36,18 +37,17 @@
 // gradients' time.  (D's lower terms of both halves of a chunk first, as the gradients take them, cost
 // the forward 10 %: there each half is added by itself.)
 //
-// One CTA per (segment, head), 28 warps: 0-3 and 24-27 state (112 registers a thread where they hold M), 4-11
-// outputs, 12, 13 and one of 16, 17 scores (a 32 x 32 block each), 14 TMA loads and decays, 15
+// One CTA per (segment, head), 28 warps: 0-3 and 24-27 state (112 registers a thread where they hold
+// M), 4-11 outputs, 12, 13 and one of 16, 17 scores (a 32 x 32 block each), 14 TMA loads and decays, 15
 // issue of O, 23 issue of scores and D (two issuers: one thread's products take 50 cycles or
 // more each to issue), the rest tokf Z.  The roles run the chunks at their own pace through
-// mbarriers.  Spills and unrolled loops cost more than they save: 28 warps share 28 KB of L1, and
-// waiting for code was 42 % of all stalls when the roles were fully unrolled.
+// mbarriers.  Unrolled loops cost more than they save: the warps share what is left of L1, and waiting
+// for code is the second largest stall.  (Four state warps, each with twice the code: 178, 434 and
+// 550 us where eight take 169, 395 and 521.)
 //
-// Measured (B200): B4 T4096 H16 128 x 128 forward 157 us, B8 T8192 H16 285 us (1090 MB, 3.8 TB/s,
-// near 1000 W), gradients of the first 490 us.  Bound by the latency of a chunk's chain (TMA ->
-// tokf Z -> D -> M -> O -> rows: 4,100 cycles a chunk of 64 tokens, 6,700 for dq and dk), not by
-// bytes or tensor cycles: leaving out the stores, two of three loads, or any one role's work
-// changes the first by at most 8 %, the second by 21 %.
+// Measured (B200): B4 T4096 H16 128 x 128 forward 172 us, B8 T8192 H16 395 to 420 us (1090 MB, 2.7 TB/s),
+// gradients of the first 535 us.  Bound by the latency of a chunk's chain (TMA -> tokf Z -> D -> M -> O ->
+// rows), not by bytes or tensor cycles: DRAM 26 %, tensor pipe 29 % of the time.
 //
 // A sequence may be cut into segments: a first launch computes every segment's own state, an
 // elementwise walk over a sequence's segments gives each its incoming state (the decay is a
@@ -358,9 +358,9 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
   if (KIND == kGrad && is_state) {
     // ---------------------------------------------------------------- state (warps 0-3, 24-27)
     // M is its operand: three bf16 terms hold an fp32 value's 24 bits, and O1 wants them anyway.
-    // So M lives in tensor memory only, and a chunk's M <- e^{G_C} M + D is one short loop: held in
-    // registers as in the other kinds, the unrolled splitting alone was 11 KB of code a chunk, for
-    // which the warps waited more than they computed (put 5,300 cycles of 8,000 a chunk).
+    // So M lives in tensor memory only, and a chunk's M <- e^{G_C} M + D is one short loop (held in
+    // registers as in the other kinds, the unrolled splitting into three terms kept the warps waiting for
+    // code).
     const uint32_t quarter = tmem + ((uint32_t)(32 * quad_warp) << 16), lanes = quarter + C::cM;
     auto split = [&](const uint64_t (&m)[8], uint32_t (&r)[3][8]) {
 #pragma unroll
@@ -376,8 +376,8 @@ __device__ __forceinline__ void lin_tc(const Params &p) {
       return f2add(f2add(unpack_bf16(r[0][i]), unpack_bf16(r[1][i])), unpack_bf16(r[2][i]));
     };
     // Stored states are rows of x channels: a warp reads and writes 8 of them (32-byte pieces) at a
-    // time, in the layout that puts a row into a lane (a lane's own row, 4 bytes or 16 at a time,
-    // took 20,000 cycles in and 34,000 out).
+    // time, in the layout that puts a row into a lane (B4 T4096 H16 582 -> 515 us against a lane's own
+    // row, 4 or 16 bytes at a time).
     const size_t state = ((size_t)blockIdx.x * p.H + h) * p.elems;
     const int z0 = 32 * quad_warp + (lane >> 2), x0 = 2 * (lane & 3);
     auto at = [&](int b, int y, int i) {             // where word i of 16 lanes and channels 32 b .. is stored
@@ -1123,8 +1123,9 @@ constexpr int kSMs = 148;
 // ones, 0.6 a chunk for the first launch (B1 T4096 H32: 16 chunks 311 us, 64 463; B2 T2048 H16:
 // 8 chunks 190, 32 253).  Packed: lengths are on the device, so a segment is half an SM's share of
 // all chunks (backwards a quarter), between 8 and 64 chunks, a multiple of 4 so that even lengths
-// are cut evenly (13 sequences, 40,000 tokens, H16 forward: 32 chunks 416 us, 16 433, 34 436, 64
-// 445; 10 sequences, 9,000 tokens, H16 backward: 12 chunks 390 us, 24 422).
+// are cut evenly (14 sequences, 42,992 tokens, H16 forward: 32 chunks 416 us, 16 433, 34 436, 64
+// 445; 11 sequences, 7,923 tokens, H16 backward: 12 chunks 390 us, 24 422).  (Taken when o and dv had one
+// term of M and P each; all are some 10 % more since.)
 int segment_tokens(bool packed, int B, int T, int H, bool back) {
   const long nch = ((long)T + kC - 1) / kC;
   const long units1 = (long)B * H * (back ? 3 : 1), local1 = (long)B * H * (back ? 2 : 1);
